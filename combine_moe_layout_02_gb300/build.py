@@ -27,7 +27,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = ["api.cu", "layout.cu", "notify.cu", "dispatch.cu", "combine.cu", "layout_static.cu", "pad.cu", "expert.cu", "fused.cu", "run.cu", "exchange.cu"]
+SOURCES = ["api.cu", "layout.cu", "notify.cu", "dispatch.cu", "combine.cu", "layout_static.cu", "pad.cu", "expert.cu", "fused.cu", "run.cu", "exchange.cu",
+           "combine_grad.cu", "fp4.cu", "product.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"match_hist": ["-DMOE_LAYOUT_MATCH_HIST"], "profile": ["-DMOE_PROFILE"]}
 
@@ -65,7 +66,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     host = platform.machine()
     if not os.path.exists(stamp) or open(stamp).read().strip() != host:
         force = True
-    headers = [os.path.join(INCLUDE, "moe.h"), os.path.join(CSRC, "moe_device.cuh")]
+    headers = [os.path.join(INCLUDE, "moe.h"), os.path.join(CSRC, "moe_device.cuh"), os.path.join(CSRC, "fp4.cuh")]
     cc = nvcc()
     jobs = []
     objs = []

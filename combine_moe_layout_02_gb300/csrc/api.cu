@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "moe.h"
+#include "fp4.cuh"
 #include "moe_device.cuh"
 
 namespace moe {
@@ -513,6 +514,163 @@ moe_status moe_combine_expert(const moe_shape* shape, const void* y, int64_t y_r
     a.err = err;
     a.slot_row = slot_row;
     return from_cuda(launch_combine_expert(s, a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+moe_status combine_grad_args(const moe_shape* shape, const uint16_t* dout, const void* y, int64_t y_row_stride,
+                             const int64_t* base, int64_t arena_rows, const int32_t* routes, int64_t routes_n,
+                             const int32_t* topk_idx, const float* topk_weights, void* dy, int64_t dy_row_stride,
+                             float* dw, int32_t* err, CombineGradArgs* a) {
+    const moe_shape& s = *shape;
+    const int64_t S = s.S, row = 2 * static_cast<int64_t>(s.H);
+    if (arena_rows < 0 || (!dy && !dw && S > 0)) return MOE_ERR_INVALID_ARG;
+    if (dw && (y_row_stride < row || y_row_stride % 16 != 0)) return MOE_ERR_INVALID_ARG;
+    if (dy && (dy_row_stride < row || dy_row_stride % 16 != 0)) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(dout, S * s.H, 16) || !ok_ptr(y, dw ? arena_rows : 0, 16) || !ok_ptr(base, 1, 16) ||
+        !ok_ptr(routes, routes_n, 16) || !ok_ptr(topk_idx, S * s.K, 16) || !ok_opt(topk_weights, 16) ||
+        !ok_opt(dy, 16) || !ok_opt(dw, 16) || !ok_opt(err, 4))
+        return MOE_ERR_INVALID_ARG;
+    a->P = s.P;
+    a->E = s.E;
+    a->K = s.K;
+    a->H = s.H;
+    a->epr = s.E / s.P;
+    a->S = S;
+    a->dout = dout;
+    a->y = static_cast<const uint8_t*>(y);
+    a->y_stride = y_row_stride;
+    a->part_row_base = base;
+    a->arena_rows = arena_rows;
+    a->topk_idx = topk_idx;
+    a->topk_weights = topk_weights;
+    a->dy = static_cast<uint8_t*>(dy);
+    a->dy_stride = dy_row_stride;
+    a->dw = dw;
+    a->err = err;
+    return MOE_OK;
+}
+
+// Arguments of packing and unpacking alike.
+moe_status fp4_rows_args(int32_t groups, int64_t rows, int32_t width, int32_t gated, const void* x, int64_t x_row_stride,
+                         const void* q, const void* sf, int32_t E, const int32_t* plan, int64_t plan_ints) {
+    if (groups < 0 || rows < 0 || width < 1 || width % 32 != 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+    if (width > MOE_FP4_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    if (rows > (int64_t{1} << 40) || (groups > 0 && rows > (int64_t{1} << 40) / groups)) return MOE_ERR_UNSUPPORTED;
+    if (gated && rows % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (x_row_stride < 2 * static_cast<int64_t>(width) || x_row_stride % 16 != 0) return MOE_ERR_INVALID_ARG;
+    const int64_t n = groups * rows;
+    if (!ok_ptr(x, n, 16) || !ok_ptr(q, n, 16) || !ok_ptr(sf, n, 16)) return MOE_ERR_INVALID_ARG;
+    if (plan) {
+        if (groups != 1 || gated || rows % kFp4Tile != 0 || E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
+        if (!aligned(plan, 16) || plan_ints < plan_tiles_at(E)) return MOE_ERR_INVALID_ARG;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_combine_grad(const moe_shape* shape, const uint16_t* dout, const void* y, int64_t y_row_stride,
+                            const int64_t* part_row_base, int64_t arena_rows, const int32_t* send_head,
+                            const int32_t* topk_idx, const float* topk_weights, void* dy, int64_t dy_row_stride,
+                            float* dw, int32_t* err, void* stream) {
+    moe_status st = moe_check_shape(shape);
+    if (st != MOE_OK) return st;
+    CombineGradArgs a{};
+    st = combine_grad_args(shape, dout, y, y_row_stride, part_row_base, arena_rows, send_head,
+                           static_cast<int64_t>(shape->S) * shape->P, topk_idx, topk_weights, dy, dy_row_stride, dw, err, &a);
+    if (st != MOE_OK) return st;
+    a.send_head = send_head;
+    return from_cuda(launch_combine_grad(*shape, a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_combine_expert_grad(const moe_shape* shape, const uint16_t* dout, const void* y, int64_t y_row_stride,
+                                   const int64_t* expert_part_base, int64_t arena_rows, const int32_t* slot_row,
+                                   const int32_t* topk_idx, const float* topk_weights, void* dy,
+                                   int64_t dy_row_stride, float* dw, int32_t* err, void* stream) {
+    moe_status st = moe_check_shape(shape);
+    if (st != MOE_OK) return st;
+    CombineGradArgs a{};
+    st = combine_grad_args(shape, dout, y, y_row_stride, expert_part_base, arena_rows, slot_row,
+                           static_cast<int64_t>(shape->S) * shape->K, topk_idx, topk_weights, dy, dy_row_stride, dw, err, &a);
+    if (st != MOE_OK) return st;
+    a.slot_row = slot_row;
+    return from_cuda(launch_combine_expert_grad(*shape, a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_fp4_scale_bytes(int64_t rows, int32_t width) {
+    if (rows < 0 || width < 1 || width % 32 != 0) return -1;
+    return ceil_div(rows, kFp4Tile) * ceil_div(width, kFp4Chunk) * kFp4ChunkBytes;
+}
+
+moe_status moe_fp4_pack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint16_t* x,
+                        int64_t x_row_stride, uint8_t* q, uint8_t* sf, int32_t E, const int32_t* plan,
+                        int64_t plan_ints, void* stream) {
+    const moe_status st = fp4_rows_args(groups, rows, width, gated, x, x_row_stride, q, sf, E, plan, plan_ints);
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_fp4_pack(false, groups, rows, width, gated, const_cast<uint16_t*>(x), x_row_stride, q, sf,
+                                     plan, E, plan_ints, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_fp4_unpack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint8_t* q,
+                          const uint8_t* sf, uint16_t* x, int64_t x_row_stride, int32_t E, const int32_t* plan,
+                          int64_t plan_ints, void* stream) {
+    const moe_status st = fp4_rows_args(groups, rows, width, gated, x, x_row_stride, q, sf, E, plan, plan_ints);
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_fp4_pack(true, groups, rows, width, gated, x, x_row_stride, const_cast<uint8_t*>(q),
+                                     const_cast<uint8_t*>(sf), plan, E, plan_ints, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_expert_plan_ints(const moe_shape* s) {
+    if (moe_check_shape(s) != MOE_OK || s->expert_alignment % kFp4Tile != 0) return -1;
+    // every expert's last tile may be short
+    return plan_tiles_at(s->E) + 4 * (s->E + static_cast<int64_t>(s->S) * s->K / kPlanTileRows);
+}
+
+moe_status moe_expert_plan(const moe_shape* shape, const int32_t* num_tokens_per_expert, int32_t* plan,
+                           int64_t plan_ints, int32_t* err, void* stream) {
+    moe_status st = moe_check_shape(shape);
+    if (st != MOE_OK) return st;
+    const int64_t need = moe_expert_plan_ints(shape);
+    if (need < 0 || plan_ints < need) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(num_tokens_per_expert, 1, 16) || !ok_ptr(plan, 1, 16) || !ok_opt(err, 4)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_expert_plan(*shape, num_tokens_per_expert, plan, plan_ints, err,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dispatch_expert_fp4(const moe_shape* shape, const uint16_t* x, const int32_t* topk_idx,
+                                   const float* topk_weights, const int32_t* slot_row,
+                                   const int64_t* expert_part_base, uint8_t* q, uint8_t* sf, int64_t arena_rows,
+                                   int32_t* recv_src_idx, float* recv_weight, int32_t* err, void* stream) {
+    moe_status st = moe_check_shape(shape);
+    if (st != MOE_OK) return st;
+    const moe_shape& s = *shape;
+    const int64_t S = s.S;
+    if (arena_rows < 0 || s.H % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(x, S * s.H, 16) || !ok_ptr(topk_idx, S * s.K, 16) || !ok_ptr(slot_row, S * s.K, 16) ||
+        !ok_ptr(expert_part_base, 1, 16) || !ok_ptr(q, arena_rows, 16) || !ok_ptr(sf, arena_rows, 16) ||
+        !ok_opt(recv_src_idx, 16) || !ok_opt(recv_weight, 16) || !ok_opt(topk_weights, 16) || !ok_opt(err, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_dispatch_fp4(s, x, topk_idx, topk_weights, slot_row, expert_part_base, q, sf, arena_rows,
+                                         recv_src_idx, recv_weight, err, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_expert_product_fp4(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq,
+                                  const uint8_t* wsf, const uint8_t* xq, const uint8_t* xsf, int64_t arena_rows,
+                                  const int32_t* plan, int64_t plan_ints, uint16_t* y, int64_t y_row_stride,
+                                  int32_t* err, void* stream) {
+    if (E < 1 || N < 1 || K < 1 || N % 32 != 0 || K % 32 != 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || N > 2 * MOE_FP4_MAX_WIDTH || K > MOE_FP4_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    if (arena_rows < 0 || arena_rows % kFp4Tile != 0) return MOE_ERR_INVALID_ARG;
+    if (arena_rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (y_row_stride < (gated ? N : 2 * static_cast<int64_t>(N)) || y_row_stride % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(wq, 1, 16) || !ok_ptr(wsf, 1, 16) || !ok_ptr(xq, arena_rows, 16) || !ok_ptr(xsf, arena_rows, 16) ||
+        !ok_ptr(y, arena_rows, 16) || !ok_ptr(plan, 1, 16) || !ok_opt(err, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (plan_ints < plan_tiles_at(E)) return MOE_ERR_INVALID_ARG;
+    if (arena_rows == 0) return MOE_OK;
+    return from_cuda(launch_product(E, N, K, gated, wq, wsf, xq, xsf, arena_rows, plan, plan_ints, y, y_row_stride, err,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 #ifdef MOE_PROFILE

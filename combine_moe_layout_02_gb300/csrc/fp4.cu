@@ -1,0 +1,451 @@
+// fp4.cu -- MXFP4 rows: packing and unpacking (moe_fp4_pack, moe_fp4_unpack),
+// the experts' row tiles (moe_expert_plan) and the expert-major dispatch that
+// packs on the way (moe_dispatch_expert_fp4). Format and layout: fp4.cuh.
+#include <cuda_bf16.h>
+
+#include "fp4.cuh"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Packing and unpacking. The unit of work is one scale chunk: 128 rows x 128
+// elements, one CTA of 256 threads. Eight threads share a row's 128 elements
+// (16 each, half a block), and a thread takes rows r, r + 32, r + 64 and
+// r + 96, whose scale words are the 16 bytes at r * 16 of the chunk.
+
+constexpr int kPackThreads = 256;
+
+struct PackArgs {
+    int64_t rows;        // rows per group (plain mode) or of the arena (plan mode)
+    int32_t groups, width, gated;
+    uint16_t* x;         // read by pack, written by unpack
+    int64_t x_stride;    // bytes
+    uint8_t* q;
+    uint8_t* sf;
+    const int32_t* plan;  // NULL: every row
+    int32_t E, tile_cap;
+};
+
+// The rows of a unit: `n` of them from packed row `row0` of group `group`.
+struct PackTile {
+    int64_t group, row0;
+    int32_t n;
+};
+
+__device__ __forceinline__ PackTile pack_tile(const PackArgs& a, int64_t t, int64_t tiles_per_group) {
+    PackTile o;
+    if (a.plan == nullptr) {
+        o.group = t / tiles_per_group;
+        o.row0 = (t - o.group * tiles_per_group) * kFp4Tile;
+        const int64_t left = a.rows - o.row0;
+        o.n = static_cast<int32_t>(left < kFp4Tile ? left : kFp4Tile);
+        return o;
+    }
+    const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t / 2);
+    const int half = static_cast<int>(t & 1) * kFp4Tile;
+    o.group = 0;
+    o.row0 = static_cast<int64_t>(p.y) + half;
+    o.n = p.z - half;
+    o.n = o.n < 0 ? 0 : (o.n > kFp4Tile ? kFp4Tile : o.n);
+    // a plan that does not belong to this arena names no row of it
+    if (p.y < 0 || p.y % kFp4Tile != 0 || o.row0 + o.n > a.rows) o.n = 0;
+    return o;
+}
+
+__device__ __forceinline__ int64_t pack_units(const PackArgs& a, int64_t tiles_per_group, int64_t chunks) {
+    if (a.plan == nullptr) return a.groups * tiles_per_group * chunks;
+    int32_t n = __ldg(a.plan);
+    n = n < 0 ? 0 : (n > a.tile_cap ? a.tile_cap : n);
+    return 2 * static_cast<int64_t>(n) * chunks;
+}
+
+template <bool UNPACK>
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
+    pdl_wait_then_release();
+    const int tid = threadIdx.x;
+    const int r = tid >> 3, part = tid & 7;  // row of each quarter, 16-element part of its 128 elements
+    const int64_t chunks = ceil_div(a.width, kFp4Chunk);
+    const int64_t tiles_per_group = ceil_div(a.rows, kFp4Tile);
+    const int64_t units = pack_units(a, tiles_per_group, chunks);
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t t = u / chunks, c = u - t * chunks;
+        const PackTile tile = pack_tile(a, t, tiles_per_group);
+        if (tile.n == 0) continue;  // the same for the whole block
+        const int64_t col = c * kFp4Chunk + part * 16;
+        const bool in = col < a.width;  // a multiple of 32: a block is in or out as a whole
+        uint8_t* chunk = a.sf + ((tile.group * tiles_per_group + tile.row0 / kFp4Tile) * chunks + c) * kFp4ChunkBytes;
+        if (UNPACK) {
+            const uint4 words = __ldg(reinterpret_cast<const uint4*>(chunk) + r);
+            const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int m = r + 32 * p;
+                if (m >= tile.n || !in) continue;
+                const int64_t row = tile.group * a.rows + tile.row0 + m;
+                const int64_t src = a.gated ? tile.group * a.rows + fp4_gated_row(tile.row0 + m, a.rows) : row;
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.q + row * (a.width / 2) + col / 2));
+                const float s = fp4_scale((w[p] >> (8 * (part >> 1))) & 255u);
+                uint32_t o[8];
+                const uint32_t codes[2] = {q.x, q.y};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float f[8];
+                    fp4_values8(codes[h], f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // exact: at most 2 significant bits, and 2^-128 is a bf16 value
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i] * s, f[2 * i + 1] * s);
+                        o[4 * h + i] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                }
+                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.x) + src * a.x_stride + col * 2);
+                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        } else {
+            uint4 v[4][2];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int m = r + 32 * p;
+                v[p][0] = v[p][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (m < tile.n && in) {
+                    const int64_t row = tile.row0 + m;
+                    const int64_t src = tile.group * a.rows + (a.gated ? fp4_gated_row(row, a.rows) : row);
+                    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.x) +
+                                                                    src * a.x_stride + col * 2);
+                    v[p][0] = __ldg(s);
+                    v[p][1] = __ldg(s + 1);
+                }
+            }
+            uint32_t mine = 0;  // this thread's block's scale codes, byte p for row r + 32 p
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m2 = fp4_absmax(m2, v[p][h].x);
+                    m2 = fp4_absmax(m2, v[p][h].y);
+                    m2 = fp4_absmax(m2, v[p][h].z);
+                    m2 = fp4_absmax(m2, v[p][h].w);
+                }
+                m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+                const uint32_t most = max(m2 & 0xffffu, m2 >> 16);
+                const uint32_t s = fp4_scale_code(most);
+                mine |= s << (8 * p);
+                const int m = r + 32 * p;
+                if (m < tile.n && in) {
+                    const float inv = fp4_inverse(s);
+                    const uint2 q = make_uint2(fp4_codes8(v[p][0], inv), fp4_codes8(v[p][1], inv));
+                    const int64_t row = tile.group * a.rows + tile.row0 + m;
+                    *reinterpret_cast<uint2*>(a.q + row * (a.width / 2) + col / 2) = q;
+                }
+            }
+            // The row's word of quarter p holds the four blocks' codes: thread
+            // pair p of the row's eight threads gathers byte p of each.
+            const int p = part >> 1, lane0 = (tid & 31) & ~7;
+            uint32_t word = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                word |= ((__shfl_sync(0xffffffffu, mine, lane0 + 2 * j) >> (8 * p)) & 255u) << (8 * j);
+            if ((part & 1) == 0) *reinterpret_cast<uint32_t*>(chunk + r * 16 + p * 4) = word;
+        }
+    }
+}
+
+template <bool UNPACK>
+cudaError_t launch_pack_t(const PackArgs& a, int64_t units_max, cudaStream_t stream) {
+    if (units_max <= 0) return cudaSuccess;
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(pack_kernel<UNPACK>), 0, kPackThreads, &per_sm);
+    if (e != cudaSuccess) return e;
+    int64_t grid = static_cast<int64_t>(device_sm_count()) * (per_sm < 1 ? 1 : per_sm);
+    if (grid > units_max) grid = units_max;
+    return launch_pdl(pack_kernel<UNPACK>, static_cast<unsigned>(grid), kPackThreads, 0, stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// The experts' row tiles: one CTA. Counts are summed over the source ranks
+// (threads side by side on the experts, the ranks split over the thread groups
+// that are left), then first rows and tile numbers are exclusive scans.
+
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_t* __restrict__ ntpe,
+            int32_t* __restrict__ plan, int32_t tile_cap, int32_t* __restrict__ err) {
+    pdl_wait_then_release();
+    extern __shared__ __align__(16) int32_t sm_plan[];
+    int32_t* counts = sm_plan;                     // [E]
+    __shared__ int64_t row_part[32];
+    __shared__ int32_t tile_part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < E; e += kPlanThreads) counts[e] = 0;
+    __syncthreads();
+    const int lanes_e = E < kPlanThreads ? E : kPlanThreads;
+    const int parts = kPlanThreads / lanes_e;
+    const int part = tid / lanes_e;
+    if (part < parts) {
+        for (int e = tid % lanes_e; e < E; e += lanes_e) {
+            int32_t sum = 0;
+#pragma unroll 8
+            for (int s = part; s < P; s += parts) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
+            atomicAdd(counts + e, sum);  // integers: any order gives the same sum
+        }
+    }
+    __syncthreads();
+    // Thread t scans experts [t * per, (t + 1) * per).
+    const int per = (E + kPlanThreads - 1) / kPlanThreads;
+    int64_t rows = 0;
+    int32_t tiles = 0;
+    bool bad = false;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e >= E) break;
+        int32_t n = counts[e];
+        if (n < 0 || n > max_slots) {  // not counts of this shape
+            bad = true;
+            counts[e] = n = 0;
+        }
+        rows += round_up(n, align);
+        tiles += (n + kPlanTileRows - 1) / kPlanTileRows;
+    }
+    int64_t rincl = rows;
+    int32_t tincl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t ru = __shfl_up_sync(0xffffffffu, rincl, o);
+        const int32_t tu = __shfl_up_sync(0xffffffffu, tincl, o);
+        if (lane >= o) {
+            rincl += ru;
+            tincl += tu;
+        }
+    }
+    if (lane == 31) {
+        row_part[warp] = rincl;
+        tile_part[warp] = tincl;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t r = row_part[lane];
+        int32_t t = tile_part[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t ru = __shfl_up_sync(0xffffffffu, r, o);
+            const int32_t tu = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) {
+                r += ru;
+                t += tu;
+            }
+        }
+        row_part[lane] = r;
+        tile_part[lane] = t;
+    }
+    __syncthreads();
+    int64_t row = rincl - rows + (warp ? row_part[warp - 1] : 0);
+    int32_t tile = tincl - tiles + (warp ? tile_part[warp - 1] : 0);
+    int4* list = reinterpret_cast<int4*>(plan + plan_tiles_at(E));
+    const int e4 = static_cast<int>(round_up(E, 4));
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e >= E) break;
+        int32_t n = counts[e];
+        if (row + n > INT32_MAX) {
+            bad = true;
+            n = 0;
+        }
+        plan[4 + e] = static_cast<int32_t>(row > INT32_MAX ? INT32_MAX : row);
+        plan[4 + e4 + e] = n;
+        for (int32_t at = 0; at < n; at += kPlanTileRows, ++tile) {
+            if (tile >= tile_cap) {
+                bad = true;
+                break;
+            }
+            list[tile] = make_int4(e, static_cast<int32_t>(row + at), n - at < kPlanTileRows ? n - at : kPlanTileRows, 0);
+        }
+        row += round_up(n, align);
+    }
+    if (bad) raise_error(err, MOE_ERR_INCONSISTENT);
+    if (tid == 0) {
+        plan[0] = tile_part[31] < tile_cap ? tile_part[31] : tile_cap;
+        plan[1] = static_cast<int32_t>(row_part[31] > INT32_MAX ? INT32_MAX : row_part[31]);
+        plan[2] = E;
+        plan[3] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Expert-major dispatch with an MXFP4 payload. One warp per token: the row is
+// read once and rounded once, whatever the number of its slots; the packed row
+// is staged in shared memory and sent with one bulk store per slot, the scale
+// words go straight to the slots' chunks.
+
+constexpr int kFp4DispatchWarps = 8;
+
+struct Fp4DispatchArgs {
+    int32_t P, E, K, H, epr;
+    int64_t S, T;
+    const uint16_t* x;
+    const int32_t* topk_idx;
+    const float* topk_weights;
+    const int32_t* slot_row;
+    const int64_t* part_row_base;
+    uint8_t* q;
+    uint8_t* sf;
+    int64_t arena_rows;
+    int32_t* recv_src_idx;
+    float* recv_weight;
+    int32_t* err;
+    int32_t qbytes, swords;  // packed row bytes, scale words per row
+};
+
+__host__ __device__ __forceinline__ size_t fp4_stage_bytes(int32_t H) {
+    return static_cast<size_t>(round_up(H / 2, 16) + round_up(ceil_div(H, kFp4Chunk) * 4, 16));
+}
+
+__global__ void __launch_bounds__(kFp4DispatchWarps * 32) dispatch_fp4_kernel(const Fp4DispatchArgs a) {
+    pdl_wait_then_release();
+    extern __shared__ __align__(128) unsigned char smem_d4[];
+    int64_t* prb = reinterpret_cast<int64_t*>(smem_d4);
+    const size_t stage = fp4_stage_bytes(a.H);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned char* own = smem_d4 + round_up((a.P + 1) * 8, 128) + 2 * stage * warp;
+    for (int i = threadIdx.x; i <= a.P; i += blockDim.x) prb[i] = a.part_row_base[i];
+    __syncthreads();
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kFp4DispatchWarps;
+    int buf = 0;
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kFp4DispatchWarps + warp; g < a.S; g += warps) {
+        // Lane k < K: slot k's row, or -1.
+        int64_t row = -1;
+        if (lane < a.K) {
+            const int32_t e = __ldg(a.topk_idx + g * a.K + lane);
+            const int32_t sr = __ldg(a.slot_row + g * a.K + lane);
+            if (e >= 0 && e < a.E && sr >= 0) {
+                const int64_t lo = prb[e / a.epr], hi = prb[e / a.epr + 1];
+                row = lo + sr;
+                if (sr >= hi - lo || row < 0 || row >= a.arena_rows) {
+                    raise_error(a.err, MOE_ERR_CAPACITY);
+                    row = -1;
+                }
+            }
+        }
+        uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+        if (live == 0) continue;
+        unsigned char* q = own + buf * stage;
+        uint32_t* words = reinterpret_cast<uint32_t*>(q + round_up(a.qbytes, 16));
+        bulk_wait_read<1>();  // the stores of two tokens ago have read this buffer
+        __syncwarp();
+        const uint16_t* x = a.x + g * a.H;
+#pragma unroll 2
+        for (int c0 = 0; c0 < a.H; c0 += 512) {
+            const int col = c0 + lane * 16;
+            uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+            if (col < a.H) {
+                v0 = __ldg(reinterpret_cast<const uint4*>(x + col));
+                v1 = __ldg(reinterpret_cast<const uint4*>(x + col) + 1);
+            }
+            uint32_t m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(0u, v0.x), v0.y), v0.z), v0.w);
+            m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(m2, v1.x), v1.y), v1.z), v1.w);
+            m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+            const uint32_t s = fp4_scale_code(max(m2 & 0xffffu, m2 >> 16));
+            if (col < a.H) {
+                const float inv = fp4_inverse(s);
+                *reinterpret_cast<uint2*>(q + col / 2) = make_uint2(fp4_codes8(v0, inv), fp4_codes8(v1, inv));
+            }
+            // Eight lanes cover a chunk's four blocks: its word (0 past the width).
+            uint32_t word = s << (8 * ((lane >> 1) & 3));
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            const int c = (c0 >> 7) + (lane >> 3);
+            if ((lane & 7) == 0 && c < a.swords) words[c] = word;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (row >= 0) {
+            bulk_store(a.q + row * a.qbytes, q, static_cast<uint32_t>(a.qbytes));
+            if (a.recv_src_idx) a.recv_src_idx[row] = static_cast<int32_t>(g % a.T);
+            if (a.recv_weight) a.recv_weight[row] = a.topk_weights ? __ldg(a.topk_weights + g * a.K + lane) : 1.f;
+        }
+        bulk_commit();
+        while (live) {
+            const int k = __ffs(live) - 1;
+            live &= live - 1;
+            const int64_t dst = __shfl_sync(0xffffffffu, row, k);
+            uint8_t* base = a.sf + (dst / kFp4Tile) * a.swords * kFp4ChunkBytes + fp4_word_at(static_cast<int>(dst % kFp4Tile));
+            for (int c = lane; c < a.swords; c += 32)
+                *reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(c) * kFp4ChunkBytes) = words[c];
+        }
+        __syncwarp();
+        buf ^= 1;
+    }
+    bulk_wait<0>();
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_pack(bool unpack, int32_t groups, int64_t rows, int32_t width, int32_t gated, uint16_t* x,
+                            int64_t x_stride, uint8_t* q, uint8_t* sf, const int32_t* plan, int32_t E,
+                            int64_t plan_ints, cudaStream_t stream) {
+    PackArgs a{};
+    a.rows = rows;
+    a.groups = groups;
+    a.width = width;
+    a.gated = gated;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.q = q;
+    a.sf = sf;
+    a.plan = plan;
+    a.E = E;
+    a.tile_cap = plan ? plan_capacity(E, plan_ints) : 0;
+    const int64_t tiles = plan ? 2 * static_cast<int64_t>(a.tile_cap) : groups * ceil_div(rows, kFp4Tile);
+    const int64_t units = tiles * ceil_div(width, kFp4Chunk);
+    return unpack ? launch_pack_t<true>(a, units, stream) : launch_pack_t<false>(a, units, stream);
+}
+
+cudaError_t launch_expert_plan(const moe_shape& s, const int32_t* ntpe, int32_t* plan, int64_t plan_ints, int32_t* err,
+                               cudaStream_t stream) {
+    const size_t smem = static_cast<size_t>(s.E) * 4;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(plan_kernel), smem, kPlanThreads, nullptr);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(plan_kernel, 1u, kPlanThreads, smem, stream, s.P, s.E, s.expert_alignment,
+                      static_cast<int64_t>(s.S) * s.K, ntpe, plan, plan_capacity(s.E, plan_ints), err);
+}
+
+cudaError_t launch_dispatch_fp4(const moe_shape& s, const uint16_t* x, const int32_t* topk_idx, const float* topk_weights,
+                                const int32_t* slot_row, const int64_t* part_row_base, uint8_t* q, uint8_t* sf,
+                                int64_t arena_rows, int32_t* recv_src_idx, float* recv_weight, int32_t* err,
+                                cudaStream_t stream) {
+    if (s.S == 0) return cudaSuccess;
+    Fp4DispatchArgs a{};
+    a.P = s.P;
+    a.E = s.E;
+    a.K = s.K;
+    a.H = s.H;
+    a.epr = s.E / s.P;
+    a.S = s.S;
+    a.T = s.S / s.P;
+    a.x = x;
+    a.topk_idx = topk_idx;
+    a.topk_weights = topk_weights;
+    a.slot_row = slot_row;
+    a.part_row_base = part_row_base;
+    a.q = q;
+    a.sf = sf;
+    a.arena_rows = arena_rows;
+    a.recv_src_idx = recv_src_idx;
+    a.recv_weight = recv_weight;
+    a.err = err;
+    a.qbytes = s.H / 2;
+    a.swords = static_cast<int32_t>(ceil_div(s.H, kFp4Chunk));
+    const size_t smem = static_cast<size_t>(round_up((s.P + 1) * 8, 128)) + 2 * fp4_stage_bytes(s.H) * kFp4DispatchWarps;
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(dispatch_fp4_kernel), smem, kFp4DispatchWarps * 32, &per_sm);
+    if (e != cudaSuccess) return e;
+    int64_t grid = static_cast<int64_t>(device_sm_count()) * (per_sm < 1 ? 1 : per_sm);
+    const int64_t need = ceil_div(s.S, kFp4DispatchWarps);
+    if (grid > need) grid = need;
+    return launch_pdl(dispatch_fp4_kernel, static_cast<unsigned>(grid), kFp4DispatchWarps * 32, smem, stream, a);
+}
+
+}  // namespace moe

@@ -30,7 +30,9 @@ EXPORTS = ("moe_status_string", "moe_check_shape", "moe_slot_stride", "moe_scrat
            "moe_max_recv_rows", "moe_layout", "moe_notify", "moe_dispatch", "moe_combine",
            "moe_layout_static_scratch", "moe_pad_partitions", "moe_max_expert_rows",
            "moe_notify_expert", "moe_dispatch_expert", "moe_combine_expert", "moe_dispatch_fused",
-           "moe_run_host_workspace_bytes", "moe_run_host", "moe_test_fused_barrier", "moe_exchange_plan")
+           "moe_run_host_workspace_bytes", "moe_run_host", "moe_test_fused_barrier", "moe_exchange_plan",
+           "moe_combine_grad", "moe_combine_expert_grad", "moe_fp4_scale_bytes", "moe_fp4_pack", "moe_fp4_unpack",
+           "moe_expert_plan_ints", "moe_expert_plan", "moe_dispatch_expert_fp4", "moe_expert_product_fp4")
 
 # moe_run_host flags (include/moe.h).
 MOE_RUN_FUSED = 1
@@ -38,6 +40,9 @@ MOE_RUN_EXPERT = 2
 
 # Bytes of the scratch buffer built into the library (include/moe.h).
 MOE_LAYOUT_STATIC_SCRATCH_BYTES = 1024 * 4
+
+# Rows of one chunk of MXFP4 scales: the expert_alignment of the 4-bit path is a multiple of it.
+MOE_FP4_ROW_TILE = 128
 
 
 class MoeError(RuntimeError):
@@ -123,6 +128,23 @@ def _open_lib() -> ctypes.CDLL:
     L.moe_test_fused_barrier.argtypes = [ctypes.c_uint32, i32]
     L.moe_exchange_plan.restype = i32
     L.moe_exchange_plan.argtypes = [sp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    for name in ("moe_combine_grad", "moe_combine_expert_grad"):
+        getattr(L, name).restype = i32
+        getattr(L, name).argtypes = [sp, vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp]
+    L.moe_fp4_scale_bytes.restype = i64
+    L.moe_fp4_scale_bytes.argtypes = [i64, i32]
+    L.moe_fp4_pack.restype = i32
+    L.moe_fp4_pack.argtypes = [i32, i64, i32, i32, vp, i64, vp, vp, i32, vp, i64, vp]
+    L.moe_fp4_unpack.restype = i32
+    L.moe_fp4_unpack.argtypes = [i32, i64, i32, i32, vp, vp, vp, i64, i32, vp, i64, vp]
+    L.moe_expert_plan_ints.restype = i64
+    L.moe_expert_plan_ints.argtypes = [sp]
+    L.moe_expert_plan.restype = i32
+    L.moe_expert_plan.argtypes = [sp, vp, vp, i64, vp, vp]
+    L.moe_dispatch_expert_fp4.restype = i32
+    L.moe_dispatch_expert_fp4.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+    L.moe_expert_product_fp4.restype = i32
+    L.moe_expert_product_fp4.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp]
     _lib = L
     return L
 
@@ -260,6 +282,113 @@ def moe_combine_expert(shape, y, y_row_stride, expert_part_base, arena_rows, slo
                                   _ptr(topk_idx), _ptr(topk_weights), _ptr(out), _ptr(err),
                                   _stream(stream))
     _check(st, "moe_combine_expert")
+
+
+def moe_combine_grad(shape, dout, y, y_row_stride, part_row_base, arena_rows, send_head, topk_idx, topk_weights,
+                     dy, dy_row_stride, dw, err, stream=None):
+    """Backward of moe_combine: dy rows and dw [S,K] (either may be None)."""
+    st = lib().moe_combine_grad(ctypes.byref(shape), _ptr(dout), _ptr(y), int(y_row_stride), _ptr(part_row_base),
+                                int(arena_rows), _ptr(send_head), _ptr(topk_idx), _ptr(topk_weights), _ptr(dy),
+                                int(dy_row_stride), _ptr(dw), _ptr(err), _stream(stream))
+    _check(st, "moe_combine_grad")
+
+
+def moe_combine_expert_grad(shape, dout, y, y_row_stride, expert_part_base, arena_rows, slot_row, topk_idx,
+                            topk_weights, dy, dy_row_stride, dw, err, stream=None):
+    """Backward of moe_combine_expert: dy rows and dw [S,K] (either may be None)."""
+    st = lib().moe_combine_expert_grad(ctypes.byref(shape), _ptr(dout), _ptr(y), int(y_row_stride),
+                                       _ptr(expert_part_base), int(arena_rows), _ptr(slot_row), _ptr(topk_idx),
+                                       _ptr(topk_weights), _ptr(dy), int(dy_row_stride), _ptr(dw), _ptr(err),
+                                       _stream(stream))
+    _check(st, "moe_combine_expert_grad")
+
+
+def moe_fp4_scale_bytes(rows: int, width: int) -> int:
+    return int(lib().moe_fp4_scale_bytes(int(rows), int(width)))
+
+
+def _plan_args(E, plan):
+    return (int(E), _ptr(plan), int(plan.numel())) if plan is not None else (0, None, 0)
+
+
+def moe_fp4_pack(groups, rows, width, gated, x, x_row_stride, q, sf, E=0, plan=None, stream=None):
+    """bf16 rows to MXFP4 operands (include/moe.h); with a plan, only the experts' rows."""
+    st = lib().moe_fp4_pack(int(groups), int(rows), int(width), int(gated), _ptr(x), int(x_row_stride), _ptr(q),
+                            _ptr(sf), *_plan_args(E, plan), _stream(stream))
+    _check(st, "moe_fp4_pack")
+
+
+def moe_fp4_unpack(groups, rows, width, gated, q, sf, x, x_row_stride, E=0, plan=None, stream=None):
+    """The bf16 values of MXFP4 operands; arguments as moe_fp4_pack's."""
+    st = lib().moe_fp4_unpack(int(groups), int(rows), int(width), int(gated), _ptr(q), _ptr(sf), _ptr(x),
+                              int(x_row_stride), *_plan_args(E, plan), _stream(stream))
+    _check(st, "moe_fp4_unpack")
+
+
+def moe_expert_plan_ints(shape: moe_shape) -> int:
+    return int(lib().moe_expert_plan_ints(ctypes.byref(shape)))
+
+
+def expert_plan_buffer(shape: moe_shape, device="cuda"):
+    """A plan's int32 tensor for this shape (expert_alignment a multiple of MOE_FP4_ROW_TILE)."""
+    import torch
+
+    n = moe_expert_plan_ints(shape)
+    if n < 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_plan_ints")
+    return torch.empty((n,), dtype=torch.int32, device=device)
+
+
+def moe_expert_plan(shape, num_tokens_per_expert, plan, err=None, stream=None):
+    st = lib().moe_expert_plan(ctypes.byref(shape), _ptr(num_tokens_per_expert), _ptr(plan), int(plan.numel()),
+                               _ptr(err), _stream(stream))
+    _check(st, "moe_expert_plan")
+
+
+def moe_dispatch_expert_fp4(shape, x, topk_idx, topk_weights, slot_row, expert_part_base, q, sf, arena_rows,
+                            recv_src_idx, recv_weight, err, stream=None):
+    st = lib().moe_dispatch_expert_fp4(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(topk_weights),
+                                       _ptr(slot_row), _ptr(expert_part_base), _ptr(q), _ptr(sf), int(arena_rows),
+                                       _ptr(recv_src_idx), _ptr(recv_weight), _ptr(err), _stream(stream))
+    _check(st, "moe_dispatch_expert_fp4")
+
+
+def moe_expert_product_fp4(E, N, K, gated, wq, wsf, xq, xsf, arena_rows, plan, y, err, y_row_stride=None, stream=None):
+    """y's rows of every expert from MXFP4 weights and rows; y rows are packed unless y_row_stride says otherwise."""
+    if y_row_stride is None:
+        y_row_stride = (N // 2 if gated else N) * 2
+    st = lib().moe_expert_product_fp4(int(E), int(N), int(K), int(gated), _ptr(wq), _ptr(wsf), _ptr(xq), _ptr(xsf),
+                                      int(arena_rows), _ptr(plan), int(plan.numel()), _ptr(y), int(y_row_stride),
+                                      _ptr(err), _stream(stream))
+    _check(st, "moe_expert_product_fp4")
+
+
+class Fp4Rows:
+    """MXFP4 operands of `groups` matrices of rows x width, allocated with torch.
+
+    ``q`` holds the codes, ``sf`` the scales in the products' layout. With
+    groups = E and rows = N these are the experts' weights; ``gated`` takes
+    them from [gate rows, up rows] order (see include/moe.h).
+    """
+
+    def __init__(self, rows: int, width: int, device="cuda", groups: int = 1, gated: bool = False):
+        import torch
+
+        self.rows, self.width, self.groups, self.gated = int(rows), int(width), int(groups), bool(gated)
+        nbytes = moe_fp4_scale_bytes(rows, width)
+        if nbytes < 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_fp4_scale_bytes")
+        self.q = torch.empty((self.groups * self.rows, self.width // 2), dtype=torch.uint8, device=device)
+        self.sf = torch.empty((self.groups * nbytes,), dtype=torch.uint8, device=device)
+
+    def pack(self, x, E=0, plan=None, stream=None):
+        moe_fp4_pack(self.groups, self.rows, self.width, self.gated, x, 2 * self.width, self.q, self.sf, E, plan, stream)
+        return self
+
+    def unpack(self, out, E=0, plan=None, stream=None):
+        moe_fp4_unpack(self.groups, self.rows, self.width, self.gated, self.q, self.sf, out, 2 * self.width, E, plan,
+                       stream)
+        return out
 
 
 def moe_pad_partitions(shape, num_recv_tokens, part_row_base, recv_arena, arena_rows,
@@ -462,7 +591,7 @@ class Buffers:
                            self.recv_topk_weights, stream)
 
     # ---- expert-major layout (after layout and notify) --------------------
-    def _expert_buffers(self, arena_rows=None):
+    def _slot_tables(self):
         import torch
 
         if getattr(self, "slot_row", None) is not None:
@@ -470,6 +599,14 @@ class Buffers:
         s, dev = self.shape, self.device
         self.slot_row = torch.empty((s.S, s.K), dtype=torch.int32, device=dev)
         self.expert_part_base = torch.empty((s.P + 1,), dtype=torch.int64, device=dev)
+
+    def _expert_buffers(self, arena_rows=None):
+        import torch
+
+        if getattr(self, "expert_arena", None) is not None:
+            return
+        s, dev = self.shape, self.device
+        self._slot_tables()
         self.expert_rows = moe_max_expert_rows(s) if arena_rows is None else int(arena_rows)
         rows = max(self.expert_rows, 1)
         self.expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
@@ -492,6 +629,59 @@ class Buffers:
             y, y_row_stride = self.expert_arena, self.stride
         moe_combine_expert(self.shape, y, y_row_stride, self.expert_part_base, self.expert_rows,
                            self.slot_row, topk_idx, topk_weights, out, self.err, stream)
+
+    # ---- MXFP4 experts (after layout, notify and notify_expert; expert_alignment a
+    # multiple of MOE_FP4_ROW_TILE) ------------------------------------------------
+    def _fp4_buffers(self):
+        import torch
+
+        if getattr(self, "plan", None) is not None:
+            return
+        s, dev = self.shape, self.device
+        self.plan = expert_plan_buffer(s, dev)
+        t = MOE_FP4_ROW_TILE
+        self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
+        self.fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
+        self._slot_tables()
+
+    def expert_plan(self, stream=None):
+        self._fp4_buffers()
+        moe_expert_plan(self.shape, self.num_tokens_per_expert, self.plan, self.err, stream)
+
+    def dispatch_expert_fp4(self, x, topk_idx, topk_weights, stream=None, recv_src_idx=None, recv_weight=None):
+        self._fp4_buffers()
+        moe_dispatch_expert_fp4(self.shape, x, topk_idx, topk_weights, self.slot_row, self.expert_part_base,
+                                self.fp4.q, self.fp4.sf, self.fp4_rows, recv_src_idx, recv_weight, self.err, stream)
+
+    def expert_ffn_fp4(self, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, stream=None):
+        """The whole expert layer: out[g] = sum over k of w[g][k] * W2_e (silu(gate) * up), gate and up from W1_e x.
+
+        w1 / w1_sf: the experts' gated weights [E, 2 * inner, H] as MXFP4, w2 / w2_sf: [E, H, inner]. Rows are packed
+        to MXFP4 before each product; the products' results are bf16.
+        """
+        import torch
+
+        s = self.shape
+        self._fp4_buffers()
+        inner = w2.shape[-1] * 2
+        if getattr(self, "ffn_inner", None) is None or self.ffn_inner.width != inner:
+            self.ffn_inner = Fp4Rows(self.fp4_rows, inner, self.device)
+            self.ffn_h = torch.empty((self.fp4_rows, inner), dtype=torch.bfloat16, device=self.device)
+            self.ffn_y = torch.empty((self.fp4_rows, s.H), dtype=torch.bfloat16, device=self.device)
+        self.layout(topk_idx, stream)
+        self.notify(stream)
+        moe_notify_expert(s, topk_idx, self.num_recv_tokens_per_expert, self.recv_expert_offset, self.slot_row,
+                          self.expert_part_base, self.scratch, stream)
+        self.expert_plan(stream)
+        self.dispatch_expert_fp4(x, topk_idx, topk_weights, stream)
+        moe_expert_product_fp4(s.E, 2 * inner, s.H, True, w1, w1_sf, self.fp4.q, self.fp4.sf, self.fp4_rows, self.plan,
+                               self.ffn_h, self.err, stream=stream)
+        self.ffn_inner.pack(self.ffn_h, s.E, self.plan, stream)
+        moe_expert_product_fp4(s.E, s.H, inner, False, w2, w2_sf, self.ffn_inner.q, self.ffn_inner.sf, self.fp4_rows,
+                               self.plan, self.ffn_y, self.err, stream=stream)
+        moe_combine_expert(s, self.ffn_y, 2 * s.H, self.expert_part_base, self.fp4_rows, self.slot_row, topk_idx,
+                           topk_weights, out, self.err, stream)
+        return out
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):
         """layout + notify + dispatch in one launch (small shapes only)."""

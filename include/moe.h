@@ -310,6 +310,150 @@ moe_status moe_combine_expert(const moe_shape* shape, const void* y, int64_t y_r
                               int32_t* err, void* stream);
 
 /*
+ * moe_combine_grad / moe_combine_expert_grad -- the backward pass of
+ * moe_combine / moe_combine_expert. With dout the gradient of out,
+ *
+ *   dy[row]  = bf16_rne( c * f32(dout[g]) ) for every row that token g's combine
+ *              reads; c is that row's weight as in the forward call (rank
+ *              layout: the sum, in ascending k, of the token's weights on the
+ *              rank; 1 when topk_weights is NULL), one binary32 product;
+ *   dw[g][k] = sum over h of f32(dout[g][h]) * f32(y[row of slot k][h]) in
+ *              binary32; slots whose experts share a rank share its row (rank
+ *              layout). 0 for a masked slot or a row that is skipped.
+ *
+ *   dout  bf16 bits [S,H]; y, y_row_stride, part_row_base (expert_part_base),
+ *         arena_rows, send_head (slot_row), topk_idx, topk_weights: as in the
+ *         forward call (y may be NULL when dw is)
+ *   dy    bf16 rows, dy_row_stride bytes apart (a multiple of 16, >= 2H), in the
+ *         arena's rows; NULL for no dy. Rows that no token owns (alignment gaps,
+ *         rows past a partition's tokens) are not written. May not overlap y or dout.
+ *   dw    float [S,K], every element written; NULL for no dw
+ *   err   int32 device word or NULL (MOE_ERR_CAPACITY, MOE_ERR_INCONSISTENT)
+ *
+ * The backward pass of dispatch (each row a copy of x[g]) is the forward
+ * combine without weights: moe_combine / moe_combine_expert with topk_weights =
+ * NULL sums the rows' gradients into dx[g].
+ */
+moe_status moe_combine_grad(const moe_shape* shape, const uint16_t* dout, const void* y, int64_t y_row_stride,
+                            const int64_t* part_row_base, int64_t arena_rows, const int32_t* send_head,
+                            const int32_t* topk_idx, const float* topk_weights, void* dy, int64_t dy_row_stride,
+                            float* dw, int32_t* err, void* stream);
+moe_status moe_combine_expert_grad(const moe_shape* shape, const uint16_t* dout, const void* y, int64_t y_row_stride,
+                                   const int64_t* expert_part_base, int64_t arena_rows, const int32_t* slot_row,
+                                   const int32_t* topk_idx, const float* topk_weights, void* dy,
+                                   int64_t dy_row_stride, float* dw, int32_t* err, void* stream);
+
+/*
+ * MXFP4 rows (OCP Microscaling Formats v1.0: e2m1 elements under one ue8m0
+ * power of two per 32 of them), for the experts' products.
+ *
+ * A row of `width` elements (a multiple of 32) is width / 2 bytes of codes, the
+ * even element in the low nibble, rows packed back to back, and width / 32
+ * scale bytes. A block whose largest magnitude is m has scale code
+ * s = max(0, floor(log2 m) + 125) and its elements are rounded to the nearest
+ * e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6) times 2^(s - 127), ties to the even
+ * code; magnitudes above 6 become 6. A block that holds an infinity or a NaN gets
+ * s = 255 (NaN) and codes 0. Packing is exact to the bit.
+ *
+ * The scales of `rows` rows are ceil(rows / 128) * ceil(width / 128) chunks of
+ * 512 bytes (moe_fp4_scale_bytes): chunk [row / 128][block / 4], in which the
+ * 4 scales of row m are the bytes from (m % 32) * 16 + (m % 128) / 32 * 4 on. Scales
+ * past the width are 0.
+ *
+ * Weights of E experts with N rows each are E such operands back to back
+ * (groups = E, rows = N). Gated weights hold gate and up rows by turns: 16 gate
+ * rows, then the 16 up rows that belong to them; gated = 1 makes moe_fp4_pack
+ * take them from the usual order (all N / 2 gate rows, then all up rows).
+ */
+#define MOE_FP4_ROW_TILE 128
+int64_t moe_fp4_scale_bytes(int64_t rows, int32_t width);
+
+/*
+ * moe_fp4_pack / moe_fp4_unpack -- bf16 rows to MXFP4, and back to the bf16
+ * values they stand for (every one is exact in bf16).
+ *
+ *   groups, rows   groups >= 0 operands of rows >= 0 rows each; x and q hold
+ *                  groups * rows rows, sf groups * moe_fp4_scale_bytes(rows, width) bytes
+ *   width          a multiple of 32, at most MOE_FP4_MAX_WIDTH
+ *   gated          0, or 1: x in gate / up order, the operand by turns (rows % 32 == 0)
+ *   x              bf16 bits, rows x_row_stride bytes apart (a multiple of 16, >= 2 * width)
+ *   q              uint8 [groups * rows, width / 2], 16-byte aligned
+ *   sf             uint8, 16-byte aligned
+ *   plan           NULL, or a plan of moe_expert_plan for E experts (plan_ints words):
+ *                  only the rows that it gives to experts are read and written
+ *                  (groups = 1, gated = 0, rows = the arena's, a multiple of 128).
+ *                  Scales of the other rows of a 128-row tile become 0.
+ */
+#define MOE_FP4_MAX_WIDTH 32768
+moe_status moe_fp4_pack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint16_t* x,
+                        int64_t x_row_stride, uint8_t* q, uint8_t* sf, int32_t E, const int32_t* plan,
+                        int64_t plan_ints, void* stream);
+moe_status moe_fp4_unpack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint8_t* q,
+                          const uint8_t* sf, uint16_t* x, int64_t x_row_stride, int32_t E, const int32_t* plan,
+                          int64_t plan_ints, void* stream);
+
+/*
+ * moe_expert_plan -- where the experts' rows lie in the expert-major arena, and
+ * the row tiles that the products run over. expert_alignment must be a multiple
+ * of MOE_FP4_ROW_TILE, so that an expert's rows start at a scale chunk.
+ *
+ *   num_tokens_per_expert int32 [P,E] (from moe_layout)
+ *   plan   int32 [plan_ints], plan_ints >= moe_expert_plan_ints(shape), 16-byte aligned:
+ *          [0] row tiles, [1] arena rows in use (gaps included), [2] E, [3] 0;
+ *          then, E4 = E rounded up to a multiple of 4: first arena row of each expert
+ *          [E4], rows of each expert [E4], and the tiles [.., 4]: expert, first arena
+ *          row, rows (1..MOE_PLAN_TILE_ROWS), 0
+ *   err    int32 device word or NULL: MOE_ERR_INCONSISTENT if the counts are not
+ *          those of a routing of this shape (negative, or more than S * K)
+ */
+#define MOE_PLAN_TILE_ROWS 256
+int64_t moe_expert_plan_ints(const moe_shape* shape);
+moe_status moe_expert_plan(const moe_shape* shape, const int32_t* num_tokens_per_expert, int32_t* plan,
+                           int64_t plan_ints, int32_t* err, void* stream);
+
+/*
+ * moe_dispatch_expert_fp4 -- moe_dispatch_expert with an MXFP4 payload in the
+ * products' operand layout: every valid slot's arena row expert_part_base[d] +
+ * slot_row[g][k] of q / sf receives x[g] packed as by moe_fp4_pack (each token is
+ * read and rounded once). H must be a multiple of 32; shape->quant is ignored.
+ * The scales of other rows are not written.
+ *
+ *   q           uint8 [arena_rows, H / 2]; sf uint8 [moe_fp4_scale_bytes(arena_rows, H)]
+ *   recv_src_idx int32 [arena_rows], recv_weight float [arena_rows] (each may be
+ *               NULL), err: as for moe_dispatch_expert
+ */
+moe_status moe_dispatch_expert_fp4(const moe_shape* shape, const uint16_t* x, const int32_t* topk_idx,
+                                   const float* topk_weights, const int32_t* slot_row,
+                                   const int64_t* expert_part_base, uint8_t* q, uint8_t* sf, int64_t arena_rows,
+                                   int32_t* recv_src_idx, float* recv_weight, int32_t* err, void* stream);
+
+/*
+ * moe_expert_product_fp4 -- the experts' linear layer on MXFP4 operands. For
+ * every row r that the plan gives to expert e:
+ *
+ *   v[n] = sum over k of w_e[n][k] * x[r][k]           (products exact, binary32 sum)
+ *   gated = 0: y[r][n] = bf16_rne(v[n]),               n < N
+ *   gated = 1: y[r][i] = bf16_rne(silu(gate_i) * up_i), i < N / 2, gate_i and up_i the
+ *              i-th gate and up row's v (weights held by turns), silu(a) = a / (1 + e^-a)
+ *
+ *   E, N, K     experts, weight rows per expert and row width: N and K multiples of
+ *               32, N <= MOE_FP4_MAX_WIDTH * 2, K <= MOE_FP4_MAX_WIDTH
+ *   wq, wsf     the weights' E operands of N x K
+ *   xq, xsf     the rows' operand of arena_rows x K (arena_rows a multiple of 128)
+ *   plan        moe_expert_plan's, plan_ints words
+ *   y           bf16 rows of the same arena, y_row_stride bytes apart (a multiple of
+ *               16, at least 2 bytes per value); rows that are no expert's are not written
+ *   err         int32 device word or NULL: MOE_ERR_CAPACITY for a tile outside the arena
+ *               or of no expert (skipped), MOE_ERR_DEVICE_TIMEOUT
+ * All of q, sf, x, y 16-byte aligned. A row holding a NaN block gives NaN; no row
+ * affects another.
+ */
+moe_status moe_expert_product_fp4(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq,
+                                  const uint8_t* wsf, const uint8_t* xq, const uint8_t* xsf, int64_t arena_rows,
+                                  const int32_t* plan, int64_t plan_ints, uint16_t* y, int64_t y_row_stride,
+                                  int32_t* err, void* stream);
+
+/*
  * moe_pad_partitions -- fixed-length receive partitions ("Ascend DeepEP MoE
  * Dispatch Optimization", section "输出长度有动态和固定两种模式": with a fixed
  * output length, num_worst_tokens, the host reads no count back and the rows

@@ -1,0 +1,431 @@
+"""MXFP4 on the GPU: packing, unpacking and the packing dispatch bit for bit against the
+definition in 64 bits, the plan against its definition, the grouped product and the expert layer
+against 64-bit sums.
+
+Tolerance of the product. The decoded operands and their products are exact in binary32; a sum of K
+of them in any order, each addition off by at most two units in the last place of 2^-24 (rounded or
+cut), is off by at most K * 2^-23 * sum |w x|. Rounding the result to bf16 adds half a unit in the last of 8 bits, 2^-8 of
+its magnitude. Gated results carry both sums' errors through silu(g) * u: |silu'| <= 1.1 and
+|silu(g)| <= |g|; exp, the division and the product add at most 2^-18 of the result's magnitude.
+"""
+
+import numpy as np
+import pytest
+
+from combine_moe_layout_02_gb300 import inputs, moe
+from tests import fp4_ref as ref
+from tests.helpers import bf16_bits_to_f32, f32_to_bf16_bits_torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+
+    return torch, torch.device("cuda", 0)
+
+
+def _bits(x):
+    return f32_to_bf16_bits_torch(np.asarray(x, np.float32))
+
+
+def _up(bits):
+    torch, dev = _torch()
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).to(dev)
+
+
+def _rows(rows, width, seed, kind="normal"):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((rows, width))
+    if kind == "wide":  # blocks over all of bf16's binades, its denormals and its largest values among them
+        x *= np.exp2(rng.integers(-133, 127, (rows, width // 32)).repeat(32, 1).astype(np.float64))
+        x = np.clip(x, -3.3e38, 3.3e38)
+    if kind == "ties":  # every tie of the grid under every scale that keeps it exact
+        t = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 0.0, 7.96875])
+        x = rng.choice(np.concatenate([t, -t]), (rows, width)) * np.exp2(
+            rng.integers(-100, 100, (rows, width // 32)).repeat(32, 1).astype(np.float64))
+    bits = _bits(x)
+    if kind == "special":
+        flat = bits.reshape(-1)
+        flat[rng.choice(flat.size, flat.size // 97 + 1, replace=False)] = 0x7F80  # inf
+        flat[rng.choice(flat.size, flat.size // 89 + 1, replace=False)] = 0xFFC1  # NaN
+        bits[:, :32] = 0
+        bits[0, 0] = 0x8000
+    return bits
+
+
+PACK = [(1, 32), (3, 64), (33, 96), (127, 160), (128, 128), (129, 256), (300, 2080), (5, 7168), (257, 1120)]
+
+
+@pytest.mark.parametrize("rows,width", PACK)
+@pytest.mark.parametrize("kind", ["normal", "wide", "ties", "special"])
+def test_pack_and_unpack(rows, width, kind):
+    torch, dev = _torch()
+    bits = _rows(rows, width, rows + width, kind)
+    op = moe.Fp4Rows(rows, width, dev)
+    op.q.fill_(0x5A)
+    op.sf.fill_(0x5A)
+    op.pack(_up(bits))
+    back = torch.full((rows, width), 0x5555, dtype=torch.int16, device=dev)
+    op.unpack(back)
+    torch.cuda.synchronize()
+    codes, s = ref.pack(bf16_bits_to_f32(bits).astype(np.float64))
+    np.testing.assert_array_equal(op.q.cpu().numpy(), ref.nibbles(codes))
+    np.testing.assert_array_equal(op.sf.cpu().numpy(), ref.tiled(s).reshape(-1))
+    got = bf16_bits_to_f32(back.cpu().numpy().view(np.uint16)).astype(np.float64)
+    np.testing.assert_array_equal(got, ref.values(codes, s))
+
+
+def test_pack_gated_groups_and_strides():
+    """Weights: groups with rows that end inside a tile, gate and up rows by turns, rows apart from each other."""
+    torch, dev = _torch()
+    groups, rows, width, pad = 3, 160, 96, 24
+    bits = _rows(groups * rows, width, 5)
+    wide = np.full((groups * rows, width + pad), 0x7FC0, np.uint16)
+    wide[:, :width] = bits
+    op = moe.Fp4Rows(rows, width, dev, groups=groups, gated=True)
+    x = _up(wide)
+    moe.moe_fp4_pack(groups, rows, width, 1, x, 2 * (width + pad), op.q, op.sf)
+    back = torch.full((groups * rows, width + pad), 0x5555, dtype=torch.int16, device=dev)
+    moe.moe_fp4_unpack(groups, rows, width, 1, op.q, op.sf, back, 2 * (width + pad))
+    torch.cuda.synchronize()
+    codes, s = ref.pack(bf16_bits_to_f32(bits).astype(np.float64))
+    src = np.concatenate([g * rows + ref.gated_rows(rows) for g in range(groups)])
+    np.testing.assert_array_equal(op.q.cpu().numpy(), ref.nibbles(codes[src]))
+    want = np.concatenate([ref.tiled(s[src][g * rows:(g + 1) * rows]).reshape(-1) for g in range(groups)])
+    np.testing.assert_array_equal(op.sf.cpu().numpy(), want)
+    got = back.cpu().numpy().view(np.uint16)
+    np.testing.assert_array_equal(bf16_bits_to_f32(got[:, :width]).astype(np.float64), ref.values(codes, s))
+    assert (got[:, width:] == 0x5555).all()
+
+
+def _plan_of(counts, align):
+    first, tiles, at = [], [], 0
+    for e, n in enumerate(counts):
+        first.append(at)
+        tiles += [(e, at + a, min(256, n - a), 0) for a in range(0, n, 256)]
+        at += -(-n // align) * align
+    return first, tiles, at
+
+
+def _counts_to_ntpe(counts, P, rng):
+    out = np.zeros((P, len(counts)), np.int32)
+    for e, n in enumerate(counts):
+        np.add.at(out[:, e], rng.integers(0, P, n), 1)
+    return out
+
+
+@pytest.mark.parametrize("P,E,align", [(1, 1, 128), (4, 16, 128), (3, 33, 256), (8, 256, 128), (16, 4096, 384), (1024, 1024, 128)])
+def test_plan(P, E, align):
+    torch, dev = _torch()
+    if E % P:
+        E = P * (E // P)
+    rng = np.random.default_rng(E)
+    counts = rng.choice([0, 0, 1, 2, 127, 128, 129, 255, 256, 257, 700], E)
+    S = -(-int(counts.sum()) // (2 * P)) * P + P
+    shape = moe.make_shape(P, E, S, 2, 64, expert_alignment=align)
+    plan = moe.expert_plan_buffer(shape, dev)
+    plan.fill_(-7)
+    err = torch.zeros(4, dtype=torch.int32, device=dev)
+    moe.moe_expert_plan(shape, torch.from_numpy(_counts_to_ntpe(counts, P, rng)).to(dev), plan, err)
+    got = plan.cpu().numpy()
+    first, tiles, total = _plan_of(counts, align)
+    assert int(err[0]) == 0 and list(got[:4]) == [len(tiles), total, E, 0]
+    e4 = -(-E // 4) * 4
+    np.testing.assert_array_equal(got[4:4 + E], first)
+    np.testing.assert_array_equal(got[4 + e4:4 + e4 + E], counts)
+    np.testing.assert_array_equal(got[4 + 2 * e4:4 + 2 * e4 + 4 * len(tiles)].reshape(-1, 4), np.array(tiles).reshape(-1, 4))
+
+
+def test_plan_reports_counts_of_another_shape():
+    torch, dev = _torch()
+    shape = moe.make_shape(2, 4, 64, 2, 64, expert_alignment=128)
+    plan = moe.expert_plan_buffer(shape, dev)
+    for bad in (-1, 129):
+        err = torch.zeros(4, dtype=torch.int32, device=dev)
+        ntpe = torch.tensor([[bad, 0, 0, 0], [0, 3, 0, 0]], dtype=torch.int32, device=dev)
+        moe.moe_expert_plan(shape, ntpe, plan, err)
+        assert int(err[0]) == moe.MOE_ERR_INCONSISTENT
+        assert int(plan[0]) == 1  # the other expert's tile
+
+
+def _operand(rows, width, seed, mid, spread=3):
+    """Random codes and scale codes, as an operand and as 64-bit values."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (rows, width)).astype(np.uint8)
+    s = (mid + rng.integers(0, spread, (rows, width // 32))).astype(np.uint8)
+    return codes, s
+
+
+def _product_case(counts, N, K, gated, seed=0, gap_scale=255, pad=0, nan_row=None):
+    """Runs one product; returns (y float64 rows, want, tolerance) of the valid rows after checking the rest."""
+    torch, dev = _torch()
+    E = len(counts)
+    first, tiles, total = _plan_of(counts, 128)
+    total = max(total, 128)
+    mine = np.concatenate([np.arange(f, f + n) for f, n in zip(first, counts)]).astype(int) if sum(counts) else np.zeros(0, int)
+    xc, xs = _operand(total, K, seed, 125)
+    gap = np.ones(total, bool)
+    gap[mine] = False
+    xs[gap] = gap_scale  # whatever lies in the gaps reaches nothing
+    if nan_row is not None:
+        xs[nan_row, 0] = 255
+    wc, wsc = _operand(E * N, K, seed + 1, 124)
+    S = max(1, sum(counts))
+    shape = moe.make_shape(1, E, S, 1, K, expert_alignment=128)
+    plan = moe.expert_plan_buffer(shape, dev)
+    err = torch.zeros(4, dtype=torch.int32, device=dev)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    moe.moe_expert_plan(shape, up(np.array(counts, np.int32)[None]), plan, err)
+    wsf = np.concatenate([ref.tiled(wsc[e * N:(e + 1) * N], fill=255).reshape(-1) for e in range(E)])
+    back = N // 2 if gated else N
+    y = torch.full((total, back + pad), 0x5555, dtype=torch.int16, device=dev)
+    moe.moe_expert_product_fp4(E, N, K, gated, up(ref.nibbles(wc)), up(wsf), up(ref.nibbles(xc)),
+                               up(ref.tiled(xs).reshape(-1)), total, plan, y, err, y_row_stride=2 * (back + pad))
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    got = y.cpu().numpy().view(np.uint16)
+    assert (got[gap] == 0x5555).all() and (got[:, back:] == 0x5555).all(), "stray writes"
+    x, w = ref.values(xc, xs), ref.values(wc, wsc)
+    want, tol = np.zeros((total, back)), np.zeros((total, back))
+    for e, (f, n) in enumerate(zip(first, counts)):
+        a, b = x[f:f + n], w[e * N:(e + 1) * N]
+        v, m = a @ b.T, K * 2.0 ** -23 * (np.abs(a) @ np.abs(b).T)
+        if gated:
+            at = np.arange(back) // 16 * 32 + np.arange(back) % 16
+            g, u, dg, du = v[:, at], v[:, at + 16], m[:, at], m[:, at + 16]
+            with np.errstate(over="ignore", invalid="ignore"):
+                silu = g / (1 + np.exp(-g))
+                v = silu * u
+                m = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du + 2.0 ** -18 * np.abs(v)
+        want[f:f + n], tol[f:f + n] = v, m + 2.0 ** -8 * (np.abs(v) + m) + 2.0 ** -126
+    return bf16_bits_to_f32(got[mine][:, :back]).astype(np.float64), want[mine], tol[mine], mine
+
+
+def _near(got, want, tol):
+    ok = np.abs(got - want) <= tol
+    assert ok.all(), (np.argwhere(~ok)[:5], got[~ok][:5], want[~ok][:5], tol[~ok][:5])
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("N,K", [(32, 32), (96, 64), (128, 128), (160, 96), (256, 256), (288, 416), (512, 1056),
+                                 (544, 2048)])
+def test_product_small_counts(N, K, gated):
+    got, want, tol, _ = _product_case([1, 0, 3, 17, 0, 32, 33], N, K, gated, seed=N + K)
+    _near(got, want, tol)
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+def test_product_counts_around_the_tiles(gated):
+    got, want, tol, _ = _product_case([127, 128, 129, 0, 255, 256, 257, 513, 1], 320, 352, gated, seed=3)
+    _near(got, want, tol)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1], 4096, 7168), ([2, 300, 0, 40], 768, 7168), ([1400], 7168, 2048),
+                                        ([0, 0], 64, 64), ([5] * 70, 256, 512)])
+def test_product_longer(counts, N, K):
+    got, want, tol, _ = _product_case(counts, N, K, 0, seed=sum(counts))
+    _near(got, want, tol)
+
+
+def test_product_wide_rows_apart_and_nan_row():
+    counts = [70, 3, 130]
+    got, want, tol, mine = _product_case(counts, 96, 160, 0, seed=9, pad=8, nan_row=128 + 1)
+    bad = mine == 128 + 1
+    assert np.isnan(got[bad]).all()
+    _near(got[~bad], want[~bad], tol[~bad])
+
+
+def test_product_reports_a_plan_of_another_arena():
+    torch, dev = _torch()
+    shape = moe.make_shape(1, 2, 600, 1, 64, expert_alignment=128)
+    plan = moe.expert_plan_buffer(shape, dev)
+    err = torch.zeros(4, dtype=torch.int32, device=dev)
+    moe.moe_expert_plan(shape, torch.tensor([[5, 300]], dtype=torch.int32, device=dev), plan, err)
+    w, x = moe.Fp4Rows(32, 64, dev, groups=2), moe.Fp4Rows(128, 64, dev)
+    for t in (w.q, w.sf, x.q, x.sf):
+        t.zero_()
+    y = torch.full((128, 32), 7, dtype=torch.int16, device=dev)
+    moe.moe_expert_product_fp4(2, 32, 64, 0, w.q, w.sf, x.q, x.sf, 128, plan, y, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == moe.MOE_ERR_CAPACITY
+    assert (y[:5] == 0).all() and (y[5:] == 7).all()  # expert 0's rows are in the arena, expert 1's are not
+
+
+@pytest.mark.parametrize("P,E,T,H,K,mask", [(4, 16, 64, 256, 2, 0.0), (8, 64, 50, 96, 6, 0.2), (1, 8, 7, 7168, 3, 0.0),
+                                            (32, 256, 9, 1056, 8, 0.5), (5, 5, 33, 32, 5, 1.0), (16, 64, 1, 16384, 16, 0.0)])
+def test_dispatch_fp4(P, E, T, H, K, mask):
+    """Rows of every slot as packing gives them, at the rows that moe_dispatch_expert would use; nothing else written."""
+    torch, dev = _torch()
+    w = inputs.make(P, E, T, H, K, seed=P + H, mask_frac=mask, expert_alignment=128)
+    if mask == 0.5:
+        w.topk_idx[3:7] = -1  # tokens without an expert
+    shape = moe.make_shape(P, E, w.S, K, H, w.C, 128)
+    buf = moe.Buffers(shape, dev, arena_rows=0, side_arrays=False)
+    x, idx = _up(w.x_bits), torch.from_numpy(w.topk_idx).to(dev)
+    wts = torch.from_numpy(w.topk_weights).to(dev)
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx)
+    buf.expert_plan()
+    src = torch.full((buf.fp4_rows,), -7, dtype=torch.int32, device=dev)
+    wgt = torch.full((buf.fp4_rows,), -7.0, dtype=torch.float32, device=dev)
+    buf.fp4.q.fill_(0x5A)
+    buf.fp4.sf.fill_(0x5A)
+    buf.dispatch_expert_fp4(x, idx, wts, recv_src_idx=src, recv_weight=wgt)
+    torch.cuda.synchronize()
+    assert int(buf.err[0]) == 0
+    codes, s = ref.pack(bf16_bits_to_f32(w.x_bits).astype(np.float64))
+    q = np.full((buf.fp4_rows, H // 2), 0x5A, np.uint8)
+    sf = np.full((buf.fp4_rows // 128, -(-H // 128), 512), 0x5A, np.uint8)
+    want_src, want_w = np.full(buf.fp4_rows, -7), np.full(buf.fp4_rows, -7.0, np.float32)
+    counts = np.bincount(w.topk_idx[w.topk_idx >= 0], minlength=E)
+    first, _, _ = _plan_of(counts, 128)
+    seen = np.zeros(E, int)
+    words = ref.tiled(s)
+    for g in range(w.S):
+        for k in range(K):
+            e = w.topk_idx[g, k]
+            if e < 0:
+                continue
+            row = first[e] + seen[e]
+            seen[e] += 1
+            q[row] = ref.nibbles(codes[g:g + 1])[0]
+            m, a = row % 128, g % 128
+            sf[row // 128, :, m % 32 * 16 + m // 32 * 4:][:, :4] = words[g // 128, :, a % 32 * 16 + a // 32 * 4:][:, :4]
+            want_src[row], want_w[row] = g % T, w.topk_weights[g, k]
+    np.testing.assert_array_equal(buf.fp4.q.cpu().numpy(), q)
+    np.testing.assert_array_equal(buf.fp4.sf.cpu().numpy().reshape(sf.shape), sf)
+    np.testing.assert_array_equal(src.cpu().numpy(), want_src)
+    np.testing.assert_array_equal(wgt.cpu().numpy(), want_w)
+
+
+def test_dispatch_fp4_reports_rows_past_the_arena():
+    torch, dev = _torch()
+    w = inputs.make(2, 4, 16, 64, 2, seed=1, expert_alignment=128)
+    shape = moe.make_shape(2, 4, w.S, 2, 64, w.C, 128)
+    buf = moe.Buffers(shape, dev, arena_rows=0, side_arrays=False)
+    x, idx = _up(w.x_bits), torch.from_numpy(w.topk_idx).to(dev)
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx)
+    buf._fp4_buffers()
+    buf.fp4.q.fill_(0x5A)
+    moe.moe_dispatch_expert_fp4(shape, x, idx, None, buf.slot_row, buf.expert_part_base, buf.fp4.q, buf.fp4.sf, 130, None,
+                                None, buf.err)
+    torch.cuda.synchronize()
+    assert int(buf.err[0]) == moe.MOE_ERR_CAPACITY
+    assert (buf.fp4.q[130:] == 0x5A).all() and not (buf.fp4.q[:2] == 0x5A).all()
+
+
+def test_pack_by_plan_touches_the_experts_rows_only():
+    torch, dev = _torch()
+    counts, width = [3, 0, 130, 257, 1], 224
+    first, _, total = _plan_of(counts, 128)
+    total += 128  # an arena with room to spare
+    shape = moe.make_shape(1, 5, sum(counts), 1, 64, expert_alignment=128)
+    plan = moe.expert_plan_buffer(shape, dev)
+    moe.moe_expert_plan(shape, torch.tensor([counts], dtype=torch.int32, device=dev), plan)
+    bits = _rows(total, width, 4)
+    op = moe.Fp4Rows(total, width, dev)
+    op.q.fill_(0x5A)
+    op.pack(_up(bits), E=5, plan=plan)
+    back = torch.full((total, width), 0x5555, dtype=torch.int16, device=dev)
+    op.unpack(back, E=5, plan=plan)
+    torch.cuda.synchronize()
+    codes, s = ref.pack(bf16_bits_to_f32(bits).astype(np.float64))
+    mine = np.concatenate([np.arange(f, f + n) for f, n in zip(first, counts)])
+    q, got = op.q.cpu().numpy(), back.cpu().numpy().view(np.uint16)
+    np.testing.assert_array_equal(q[mine], ref.nibbles(codes[mine]))
+    np.testing.assert_array_equal(ref.untiled(op.sf.cpu().numpy(), total, width)[mine], s[mine])
+    np.testing.assert_array_equal(bf16_bits_to_f32(got[mine]).astype(np.float64), ref.values(codes, s)[mine])
+    rest = np.setdiff1d(np.arange(total), mine)
+    assert (q[rest] == 0x5A).all() and (got[rest] == 0x5555).all()
+
+
+@pytest.mark.parametrize("P,E,T,H,K,inner,mask", [(4, 16, 64, 256, 2, 128, 0.0), (2, 8, 33, 160, 3, 96, 0.3),
+                                                  (8, 16, 1, 512, 4, 64, 0.0)])
+def test_expert_ffn(P, E, T, H, K, inner, mask):
+    """The layer's own steps give its result: the same operators one by one, each checked above, and combine in 64 bits."""
+    torch, dev = _torch()
+    w = inputs.make(P, E, T, H, K, seed=inner, mask_frac=mask, expert_alignment=128)
+    shape = moe.make_shape(P, E, w.S, K, H, w.C, 128)
+    w1 = moe.Fp4Rows(2 * inner, H, dev, groups=E, gated=True).pack(_up(_bits(
+        np.random.default_rng(1).standard_normal((E * 2 * inner, H)) / np.sqrt(H))))
+    w2 = moe.Fp4Rows(H, inner, dev, groups=E).pack(_up(_bits(
+        np.random.default_rng(2).standard_normal((E * H, inner)) / np.sqrt(inner))))
+    buf = moe.Buffers(shape, dev, arena_rows=0, side_arrays=False)
+    x, idx = _up(w.x_bits), torch.from_numpy(w.topk_idx).to(dev)
+    wts = torch.from_numpy(w.topk_weights).to(dev)
+    out = torch.full((w.S, H), 0x5555, dtype=torch.int16, device=dev)
+    w2q = w2.q.view(E, H, inner // 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # a stream that is not the tensors' own
+        buf.expert_ffn_fp4(x, idx, wts, w1.q.view(E, 2 * inner, H // 2), w1.sf, w2q, w2.sf, out)
+    side.synchronize()
+    assert int(buf.err[0]) == 0
+    # From h on in 64 bits: h as the first product left it, packed, times W2, weighted.
+    counts = np.bincount(w.topk_idx[w.topk_idx >= 0], minlength=E)
+    first, _, _ = _plan_of(counts, 128)
+    h = bf16_bits_to_f32(buf.ffn_h.view(torch.int16).cpu().numpy().view(np.uint16)).astype(np.float64)
+    xq = ref.values(*ref.pack(bf16_bits_to_f32(w.x_bits).astype(np.float64)))
+    v1 = ref.values(ref.unnibble(w1.q.cpu().numpy()), np.concatenate(
+        [ref.untiled(p, 2 * inner, H) for p in w1.sf.cpu().numpy().reshape(E, -1)]))
+    v2 = ref.values(ref.unnibble(w2.q.cpu().numpy()), np.concatenate(
+        [ref.untiled(p, H, inner) for p in w2.sf.cpu().numpy().reshape(E, -1)]))
+    seen = np.zeros(E, int)
+    want, tol = np.zeros((w.S, H)), np.zeros((w.S, H))
+    at = np.arange(inner) // 16 * 32 + np.arange(inner) % 16
+    for g in range(w.S):
+        for k in range(K):
+            e = w.topk_idx[g, k]
+            if e < 0:
+                continue
+            row = first[e] + seen[e]
+            seen[e] += 1
+            we = v1[e * 2 * inner:(e + 1) * 2 * inner]
+            v, m = we @ xq[g], H * 2.0 ** -23 * (np.abs(we) @ np.abs(xq[g]))
+            silu = v[at] / (1 + np.exp(-v[at]))
+            hv = silu * v[at + 16]
+            hm = 1.1 * m[at] * (np.abs(v[at + 16]) + m[at + 16]) + np.abs(silu) * m[at + 16] + 2.0 ** -18 * np.abs(hv)
+            _near(h[row], hv, hm + 2.0 ** -8 * (np.abs(hv) + hm) + 2.0 ** -126)
+            hq = ref.values(*ref.pack(h[row][None]))[0]
+            w2e = v2[e * H:(e + 1) * H]
+            y, ym = w2e @ hq, inner * 2.0 ** -23 * (np.abs(w2e) @ np.abs(hq))
+            ym = ym + 2.0 ** -8 * (np.abs(y) + ym)
+            c = float(w.topk_weights[g, k])
+            want[g] += c * y
+            tol[g] += c * ym + 2.0 ** -22 * c * np.abs(y)  # combine: a product and a sum in binary32 each
+    tol += 2.0 ** -8 * (np.abs(want) + tol) + K * 2.0 ** -23 * np.abs(want) + 2.0 ** -126
+    _near(bf16_bits_to_f32(out.cpu().numpy().view(np.uint16)).astype(np.float64), want, tol)
+
+
+def test_same_bits_every_run_and_in_a_graph():
+    torch, dev = _torch()
+    E, N, K, counts = 4, 416, 1184, [200, 0, 57, 300]
+    first, _, total = _plan_of(counts, 128)
+    xc, xs = _operand(total, K, 1, 125)
+    wc, ws = _operand(E * N, K, 2, 124)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    wsf = up(np.concatenate([ref.tiled(ws[e * N:(e + 1) * N]).reshape(-1) for e in range(E)]))
+    wq, xq, xsf = up(ref.nibbles(wc)), up(ref.nibbles(xc)), up(ref.tiled(xs).reshape(-1))
+    shape = moe.make_shape(1, E, sum(counts), 1, K, expert_alignment=128)
+    plan, err = moe.expert_plan_buffer(shape, dev), torch.zeros(4, dtype=torch.int32, device=dev)
+    ntpe = torch.tensor([counts], dtype=torch.int32, device=dev)
+    y = [torch.zeros((total, N), dtype=torch.int16, device=dev) for _ in range(3)]
+
+    def call(out):
+        moe.moe_expert_plan(shape, ntpe, plan, err)
+        moe.moe_expert_product_fp4(E, N, K, 0, wq, wsf, xq, xsf, total, plan, out, err)
+
+    call(y[0])
+    call(y[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(y[2])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
