@@ -2,21 +2,54 @@
 // (moe_expert_product_fp4): for every row r of expert e,
 //   v[r][n] = sum over k of w_e[n][k] * x[r][k]
 //   y[r] = bf16_rne(v[r]), or, gated, bf16_rne(silu(gate) * up) of the pairs.
+//
+// Tensor cores, tcgen05.mma kind::mxf4 with block scales: a pair of CTAs (one
+// per SM) computes 256 weight rows x up to 256 of an expert's rows. The
+// weights are the M side and the rows the N side, because N goes in steps of
+// 32 down to 32: an expert with two rows costs a thin instruction, not a tile
+// that is mostly padding, and the last tile of a long expert is cut to size.
+// Each CTA holds its 128 weight rows, half of the rows (the pair shares them:
+// every row is fetched into shared memory once per pair) and the scales.
+//
+// Warp 0 loads (TMA, 256 elements of K per stage, a ring of stages shared by
+// the pair: both CTAs' bytes count on the leading CTA's barrier), warp 1 of the
+// leading CTA copies the stage's scales to tensor memory and issues its four
+// products of K = 64, warps 4-7 of both CTAs take the sums out of tensor
+// memory (128 lanes = the CTA's weight rows, columns = the expert's rows),
+// turn them with transposing matrix stores in shared memory and write 64 bytes
+// (gated: 32) of a row per warp. Sums have two places in tensor memory, columns
+// 0 and 224 on, so that a tile's sums are written while the next tile's are
+// formed; two places of 256 columns and the scales' 24 would not fit the 512,
+// so the places share 32 columns, which are read first and given back early.
+#include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "fp4.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 32, kThreads = 256;
+constexpr int kThreads = 256;
+constexpr int kStages = 6;
+constexpr int kMTile = 256;                  // weight rows of a CTA pair
+constexpr int kStageK = 256;                 // elements of K per stage: one 128-byte swizzle row
+constexpr uint32_t kWBytes = 128 * 128;      // a CTA's weight rows of a stage
+constexpr uint32_t kXBox = 32 * 128;         // 32 rows of a stage
+constexpr uint32_t kXBytes = 4 * kXBox;      // half of 256 rows
+constexpr uint32_t kScaleBox = 2 * kFp4ChunkBytes;  // 128 rows' scales of a stage
+constexpr uint32_t kOffX = kWBytes, kOffWS = kOffX + kXBytes, kOffXS = kOffWS + kScaleBox;
+constexpr uint32_t kStageBytes = kOffXS + 2 * kScaleBox;  // a multiple of 1024
+constexpr uint32_t kOutStride = 80;          // bytes per staged row: 64 and a shift of 4 banks per row
+constexpr uint32_t kOutBytes = 4 * 32 * kOutStride;
+constexpr uint32_t kBarBytes = 256;
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes;
+constexpr int kAcc1 = 224;                   // second place of the sums
+constexpr int kScaleCol = 480;               // scales of a stage: 8 columns of the weights', 16 of the rows'
 
 struct ProductArgs {
     int32_t E, N, K, gated, tile_cap;
-    const uint8_t* wq;
-    const uint8_t* wsf;
-    const uint8_t* xq;
-    const uint8_t* xsf;
     int64_t rows;
     const int32_t* plan;
     uint16_t* y;
@@ -24,81 +57,432 @@ struct ProductArgs {
     int32_t* err;
 };
 
-// 64 rows x 64 weight rows per CTA, 4 x 4 values per thread, both operands
-// decoded to binary32 in shared memory 32 elements (one block) at a time.
-__global__ void __launch_bounds__(kThreads) product_kernel(const ProductArgs a) {
+// Barriers of a CTA, and its abort flag.
+struct Bars {
+    uint64_t full[kStages];   // leading CTA: both CTAs' loads of a stage have landed
+    uint64_t empty[kStages];  // each CTA: the products that read a stage are done
+    uint64_t acc_full[2];     // each CTA: a tile's sums are complete
+    uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place
+    uint64_t shared_free;     // leading CTA: both CTAs have read the tile's part of the shared columns
+    uint64_t drain;           // leading CTA, after a failed wait: products in flight are done
+    uint32_t tmem;
+    uint32_t abort;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+
+// One tile of work.
+struct Unit {
+    int32_t e, row, n, m0;  // expert, first arena row, rows, first weight row of the pair
+};
+
+__device__ __forceinline__ uint32_t mma_n(int32_t rows) { return (rows + 31) & ~31; }
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Bounded wait; false if it ran out or another role of the CTA gave up.
+__device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, int32_t* err) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*reinterpret_cast<volatile uint32_t*>(&b->abort)) return false;
+    }
+    *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
+    raise_error(err, MOE_ERR_DEVICE_TIMEOUT);
+    return false;
+}
+
+// TMA tile loads into this CTA's shared memory, counted on a barrier of the pair.
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                       uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory matrix descriptors: rows of 128 bytes, swizzled, 8 rows to
+// 1024 bytes; and scale chunks, 8 lanes of 16 bytes to 128 bytes.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (8ull << 32) | (1ull << 46);
+}
+
+// Instruction descriptor: e2m1 x e2m1, ue8m0 scales, M = 256, N columns, both
+// operands K-major; `half` selects which 2 of a word's 4 scales apply.
+__device__ __forceinline__ uint32_t instr(uint32_t n, uint32_t half) {
+    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | (16u << 24) | ((2u * half) << 29) | ((2u * half) << 4);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                    uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)
+        : "memory");
+}
+
+__device__ __forceinline__ void scales_to_tmem(uint32_t col, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
+}
+
+// Arrives on `bar` of both CTAs once every product and copy issued so far is done.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 lanes x 32 columns of tensor memory: v[4 i + j], column 8 i + 2 (lane % 4) + j % 2,
+// lane row lane / 4 + 8 (j / 2).
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed: lane 8 q + j gives the address
+// of the 16 bytes that column j of block q goes to.
+__device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ float gate_times_up(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+
+// Unit u of the launch, or none (n = 0) where the plan's tile is no tile of this arena.
+__device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t mtiles) {
+    const int64_t t = u / mtiles;
+    const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
+    Unit o{p.x, p.y, p.z, static_cast<int32_t>(u - t * mtiles) * kMTile};
+    if (p.x < 0 || p.x >= a.E || p.y < 0 || p.y % kFp4Tile != 0 || p.z < 0 || p.z > kPlanTileRows ||
+        p.y + static_cast<int64_t>(p.z) > a.rows) {
+        raise_error(a.err, MOE_ERR_CAPACITY);
+        o.n = 0;
+    }
+    return o;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wsmap,
+               const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xsmap) {
+    extern __shared__ unsigned char smem_raw[];
+    // The same offset in both CTAs of the pair (their shared windows are alike).
+    unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    unsigned char* out_stage = smem + kStages * kStageBytes;
+    Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t cta = cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->acc_full[i], 1);
+            mbar_init(&bars->acc_empty[i], 8);  // 4 warps of 2 CTAs
+        }
+        mbar_init(&bars->shared_free, 8);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
     pdl_wait_then_release();
-    __shared__ float xs[kTile][kStep + 1], ws[kTile][kStep + 1];
-    const int tid = threadIdx.x, tn = tid & 15, tm = tid >> 4;
+
     int32_t tiles = __ldg(a.plan);
     tiles = tiles < 0 ? 0 : (tiles > a.tile_cap ? a.tile_cap : tiles);
-    const int64_t nt = ceil_div(a.N, kTile), chunks = ceil_div(a.K, kFp4Chunk), wtiles = ceil_div(a.N, kFp4Tile);
-    const int4* list = reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E));
-    const int64_t units = static_cast<int64_t>(tiles) * 4 * nt;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int4 t = __ldg(list + u / (4 * nt));
-        const int sub = static_cast<int>(u / nt % 4) * kTile;
-        const int n0 = static_cast<int>(u % nt) * kTile;
-        if (sub >= t.z) continue;
-        if (t.x < 0 || t.x >= a.E || t.y < 0 || t.y % kFp4Tile != 0 || t.y + static_cast<int64_t>(t.z) > a.rows) {
-            raise_error(a.err, MOE_ERR_CAPACITY);
-            continue;
+    const int64_t mtiles = ceil_div(a.N, kMTile);
+    const int64_t units = tiles * mtiles;
+    const int64_t step = gridDim.x / 2, first = blockIdx.x / 2;
+    const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int32_t wtiles = static_cast<int32_t>(ceil_div(a.N, kFp4Tile));
+            uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t u = first; ok && u < units; u += step) {
+                const Unit t = unit_of(a, u, mtiles);
+                if (t.n == 0) continue;
+                const uint32_t n = mma_n(t.n);
+                const int boxes = static_cast<int>((n / 2 + 31) / 32);
+                const int halves = n > 128 ? 2 : 1;
+                const uint32_t bytes = 2 * (kWBytes + boxes * kXBox + kScaleBox + halves * kScaleBox);
+                const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
+                const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
+                const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
+                for (int k = 0; k < nstages; ++k) {
+                    if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t base = smem_addr(smem + s * kStageBytes);
+                    const uint32_t bar = cluster_map(&bars->full[s], 0);
+                    if (cta == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
+                    tma_3d(base, &wmap, k * 128, m0, t.e, bar);
+                    for (int i = 0; i < boxes; ++i) tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar);
+                    tma_3d(base + kOffWS, &wsmap, 0, 2 * k, wtile, bar);
+                    for (int i = 0; i < halves; ++i)
+                        tma_3d(base + kOffXS + i * kScaleBox, &xsmap, 0, 2 * k, t.row / kFp4Tile + i, bar);
+                    ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok && cta == 0) {  // bounded: what is in flight lands before the pair ends
+                for (int i = 0; i < kStages && i < issued; ++i) {
+                    s = s == 0 ? kStages - 1 : s - 1;
+                    if (s == kStages - 1) phase ^= 1;
+                    mbar_wait(&bars->full[s], phase);
+                }
+            }
         }
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < a.K; k0 += kStep) {
-            // 64 rows x 4 words of 8 codes of each operand
-            const int m = tid >> 2, j = tid & 3;
-            float f[8];
-            {
-                const int64_t row = t.y + sub + m;
-                uint32_t c = 0, s = 0;
-                if (sub + m < t.z) {
-                    c = __ldg(reinterpret_cast<const uint32_t*>(a.xq + row * (a.K / 2) + k0 / 2) + j);
-                    s = a.xsf[((row / kFp4Tile) * chunks + k0 / kFp4Chunk) * kFp4ChunkBytes +
-                              fp4_word_at(static_cast<int>(row % kFp4Tile)) + (k0 >> 5 & 3)];
+        __syncwarp();
+    } else if (warp == 1 && cta == 0) {
+        if (lane == 0) {
+            uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
+            bool ok = true;
+            uint32_t last_n = 0;
+            for (int64_t u = first; ok && u < units; u += step) {
+                const Unit t = unit_of(a, u, mtiles);
+                if (t.n == 0) continue;
+                const uint32_t n = mma_n(t.n), place = i & 1;
+                const uint32_t acc = tmem + (place ? kAcc1 : 0);
+                // The place's last sums have been read; and, where this tile and
+                // the one before it both reach the shared columns, that one's
+                // part of them too.
+                if (i >= 2) ok = wait_for(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a.err);
+                if (ok && i >= 1 && (place ? last_n : n) > static_cast<uint32_t>(kAcc1))
+                    ok = wait_for(bars, &bars->shared_free, (i - 1) & 1, a.err);
+                tc_fence_after();
+                last_n = n;
+                for (int k = 0; ok && k < nstages; ++k) {
+                    if (!wait_for(bars, &bars->full[s], phase, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = smem_addr(smem + s * kStageBytes);
+                    const int left = (a.K - k * kStageK + 63) / 64;
+                    const int steps = left < 4 ? left : 4;
+                    for (int c = 0; c < 2; ++c) {
+                        scales_to_tmem(tmem + kScaleCol + 4 * c, desc_scales(base + kOffWS + c * kFp4ChunkBytes));
+                        scales_to_tmem(tmem + kScaleCol + 8 + 8 * c, desc_scales(base + kOffXS + c * kFp4ChunkBytes));
+                        if (n > 128)
+                            scales_to_tmem(tmem + kScaleCol + 12 + 8 * c,
+                                           desc_scales(base + kOffXS + kScaleBox + c * kFp4ChunkBytes));
+                    }
+                    for (int j = 0; j < steps; ++j)
+                        mma(acc, desc_rows(base) + 2 * j, desc_rows(base + kOffX) + 2 * j, instr(n, j & 1),
+                            tmem + kScaleCol + 4 * (j >> 1), tmem + kScaleCol + 8 + 8 * (j >> 1), k > 0 || j > 0);
+                    commit_both(&bars->empty[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
-                fp4_values8(c, f);
-                for (int i = 0; i < 8; ++i) xs[m][j * 8 + i] = f[i] * fp4_scale(s);
+                if (ok) commit_both(&bars->acc_full[place]);
+                ++i;
             }
-            {
-                const int n = n0 + m;
-                uint32_t c = 0, s = 0;
-                if (n < a.N) {
-                    c = __ldg(reinterpret_cast<const uint32_t*>(
-                                  a.wq + (static_cast<int64_t>(t.x) * a.N + n) * (a.K / 2) + k0 / 2) + j);
-                    s = a.wsf[((t.x * wtiles + n / kFp4Tile) * chunks + k0 / kFp4Chunk) * kFp4ChunkBytes +
-                              fp4_word_at(n % kFp4Tile) + (k0 >> 5 & 3)];
-                }
-                fp4_values8(c, f);
-                for (int i = 0; i < 8; ++i) ws[m][j * 8 + i] = f[i] * fp4_scale(s);
+            if (!ok) {  // bounded: products in flight end before tensor memory is given back
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_addr(&bars->drain))
+                             : "memory");
+                mbar_wait(&bars->drain, 0);
             }
-            __syncthreads();
-#pragma unroll 8
-            for (int k = 0; k < kStep; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) acc[i][h] = fmaf(xs[tm + 16 * i][k], ws[tn + 16 * h][k], acc[i][h]);
-            __syncthreads();
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = sub + tm + 16 * i;
-            if (m >= t.z) continue;
-            uint16_t* y = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(a.y) + (t.y + m) * a.y_stride);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int n = n0 + tn + 16 * h;
-                if (n >= a.N) continue;
-                if (!a.gated) {
-                    y[n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][h]));
-                } else if ((h & 1) == 0) {
-                    const float g = acc[i][h], s = g / (1.f + __expf(-g));
-                    y[n0 / 2 + 8 * h + tn] = __bfloat16_as_ushort(__float2bfloat16_rn(s * acc[i][h + 1]));
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int w = warp - 4;
+        const uint32_t stage = smem_addr(out_stage) + w * 32 * kOutStride;
+        const unsigned char* stage_ptr = out_stage + w * 32 * kOutStride;
+        // stmatrix: block q of 8 lanes; ungated blocks are the warp's four
+        // groups of 8 weight rows, gated two groups of each of two column blocks.
+        const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
+        const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
+        uint32_t i = 0;
+        bool ok = true;
+        for (int64_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of(a, u, mtiles);
+            if (t.n == 0) continue;
+            const uint32_t place = i & 1;
+            ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int m = t.m0 + static_cast<int>(cta) * 128 + w * 32;  // the warp's weight rows
+            const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
+            const int chunks = static_cast<int>(mma_n(t.n) / 32);
+            // Place 0 has the shared columns at its end, place 1 at its start:
+            // they are read first.
+            for (int q = 0; q < chunks; ++q) {
+                const int c = place ? q : chunks - 1 - q;
+                uint32_t v[2][16];
+                tmem_load(acc + 32 * c, v[0]);
+                tmem_load(acc + 32 * c + (16u << 16), v[1]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (q == 0) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
+                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], 0));
                 }
+                if (m >= a.N) continue;
+                const int c0 = 32 * c;  // first of the chunk's 32 rows
+                if (a.gated) {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            h[2 * b + j] = bf16_pair(
+                                gate_times_up(__uint_as_float(v[0][4 * b + 2 * j]), __uint_as_float(v[1][4 * b + 2 * j])),
+                                gate_times_up(__uint_as_float(v[0][4 * b + 2 * j + 1]),
+                                              __uint_as_float(v[1][4 * b + 2 * j + 1])));
+                    store_turned(to_gated, h[0], h[1], h[2], h[3]);
+                    store_turned(to_gated + 16 * kOutStride, h[4], h[5], h[6], h[7]);
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int r = 16 * p + (lane >> 1);
+                        if (c0 + r < t.n)
+                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.y) + (t.row + c0 + r) * a.y_stride + m +
+                                                      (lane & 1) * 16) =
+                                *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 1) * 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            h[g] = bf16_pair(__uint_as_float(v[g >> 1][4 * b + 2 * (g & 1)]),
+                                             __uint_as_float(v[g >> 1][4 * b + 2 * (g & 1) + 1]));
+                        store_turned(to + 8 * b * kOutStride, h[0], h[1], h[2], h[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int r = 8 * p + (lane >> 2);
+                        if (c0 + r < t.n)
+                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.y) + (t.row + c0 + r) * a.y_stride +
+                                                      2 * m + (lane & 3) * 16) =
+                                *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 3) * 16);
+                    }
+                }
+                __syncwarp();  // the staged rows have been read
             }
+            ++i;
         }
     }
+
+    // Neither CTA may leave while the other's copies, products or arrivals can reach it.
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once per process.
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A map of codes (bytes, swizzled rows of 128) or scales (32-bit words, as they lie).
+bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encoder()(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT32, rank,
+                     const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     codes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that can be resident at once on the current device (cached).
+int resident_pairs() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / 2 * 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel, &cfg) != cudaSuccess || n < 1) return -1;
+    if (slot) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace
@@ -106,13 +490,38 @@ __global__ void __launch_bounds__(kThreads) product_kernel(const ProductArgs a) 
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
                            uint16_t* y, int64_t y_stride, int32_t* err, cudaStream_t stream) {
-    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), wq, wsf, xq, xsf, rows, plan, y, y_stride, err};
+    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, err};
     if (a.tile_cap == 0) return cudaSuccess;
-    int per_sm = 0;
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel), 0, kThreads, &per_sm);
+    if (encoder() == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t kb = static_cast<cuuint64_t>(K) / 2, chunks = static_cast<cuuint64_t>(ceil_div(K, kFp4Chunk));
+    const cuuint64_t wt = static_cast<cuuint64_t>(ceil_div(N, kFp4Tile));
+    CUtensorMap wmap, wsmap, xmap, xsmap;
+    {
+        const cuuint64_t dims[3] = {kb, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
+        const cuuint64_t strides[2] = {kb, kb * static_cast<cuuint64_t>(N)};
+        const cuuint32_t box[3] = {128, 128, 1};
+        if (!encode(&wmap, true, wq, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {
+        const cuuint64_t dims[2] = {kb, static_cast<cuuint64_t>(rows)};
+        const cuuint64_t strides[1] = {kb};
+        const cuuint32_t box[2] = {128, 32};
+        if (!encode(&xmap, true, xq, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    for (int side = 0; side < 2; ++side) {
+        const cuuint64_t dims[3] = {kFp4ChunkBytes / 4, chunks,
+                                    side ? static_cast<cuuint64_t>(rows / kFp4Tile) : wt * static_cast<cuuint64_t>(E)};
+        const cuuint64_t strides[2] = {kFp4ChunkBytes, kFp4ChunkBytes * chunks};
+        const cuuint32_t box[3] = {kFp4ChunkBytes / 4, 2, 1};
+        if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel), kSmem, kThreads, nullptr);
     if (e != cudaSuccess) return e;
-    return launch_pdl(product_kernel, static_cast<unsigned>(device_sm_count() * (per_sm < 1 ? 1 : per_sm)), kThreads, 0,
-                      stream, a);
+    const int pairs = resident_pairs();
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    const int64_t most = a.tile_cap * ceil_div(N, kMTile);
+    const unsigned grid = 2u * static_cast<unsigned>(most < pairs ? most : pairs);
+    return launch_pdl(product_kernel, grid, kThreads, kSmem, stream, a, wmap, wsmap, xmap, xsmap);
 }
 
 }  // namespace moe
