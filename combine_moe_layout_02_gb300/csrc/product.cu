@@ -93,16 +93,29 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return done != 0;
 }
 
-// Bounded wait; false if it ran out or another role of the CTA gave up.
+// Bounded wait of a whole warp; false if it ran out or another role of the CTA gave up.
 __device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, int32_t* err) {
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*reinterpret_cast<volatile uint32_t*>(&b->abort)) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&b->abort) != 0u)) return false;
     }
     *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
     raise_error(err, MOE_ERR_DEVICE_TIMEOUT);
     return false;
 }
+
+// One lane of a converged warp. The loading and the issuing warp run their
+// loops as whole warps on warp-uniform values and only the instructions
+// themselves are one lane's: in a branch of one lane the compiler cannot keep
+// descriptors in uniform registers, and each product then took about 100
+// cycles to issue and each scale copy 80 (of 128 cycles of work; measured).
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // TMA tile loads into this CTA's shared memory, counted on a barrier of the pair.
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -183,15 +196,19 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ float gate_times_up(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) * u. e^-|g| <= 1, so nothing overflows and the denominator is in [1, 2].
+__device__ __forceinline__ float gate_times_up(float g, float u) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
+}
 
-// Unit u of the launch, or none (n = 0) where the plan's tile is no tile of this arena.
+// Unit u of the launch (the same in every lane), or none (n = 0) where the plan's tile is no tile of this arena.
 __device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t mtiles) {
     const int64_t t = u / mtiles;
     const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
-    Unit o{p.x, p.y, p.z, static_cast<int32_t>(u - t * mtiles) * kMTile};
-    if (p.x < 0 || p.x >= a.E || p.y < 0 || p.y % kFp4Tile != 0 || p.z < 0 || p.z > kPlanTileRows ||
-        p.y + static_cast<int64_t>(p.z) > a.rows) {
+    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(u - t * mtiles) * kMTile};
+    if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
+        o.row + static_cast<int64_t>(o.n) > a.rows) {
         raise_error(a.err, MOE_ERR_CAPACITY);
         o.n = 0;
     }
@@ -206,7 +223,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     unsigned char* out_stage = smem + kStages * kStageBytes;
     Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t cta = cluster_ctarank();
 
     if (threadIdx.x == 0) {
@@ -238,82 +255,84 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     int32_t tiles = __ldg(a.plan);
     tiles = tiles < 0 ? 0 : (tiles > a.tile_cap ? a.tile_cap : tiles);
     const int64_t mtiles = ceil_div(a.N, kMTile);
-    const int64_t units = tiles * mtiles;
+    const int64_t units = uniform(tiles) * mtiles;
     const int64_t step = gridDim.x / 2, first = blockIdx.x / 2;
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
 
     if (warp == 0) {
-        if (lane == 0) {
-            const int32_t wtiles = static_cast<int32_t>(ceil_div(a.N, kFp4Tile));
-            uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
-            int64_t issued = 0;
-            bool ok = true;
-            for (int64_t u = first; ok && u < units; u += step) {
-                const Unit t = unit_of(a, u, mtiles);
-                if (t.n == 0) continue;
-                const uint32_t n = mma_n(t.n);
-                const int boxes = static_cast<int>((n / 2 + 31) / 32);
-                const int halves = n > 128 ? 2 : 1;
-                const uint32_t bytes = 2 * (kWBytes + boxes * kXBox + kScaleBox + halves * kScaleBox);
-                const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
-                const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
-                const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
-                for (int k = 0; k < nstages; ++k) {
-                    if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t base = smem_addr(smem + s * kStageBytes);
-                    const uint32_t bar = cluster_map(&bars->full[s], 0);
+        const int32_t wtiles = static_cast<int32_t>(ceil_div(a.N, kFp4Tile));
+        uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
+        int64_t issued = 0;
+        bool ok = true;
+        for (int64_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of(a, u, mtiles);
+            if (t.n == 0) continue;
+            const uint32_t n = mma_n(t.n);
+            const int boxes = static_cast<int>((n / 2 + 31) / 32);
+            const int halves = n > 128 ? 2 : 1;
+            const uint32_t bytes = 2 * (kWBytes + boxes * kXBox + kScaleBox + halves * kScaleBox);
+            const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
+            const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
+            const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
+            for (int k = 0; k < nstages; ++k) {
+                if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = smem_addr(smem + s * kStageBytes);
+                const uint32_t bar = cluster_map(&bars->full[s], 0);
+                if (elected()) {
                     if (cta == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
                     tma_3d(base, &wmap, k * 128, m0, t.e, bar);
-                    for (int i = 0; i < boxes; ++i) tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < boxes) tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar);
                     tma_3d(base + kOffWS, &wsmap, 0, 2 * k, wtile, bar);
-                    for (int i = 0; i < halves; ++i)
-                        tma_3d(base + kOffXS + i * kScaleBox, &xsmap, 0, 2 * k, t.row / kFp4Tile + i, bar);
-                    ++issued;
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                    tma_3d(base + kOffXS, &xsmap, 0, 2 * k, t.row / kFp4Tile, bar);
+                    if (halves > 1) tma_3d(base + kOffXS + kScaleBox, &xsmap, 0, 2 * k, t.row / kFp4Tile + 1, bar);
+                }
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok && cta == 0) {  // bounded: what is in flight lands before the pair ends
-                for (int i = 0; i < kStages && i < issued; ++i) {
-                    s = s == 0 ? kStages - 1 : s - 1;
-                    if (s == kStages - 1) phase ^= 1;
-                    mbar_wait(&bars->full[s], phase);
-                }
+        }
+        if (!ok && cta == 0) {  // bounded: what is in flight lands before the pair ends
+            for (int i = 0; i < kStages && i < issued; ++i) {
+                s = s == 0 ? kStages - 1 : s - 1;
+                if (s == kStages - 1) phase ^= 1;
+                mbar_wait(&bars->full[s], phase);
             }
         }
         __syncwarp();
     } else if (warp == 1 && cta == 0) {
-        if (lane == 0) {
-            uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
-            bool ok = true;
-            uint32_t last_n = 0;
-            for (int64_t u = first; ok && u < units; u += step) {
-                const Unit t = unit_of(a, u, mtiles);
-                if (t.n == 0) continue;
-                const uint32_t n = mma_n(t.n), place = i & 1;
-                const uint32_t acc = tmem + (place ? kAcc1 : 0);
-                // The place's last sums have been read; and, where this tile and
-                // the one before it both reach the shared columns, that one's
-                // part of them too.
-                if (i >= 2) ok = wait_for(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a.err);
-                if (ok && i >= 1 && (place ? last_n : n) > static_cast<uint32_t>(kAcc1))
-                    ok = wait_for(bars, &bars->shared_free, (i - 1) & 1, a.err);
+        uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
+        uint32_t last_n = 0;
+        bool ok = true;
+        for (int64_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of(a, u, mtiles);
+            if (t.n == 0) continue;
+            const uint32_t n = mma_n(t.n), place = i & 1;
+            const uint32_t acc = tmem + (place ? kAcc1 : 0);
+            // The place's last sums have been read; and, where this tile and
+            // the one before it both reach the shared columns, that one's
+            // part of them too.
+            if (i >= 2) ok = wait_for(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a.err);
+            if (ok && i >= 1 && (place ? last_n : n) > static_cast<uint32_t>(kAcc1))
+                ok = wait_for(bars, &bars->shared_free, (i - 1) & 1, a.err);
+            tc_fence_after();
+            last_n = n;
+            for (int k = 0; ok && k < nstages; ++k) {
+                if (!wait_for(bars, &bars->full[s], phase, a.err)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
-                last_n = n;
-                for (int k = 0; ok && k < nstages; ++k) {
-                    if (!wait_for(bars, &bars->full[s], phase, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t base = smem_addr(smem + s * kStageBytes);
-                    const int left = (a.K - k * kStageK + 63) / 64;
-                    const int steps = left < 4 ? left : 4;
+                const uint32_t base = smem_addr(smem + s * kStageBytes);
+                const int left = (a.K - k * kStageK + 63) / 64;
+                if (elected()) {
+#pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         scales_to_tmem(tmem + kScaleCol + 4 * c, desc_scales(base + kOffWS + c * kFp4ChunkBytes));
                         scales_to_tmem(tmem + kScaleCol + 8 + 8 * c, desc_scales(base + kOffXS + c * kFp4ChunkBytes));
@@ -321,24 +340,28 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                             scales_to_tmem(tmem + kScaleCol + 12 + 8 * c,
                                            desc_scales(base + kOffXS + kScaleBox + c * kFp4ChunkBytes));
                     }
-                    for (int j = 0; j < steps; ++j)
-                        mma(acc, desc_rows(base) + 2 * j, desc_rows(base + kOffX) + 2 * j, instr(n, j & 1),
-                            tmem + kScaleCol + 4 * (j >> 1), tmem + kScaleCol + 8 + 8 * (j >> 1), k > 0 || j > 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < left)
+                            mma(acc, desc_rows(base) + 2 * j, desc_rows(base + kOffX) + 2 * j, instr(n, j & 1),
+                                tmem + kScaleCol + 4 * (j >> 1), tmem + kScaleCol + 8 + 8 * (j >> 1), k > 0 || j > 0);
                     commit_both(&bars->empty[s]);
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                    if (k == nstages - 1) commit_both(&bars->acc_full[place]);
                 }
-                if (ok) commit_both(&bars->acc_full[place]);
-                ++i;
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            if (!ok) {  // bounded: products in flight end before tensor memory is given back
+            ++i;
+        }
+        if (!ok) {  // bounded: products in flight end before tensor memory is given back
+            if (elected())
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                                  smem_addr(&bars->drain))
                              : "memory");
-                mbar_wait(&bars->drain, 0);
-            }
+            mbar_wait(&bars->drain, 0);
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -356,7 +379,6 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
             ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             const int m = t.m0 + static_cast<int>(cta) * 128 + w * 32;  // the warp's weight rows
