@@ -28,6 +28,10 @@
 
 #include "fp4.cuh"
 
+#ifndef MOE_PRODUCT_QUAD_ROWS
+#define MOE_PRODUCT_QUAD_ROWS 128
+#endif
+
 namespace moe {
 namespace {
 
@@ -60,7 +64,7 @@ struct ProductArgs {
 // Barriers of a CTA, and its abort flag.
 struct Bars {
     uint64_t full[kStages];   // leading CTA: both CTAs' loads of a stage have landed
-    uint64_t empty[kStages];  // each CTA: the products that read a stage are done
+    uint64_t empty[kStages];  // each CTA: the cluster's products that read a stage are done
     uint64_t acc_full[2];     // each CTA: a tile's sums are complete
     uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place
     uint64_t shared_free;     // leading CTA: both CTAs have read the tile's part of the shared columns
@@ -117,11 +121,22 @@ __device__ __forceinline__ bool elected() {
 
 __device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// TMA tile loads into this CTA's shared memory, counted on a barrier of the pair.
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+// TMA tile loads into this CTA's shared memory, counted on the barrier of the
+// pair's leading CTA; with a mask, into the same place of every CTA in it, each
+// counted on its own pair's.
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar,
+                                       uint16_t mask) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                       uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar),
+        "h"(mask)
         : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -160,12 +175,12 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t col, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
 }
 
-// Arrives on `bar` of both CTAs once every product and copy issued so far is done.
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
+// Arrives on `bar` of the mask's CTAs once every product and copy issued so far is done.
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(mask)
         : "memory");
 }
 
@@ -203,10 +218,11 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
 }
 
 // Unit u of the launch (the same in every lane), or none (n = 0) where the plan's tile is no tile of this arena.
+template <int PAIRS>
 __device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t mtiles) {
     const int64_t t = u / mtiles;
     const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
-    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(u - t * mtiles) * kMTile};
+    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(u - t * mtiles) * (kMTile * PAIRS)};
     if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
         o.row + static_cast<int64_t>(o.n) > a.rows) {
         raise_error(a.err, MOE_ERR_CAPACITY);
@@ -215,21 +231,23 @@ __device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t
     return o;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int PAIRS>
+__global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wsmap,
                const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xsmap) {
     extern __shared__ unsigned char smem_raw[];
-    // The same offset in both CTAs of the pair (their shared windows are alike).
+    // The same offset in every CTA of the cluster (their shared windows are alike).
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     unsigned char* out_stage = smem + kStages * kStageBytes;
     Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t cta = cluster_ctarank();
+    const uint32_t rank = cluster_ctarank(), cta = rank & 1, pair = rank >> 1, lead = rank & ~1u;
+    const uint16_t all = static_cast<uint16_t>((1u << (2 * PAIRS)) - 1);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
+            mbar_init(&bars->empty[i], PAIRS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->acc_full[i], 1);
@@ -254,9 +272,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
 
     int32_t tiles = __ldg(a.plan);
     tiles = tiles < 0 ? 0 : (tiles > a.tile_cap ? a.tile_cap : tiles);
-    const int64_t mtiles = ceil_div(a.N, kMTile);
+    const int64_t mtiles = ceil_div(a.N, kMTile * PAIRS);
     const int64_t units = uniform(tiles) * mtiles;
-    const int64_t step = gridDim.x / 2, first = blockIdx.x / 2;
+    const int64_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
 
     if (warp == 0) {
@@ -265,14 +283,14 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         int64_t issued = 0;
         bool ok = true;
         for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of(a, u, mtiles);
+            const Unit t = unit_of<PAIRS>(a, u, mtiles);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n);
             const int boxes = static_cast<int>((n / 2 + 31) / 32);
             const int halves = n > 128 ? 2 : 1;
             const uint32_t bytes = 2 * (kWBytes + boxes * kXBox + kScaleBox + halves * kScaleBox);
             const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
-            const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
+            const int32_t m0 = t.m0 + static_cast<int32_t>(rank) * 128;
             const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
             for (int k = 0; k < nstages; ++k) {
                 if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a.err)) {
@@ -280,16 +298,21 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                     break;
                 }
                 const uint32_t base = smem_addr(smem + s * kStageBytes);
-                const uint32_t bar = cluster_map(&bars->full[s], 0);
+                const uint32_t bar = cluster_map(&bars->full[s], lead);
                 if (elected()) {
                     if (cta == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
                     tma_3d(base, &wmap, k * 128, m0, t.e, bar);
+                    // The CTAs with the same half of the rows load its boxes by turns, for all of them.
+                    const uint16_t mine = static_cast<uint16_t>(PAIRS == 1 ? 1u << rank : 5u << cta);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < boxes) tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar);
+                        if (i < boxes && i % PAIRS == static_cast<int>(pair))
+                            tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar, mine);
                     tma_3d(base + kOffWS, &wsmap, 0, 2 * k, wtile, bar);
-                    tma_3d(base + kOffXS, &xsmap, 0, 2 * k, t.row / kFp4Tile, bar);
-                    if (halves > 1) tma_3d(base + kOffXS + kScaleBox, &xsmap, 0, 2 * k, t.row / kFp4Tile + 1, bar);
+                    // The rows' scales go to every CTA: each half is loaded by one.
+                    if (static_cast<int>(rank) < halves)
+                        tma_3d(base + kOffXS + rank * kScaleBox, &xsmap, 0, 2 * k,
+                               t.row / kFp4Tile + static_cast<int32_t>(rank), bar, all);
                 }
                 ++issued;
                 if (++s == kStages) {
@@ -311,7 +334,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t last_n = 0;
         bool ok = true;
         for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of(a, u, mtiles);
+            const Unit t = unit_of<PAIRS>(a, u, mtiles);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n), place = i & 1;
             const uint32_t acc = tmem + (place ? kAcc1 : 0);
@@ -345,8 +368,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                         if (j < left)
                             mma(acc, desc_rows(base) + 2 * j, desc_rows(base + kOffX) + 2 * j, instr(n, j & 1),
                                 tmem + kScaleCol + 4 * (j >> 1), tmem + kScaleCol + 8 + 8 * (j >> 1), k > 0 || j > 0);
-                    commit_both(&bars->empty[s]);
-                    if (k == nstages - 1) commit_both(&bars->acc_full[place]);
+                    commit_to(&bars->empty[s], all);
+                    if (k == nstages - 1) commit_to(&bars->acc_full[place], static_cast<uint16_t>(3u << lead));
                 }
                 __syncwarp();
                 if (++s == kStages) {
@@ -375,13 +398,13 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t i = 0;
         bool ok = true;
         for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of(a, u, mtiles);
+            const Unit t = unit_of<PAIRS>(a, u, mtiles);
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
             ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
-            const int m = t.m0 + static_cast<int>(cta) * 128 + w * 32;  // the warp's weight rows
+            const int m = t.m0 + static_cast<int>(rank) * 128 + w * 32;  // the warp's weight rows
             const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
             const int chunks = static_cast<int>(mma_n(t.n) / 32);
             // Place 0 has the shared columns at its end, place 1 at its start:
@@ -395,8 +418,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (q == 0) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
-                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], 0));
+                    if (q == 0) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
+                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], lead));
                 }
                 if (m >= a.N) continue;
                 const int c0 = 32 * c;  // first of the chunk's 32 rows
@@ -483,28 +506,41 @@ bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuui
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTA pairs that can be resident at once on the current device (cached).
-int resident_pairs() {
+// Clusters that can be resident at once on the current device (cached).
+template <int PAIRS>
+int resident_clusters() {
     static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     const bool slot = dev >= 0 && dev < 64;
     if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / 2 * 2));
+    cfg.gridDim = dim3(2 * PAIRS);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 2 * PAIRS;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, product_kernel, &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<PAIRS>, &cfg) != cudaSuccess || n < 1) return -1;
     if (slot) cache[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+template <int PAIRS>
+cudaError_t launch_pairs(const ProductArgs& a, const CUtensorMap& wmap, const CUtensorMap& wsmap, const CUtensorMap& xmap,
+                         const CUtensorMap& xsmap, cudaStream_t stream) {
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel<PAIRS>), kSmem, kThreads, nullptr);
+    if (e != cudaSuccess) return e;
+    const int clusters = resident_clusters<PAIRS>();
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    const int64_t most = a.tile_cap * ceil_div(a.N, kMTile * PAIRS);
+    const unsigned grid = 2u * PAIRS * static_cast<unsigned>(most < clusters ? most : clusters);
+    return launch_pdl_cluster(product_kernel<PAIRS>, grid, kThreads, kSmem, 2u * PAIRS, stream, a, wmap, wsmap, xmap, xsmap);
 }
 
 }  // namespace
@@ -537,13 +573,9 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         const cuuint32_t box[3] = {kFp4ChunkBytes / 4, 2, 1};
         if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel), kSmem, kThreads, nullptr);
-    if (e != cudaSuccess) return e;
-    const int pairs = resident_pairs();
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
-    const int64_t most = a.tile_cap * ceil_div(N, kMTile);
-    const unsigned grid = 2u * static_cast<unsigned>(most < pairs ? most : pairs);
-    return launch_pdl(product_kernel, grid, kThreads, kSmem, stream, a, wmap, wsmap, xmap, xsmap);
+    const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
+    if (N > kMTile && per_expert >= MOE_PRODUCT_QUAD_ROWS) return launch_pairs<2>(a, wmap, wsmap, xmap, xsmap, stream);
+    return launch_pairs<1>(a, wmap, wsmap, xmap, xsmap, stream);
 }
 
 }  // namespace moe
