@@ -64,7 +64,7 @@ template <bool UNPACK>
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
     pdl_wait_then_release();
     const int tid = threadIdx.x;
-    const int r = tid >> 3, part = tid & 7;  // row of each quarter, 16-element part of its 128 elements
+    const int r = tid >> 3, part = tid & 7;  // row of each quarter, part of its 128 elements
     const int64_t chunks = ceil_div(a.width, kFp4Chunk);
     const int64_t tiles_per_group = ceil_div(a.rows, kFp4Tile);
     const int64_t units = pack_units(a, tiles_per_group, chunks);
@@ -72,38 +72,41 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
         const int64_t t = u / chunks, c = u - t * chunks;
         const PackTile tile = pack_tile(a, t, tiles_per_group);
         if (tile.n == 0) continue;  // the same for the whole block
-        const int64_t col = c * kFp4Chunk + part * 16;
-        const bool in = col < a.width;  // a multiple of 32: a block is in or out as a whole
         uint8_t* chunk = a.sf + ((tile.group * tiles_per_group + tile.row0 / kFp4Tile) * chunks + c) * kFp4ChunkBytes;
         if (UNPACK) {
+            // 8 elements at 8 * part and 8 more 64 on: the eight threads of a
+            // row write 128 bytes side by side each time.
             const uint4 words = __ldg(reinterpret_cast<const uint4*>(chunk) + r);
             const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+            const int64_t col = c * kFp4Chunk + part * 8;
+            uint32_t q[4][2];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int m = r + 32 * p;
-                if (m >= tile.n || !in) continue;
                 const int64_t row = tile.group * a.rows + tile.row0 + m;
-                const int64_t src = a.gated ? tile.group * a.rows + fp4_gated_row(tile.row0 + m, a.rows) : row;
-                const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.q + row * (a.width / 2) + col / 2));
-                const float s = fp4_scale((w[p] >> (8 * (part >> 1))) & 255u);
-                uint32_t o[8];
-                const uint32_t codes[2] = {q.x, q.y};
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    q[p][h] = m < tile.n && col + 64 * h < a.width
+                                  ? __ldg(reinterpret_cast<const uint32_t*>(a.q + row * (a.width / 2) + (col + 64 * h) / 2))
+                                  : 0u;
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int m = r + 32 * p;
+                const int64_t row = tile.row0 + m;
+                const int64_t src = tile.group * a.rows + (a.gated ? fp4_gated_row(row, a.rows) : row);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float f[8];
-                    fp4_values8(codes[h], f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // exact: at most 2 significant bits, and 2^-128 is a bf16 value
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i] * s, f[2 * i + 1] * s);
-                        o[4 * h + i] = *reinterpret_cast<const uint32_t*>(&b);
-                    }
+                    if (m >= tile.n || col + 64 * h >= a.width) continue;
+                    // every value is a bf16 value: at most 2 significant bits, from 2^-128 on
+                    const __nv_bfloat162 s = fp4_scale_pair((w[p] >> (8 * (2 * h + (part >> 2)))) & 255u);
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.x) + src * a.x_stride + (col + 64 * h) * 2) =
+                        fp4_values8(q[p][h], s);
                 }
-                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.x) + src * a.x_stride + col * 2);
-                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
             }
         } else {
+            const int64_t col = c * kFp4Chunk + part * 16;
+            const bool in = col < a.width;  // a multiple of 32: a block is in or out as a whole
             uint4 v[4][2];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {

@@ -17,6 +17,7 @@
 // (32 lanes of 16 bytes), so the product copies chunks as they are.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <stdint.h>
 
 #include "moe_device.cuh"
@@ -55,11 +56,6 @@ __device__ __forceinline__ uint32_t fp4_scale_code(uint32_t bits) {
 // rounds to code 0 either way.
 __device__ __forceinline__ float fp4_inverse(uint32_t s) { return s == 255u ? 0.f : __uint_as_float((254u - s) << 23); }
 
-// 2^(s - 127); NaN for 255.
-__device__ __forceinline__ float fp4_scale(uint32_t s) {
-    return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
-}
-
 // 8 bf16 (four words) times `inv` to 8 codes. A NaN or an infinity (inv = 0)
 // becomes code 0.
 __device__ __forceinline__ uint32_t fp4_codes8(uint4 v, float inv) {
@@ -82,16 +78,33 @@ __device__ __forceinline__ uint32_t fp4_codes8(uint4 v, float inv) {
     return inv == 0.f ? 0u : out;
 }
 
-// 8 codes to 8 binary32 e2m1 values (exact).
-__device__ __forceinline__ void fp4_values8(uint32_t codes, float (&f)[8]) {
+// 2^(s - 127) as a bf16 pair; NaN for 255.
+__device__ __forceinline__ __nv_bfloat162 fp4_scale_pair(uint32_t s) {
+    const uint32_t b = s == 0u ? 0x0040u : s == 255u ? 0x7fc0u : s << 7;
+    const uint32_t w = b * 0x10001u;
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+// 8 codes to 8 bf16 e2m1 values times a power of two, exactly. The high and
+// low bytes of a magnitude's bf16 pattern are looked up by byte permutation,
+// four codes at once (0, 0x3f00, 0x3f80, 0x3fc0, 0x4000, 0x4040, 0x4080, 0x40c0).
+__device__ __forceinline__ uint4 fp4_values8(uint32_t codes, __nv_bfloat162 scale) {
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = (codes >> (4 * i)) & 7u;
-        // subnormal codes 0 and 1 are 0 and 0.5; from 2 on the three bits are
-        // exponent and fraction of a binary32 value with bias 126
-        const float mag = c < 2u ? 0.5f * static_cast<float>(c) : __uint_as_float((c + 252u) << 22);
-        f[i] = (codes >> (4 * i)) & 8u ? -mag : mag;
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = codes >> (16 * h);
+        const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, c & 0x7777u);
+        const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, c & 0x7777u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // the two codes' sign bits 3 and 7 go to bits 15 and 31
+            const uint32_t sign = (((c >> (8 * i)) & 0x88u) * 0x01001000u) & 0x80008000u;
+            const uint32_t w = __byte_perm(lo, hi, i ? 0x7362 : 0x5140) | sign;
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), scale);
+            o[2 * h + i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Source row of packed row m of a gated operand of `rows` rows: rows come in

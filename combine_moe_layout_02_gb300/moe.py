@@ -166,11 +166,28 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_raw_stream = None
+
+
+def _current_stream():
+    """The current stream's handle. torch.cuda.current_stream() builds a Stream object (3 us of a call's 8); the
+    handle alone is read where this torch offers it."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # initialises CUDA
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is not None and device is not None:
+            _raw_stream = lambda: raw(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -381,13 +398,19 @@ class Fp4Rows:
         self.q = torch.empty((self.groups * self.rows, self.width // 2), dtype=torch.uint8, device=device)
         self.sf = torch.empty((self.groups * nbytes,), dtype=torch.uint8, device=device)
 
+        self._sizes = (self.groups, self.rows, self.width, int(self.gated))
+        self._q, self._sf = _ptr(self.q), _ptr(self.sf)
+
     def pack(self, x, E=0, plan=None, stream=None):
-        moe_fp4_pack(self.groups, self.rows, self.width, self.gated, x, 2 * self.width, self.q, self.sf, E, plan, stream)
+        """bf16 rows x [groups * rows, width] into this operand."""
+        _check(lib().moe_fp4_pack(*self._sizes, _ptr(x), 2 * self.width, self._q, self._sf, *_plan_args(E, plan),
+                                  _stream(stream)), "moe_fp4_pack")
         return self
 
     def unpack(self, out, E=0, plan=None, stream=None):
-        moe_fp4_unpack(self.groups, self.rows, self.width, self.gated, self.q, self.sf, out, 2 * self.width, E, plan,
-                       stream)
+        """The bf16 values of this operand into out [groups * rows, width]."""
+        _check(lib().moe_fp4_unpack(*self._sizes, self._q, self._sf, _ptr(out), 2 * self.width, *_plan_args(E, plan),
+                                    _stream(stream)), "moe_fp4_unpack")
         return out
 
 
