@@ -344,6 +344,12 @@ cudaError_t launch_notify_expert(const moe_shape& s, const int32_t* topk_idx, co
                                  const int32_t* reo, int32_t* slot_row, int64_t* expert_part_base,
                                  void* scratch, cudaStream_t stream);
 
+// Rows and plan of the expert layer from topk_idx alone (one partition, experts
+// at multiples of MOE_FP4_ROW_TILE rows).
+int64_t expert_route_scratch_bytes(const moe_shape& s);
+cudaError_t launch_expert_route(const moe_shape& s, const int32_t* topk_idx, int32_t* slot_row, int64_t* base,
+                                int32_t* plan, int64_t plan_ints, int32_t* err, void* scratch, cudaStream_t stream);
+
 cudaError_t launch_pad(const moe_shape& s, const int32_t* nrt, const int64_t* prb, uint8_t* arena,
                        int64_t arena_rows, int32_t* src_idx, int32_t* tk_idx, float* tk_w,
                        cudaStream_t stream);

@@ -32,7 +32,8 @@ EXPORTS = ("moe_status_string", "moe_check_shape", "moe_slot_stride", "moe_scrat
            "moe_notify_expert", "moe_dispatch_expert", "moe_combine_expert", "moe_dispatch_fused",
            "moe_run_host_workspace_bytes", "moe_run_host", "moe_test_fused_barrier", "moe_exchange_plan",
            "moe_combine_grad", "moe_combine_expert_grad", "moe_fp4_scale_bytes", "moe_fp4_pack", "moe_fp4_unpack",
-           "moe_expert_plan_ints", "moe_expert_plan", "moe_dispatch_expert_fp4", "moe_expert_product_fp4")
+           "moe_expert_plan_ints", "moe_expert_plan", "moe_dispatch_expert_fp4", "moe_expert_product_fp4",
+           "moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows", "moe_expert_ffn_fp4")
 
 # moe_run_host flags (include/moe.h).
 MOE_RUN_FUSED = 1
@@ -144,6 +145,11 @@ def _open_lib() -> ctypes.CDLL:
     L.moe_dispatch_expert_fp4.restype = i32
     L.moe_dispatch_expert_fp4.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp]
     L.moe_expert_product_fp4.restype = i32
+    for name in ("moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows"):
+        getattr(L, name).restype = i64
+        getattr(L, name).argtypes = [sp, i32]
+    L.moe_expert_ffn_fp4.restype = i32
+    L.moe_expert_ffn_fp4.argtypes = [sp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
     L.moe_expert_product_fp4.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp]
     _lib = L
     return L
@@ -378,6 +384,23 @@ def moe_expert_product_fp4(E, N, K, gated, wq, wsf, xq, xsf, arena_rows, plan, y
                                       int(arena_rows), _ptr(plan), int(plan.numel()), _ptr(y), int(y_row_stride),
                                       _ptr(err), _stream(stream))
     _check(st, "moe_expert_product_fp4")
+
+
+def moe_expert_ffn_fp4_workspace_bytes(shape: moe_shape, inner: int) -> int:
+    return int(lib().moe_expert_ffn_fp4_workspace_bytes(ctypes.byref(shape), int(inner)))
+
+
+def moe_expert_ffn_fp4_rows(shape: moe_shape, inner: int) -> int:
+    return int(lib().moe_expert_ffn_fp4_rows(ctypes.byref(shape), int(inner)))
+
+
+def moe_expert_ffn_fp4(shape, inner, x, topk_idx, topk_weights, w1q, w1sf, w2q, w2sf, out, workspace, err, h=None,
+                       stream=None):
+    """The whole expert layer (include/moe.h); workspace: uint8 tensor, h: optional inner rows."""
+    st = lib().moe_expert_ffn_fp4(ctypes.byref(shape), inner, _ptr(x), _ptr(topk_idx), _ptr(topk_weights), _ptr(w1q),
+                                  _ptr(w1sf), _ptr(w2q), _ptr(w2sf), _ptr(h), _ptr(out), _ptr(workspace),
+                                  workspace.numel(), _ptr(err), _stream(stream))
+    _check(st, "moe_expert_ffn_fp4")
 
 
 class Fp4Rows:
@@ -676,34 +699,24 @@ class Buffers:
         moe_dispatch_expert_fp4(self.shape, x, topk_idx, topk_weights, self.slot_row, self.expert_part_base,
                                 self.fp4.q, self.fp4.sf, self.fp4_rows, recv_src_idx, recv_weight, self.err, stream)
 
-    def expert_ffn_fp4(self, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, stream=None):
+    def expert_ffn_fp4(self, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, h=None, stream=None):
         """The whole expert layer: out[g] = sum over k of w[g][k] * W2_e (silu(gate) * up), gate and up from W1_e x.
 
         w1 / w1_sf: the experts' gated weights [E, 2 * inner, H] as MXFP4, w2 / w2_sf: [E, H, inner]. Rows are packed
-        to MXFP4 before each product; the products' results are bf16.
+        to MXFP4 before each product; the products' results are bf16. h: optional bf16 rows for the inner results
+        (moe_expert_ffn_fp4_rows of them).
         """
         import torch
 
-        s = self.shape
-        self._fp4_buffers()
         inner = w2.shape[-1] * 2
-        if getattr(self, "ffn_inner", None) is None or self.ffn_inner.width != inner:
-            self.ffn_inner = Fp4Rows(self.fp4_rows, inner, self.device)
-            self.ffn_h = torch.empty((self.fp4_rows, inner), dtype=torch.bfloat16, device=self.device)
-            self.ffn_y = torch.empty((self.fp4_rows, s.H), dtype=torch.bfloat16, device=self.device)
-        self.layout(topk_idx, stream)
-        self.notify(stream)
-        moe_notify_expert(s, topk_idx, self.num_recv_tokens_per_expert, self.recv_expert_offset, self.slot_row,
-                          self.expert_part_base, self.scratch, stream)
-        self.expert_plan(stream)
-        self.dispatch_expert_fp4(x, topk_idx, topk_weights, stream)
-        moe_expert_product_fp4(s.E, 2 * inner, s.H, True, w1, w1_sf, self.fp4.q, self.fp4.sf, self.fp4_rows, self.plan,
-                               self.ffn_h, self.err, stream=stream)
-        self.ffn_inner.pack(self.ffn_h, s.E, self.plan, stream)
-        moe_expert_product_fp4(s.E, s.H, inner, False, w2, w2_sf, self.ffn_inner.q, self.ffn_inner.sf, self.fp4_rows,
-                               self.plan, self.ffn_y, self.err, stream=stream)
-        moe_combine_expert(s, self.ffn_y, 2 * s.H, self.expert_part_base, self.fp4_rows, self.slot_row, topk_idx,
-                           topk_weights, out, self.err, stream)
+        if getattr(self, "ffn_inner", None) != inner:
+            n = moe_expert_ffn_fp4_workspace_bytes(self.shape, inner)
+            if n < 0:
+                raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_ffn_fp4_workspace_bytes")
+            self.ffn_workspace = torch.empty((n,), dtype=torch.uint8, device=self.device)
+            self.ffn_inner = inner
+        moe_expert_ffn_fp4(self.shape, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, self.ffn_workspace,
+                           self.err, h, stream)
         return out
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):

@@ -454,6 +454,36 @@ moe_status moe_expert_product_fp4(int32_t E, int32_t N, int32_t K, int32_t gated
                                   int32_t* err, void* stream);
 
 /*
+ * moe_expert_ffn_fp4 -- the whole expert layer of one GPU:
+ *
+ *   out[g] = bf16_rne( sum over k ascending with a valid slot of
+ *                      w[g][k] * f32(y_e) ),   y_e = W2_e h,  h = silu(gate) * up,  (gate, up) = W1_e x[g]
+ *
+ * with x and h rounded to MXFP4 (moe_fp4_pack) before each product, h and y to
+ * bf16 after it, and combine's arithmetic. The same bits as moe_dispatch_expert_fp4,
+ * moe_expert_product_fp4 (gated), moe_fp4_pack, moe_expert_product_fp4 and
+ * moe_combine_expert give one after another, in one call and without the rank
+ * tables. P, num_channels, expert_alignment and quant of the shape are only checked.
+ *
+ *   inner       a multiple of 32 (and H), at most MOE_FP4_MAX_WIDTH
+ *   x           bf16 bits [S,H]; topk_idx int32 [S,K] (negative: masked; >= E: skipped and
+ *               MOE_ERR_TOPK_OUT_OF_RANGE); topk_weights float [S,K] or NULL (1)
+ *   w1q, w1sf   gated weights, E operands of 2 * inner x H; w2q, w2sf: E of H x inner
+ *   h           NULL, or bf16 [moe_expert_ffn_fp4_rows(shape, inner), inner]: receives the
+ *               inner rows, experts in order, each from a multiple of 128 on, in (token, k) order
+ *   out         bf16 bits [S,H]
+ *   workspace   >= moe_expert_ffn_fp4_workspace_bytes(shape, inner) bytes, 256-byte aligned;
+ *               its contents do not carry over between calls
+ *   err         int32 device word or NULL; only non-zero codes are written
+ */
+int64_t moe_expert_ffn_fp4_workspace_bytes(const moe_shape* shape, int32_t inner);
+int64_t moe_expert_ffn_fp4_rows(const moe_shape* shape, int32_t inner);
+moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint16_t* x, const int32_t* topk_idx,
+                              const float* topk_weights, const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w2q,
+                              const uint8_t* w2sf, uint16_t* h, uint16_t* out, void* workspace,
+                              int64_t workspace_bytes, int32_t* err, void* stream);
+
+/*
  * moe_pad_partitions -- fixed-length receive partitions ("Ascend DeepEP MoE
  * Dispatch Optimization", section "输出长度有动态和固定两种模式": with a fixed
  * output length, num_worst_tokens, the host reads no count back and the rows

@@ -86,6 +86,27 @@ def test_product_refusals(lib):
     assert call(rows=0, xq=None, xsf=None, y=None) == moe.MOE_OK
 
 
+def test_ffn_refusals(lib):
+    s = moe.make_shape(4, 16, 64, 2, 64, expert_alignment=128)
+    need = moe.moe_expert_ffn_fp4_workspace_bytes(s, 96)
+    assert need > 0 and moe.moe_expert_ffn_fp4_rows(s, 96) == 128 * 17
+    assert moe.moe_expert_ffn_fp4_workspace_bytes(s, 48) == -1
+    assert moe.moe_expert_ffn_fp4_workspace_bytes(moe.make_shape(4, 16, 64, 2, 72), 96) == -1
+
+    def call(shape=s, inner=96, x=A, i=A, w=A, a=A, b=A, c=A, d=A, h=None, out=A, ws=A, n=need, err=None):
+        return lib.moe_expert_ffn_fp4(shape, inner, x, i, w, a, b, c, d, h, out, ws, n, err, None)
+
+    for name in ("x", "i", "a", "b", "c", "d", "out", "ws"):
+        assert call(**{name: None}) == BAD and call(**{name: A + 8}) == BAD, name
+    for name in ("w", "h"):
+        assert call(**{name: A + 8}) == BAD, name
+    assert call(n=need - 1) == BAD and call(ws=A + 16) == BAD and call(err=A + 1) == BAD
+    assert call(inner=0) == BAD and call(inner=32800) == UNSUP
+    assert call(shape=moe.make_shape(4, 16, 64, 2, 72)) == BAD
+    empty = moe.make_shape(4, 16, 0, 2, 64)
+    assert call(shape=empty, x=None, i=None, out=None, n=moe.moe_expert_ffn_fp4_workspace_bytes(empty, 96)) == moe.MOE_OK
+
+
 @pytest.mark.parametrize("name", ["moe_combine_grad", "moe_combine_expert_grad"])
 def test_gradient_refusals(lib, name):
     s = moe.make_shape(4, 16, 64, 2, 64)

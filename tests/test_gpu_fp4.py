@@ -359,16 +359,17 @@ def test_expert_ffn(P, E, T, H, K, inner, mask):
     wts = torch.from_numpy(w.topk_weights).to(dev)
     out = torch.full((w.S, H), 0x5555, dtype=torch.int16, device=dev)
     w2q = w2.q.view(E, H, inner // 2)
+    hrows = torch.full((moe.moe_expert_ffn_fp4_rows(shape, inner), inner), 0x5555, dtype=torch.int16, device=dev)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):  # a stream that is not the tensors' own
-        buf.expert_ffn_fp4(x, idx, wts, w1.q.view(E, 2 * inner, H // 2), w1.sf, w2q, w2.sf, out)
+        buf.expert_ffn_fp4(x, idx, wts, w1.q.view(E, 2 * inner, H // 2), w1.sf, w2q, w2.sf, out, h=hrows)
     side.synchronize()
     assert int(buf.err[0]) == 0
     # From h on in 64 bits: h as the first product left it, packed, times W2, weighted.
     counts = np.bincount(w.topk_idx[w.topk_idx >= 0], minlength=E)
     first, _, _ = _plan_of(counts, 128)
-    h = bf16_bits_to_f32(buf.ffn_h.view(torch.int16).cpu().numpy().view(np.uint16)).astype(np.float64)
+    h = bf16_bits_to_f32(hrows.cpu().numpy().view(np.uint16)).astype(np.float64)
     xq = ref.values(*ref.pack(bf16_bits_to_f32(w.x_bits).astype(np.float64)))
     v1 = ref.values(ref.unnibble(w1.q.cpu().numpy()), np.concatenate(
         [ref.untiled(p, 2 * inner, H) for p in w1.sf.cpu().numpy().reshape(E, -1)]))
@@ -399,6 +400,55 @@ def test_expert_ffn(P, E, T, H, K, inner, mask):
             tol[g] += c * ym + 2.0 ** -22 * c * np.abs(y)  # combine: a product and a sum in binary32 each
     tol += 2.0 ** -8 * (np.abs(want) + tol) + K * 2.0 ** -23 * np.abs(want) + 2.0 ** -126
     _near(bf16_bits_to_f32(out.cpu().numpy().view(np.uint16)).astype(np.float64), want, tol)
+
+
+def _ffn_both_ways(w, H, inner):
+    """(one call's out, the operators one by one) as bits, and the call's err."""
+    torch, dev = _torch()
+    E, S, K = w.E, w.S, w.K
+    shape = moe.make_shape(w.P, E, S, K, H, w.C, 128)
+    w1 = moe.Fp4Rows(2 * inner, H, dev, groups=E, gated=True).pack(_up(_rows(E * 2 * inner, H, 1)))
+    w2 = moe.Fp4Rows(H, inner, dev, groups=E).pack(_up(_rows(E * H, inner, 2)))
+    x, idx = _up(w.x_bits), torch.from_numpy(w.topk_idx).to(dev)
+    wts = torch.from_numpy(w.topk_weights).to(dev)
+    one = moe.Buffers(shape, dev, arena_rows=0, side_arrays=False)
+    outs = [torch.full((S, H), 0x5555, dtype=torch.int16, device=dev) for _ in range(2)]
+    one.expert_ffn_fp4(x, idx, wts, w1.q, w1.sf, w2.q, w2.sf, outs[0])
+    buf = moe.Buffers(shape, dev, arena_rows=0, side_arrays=False)
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx)
+    buf.expert_plan()
+    buf.dispatch_expert_fp4(x, idx, wts)
+    h = torch.zeros((buf.fp4_rows, inner), dtype=torch.int16, device=dev)
+    y = torch.zeros((buf.fp4_rows, H), dtype=torch.int16, device=dev)
+    moe.moe_expert_product_fp4(E, 2 * inner, H, 1, w1.q, w1.sf, buf.fp4.q, buf.fp4.sf, buf.fp4_rows, buf.plan, h, buf.err)
+    hq = moe.Fp4Rows(buf.fp4_rows, inner, dev).pack(h, E, buf.plan)
+    moe.moe_expert_product_fp4(E, H, inner, 0, w2.q, w2.sf, hq.q, hq.sf, buf.fp4_rows, buf.plan, y, buf.err)
+    moe.moe_combine_expert(shape, y, 2 * H, buf.expert_part_base, buf.fp4_rows, buf.slot_row, idx, wts, outs[1], buf.err)
+    torch.cuda.synchronize()
+    return outs[0].cpu().numpy(), outs[1].cpu().numpy(), int(one.err[0]), int(buf.err[0])
+
+
+@pytest.mark.parametrize("P,E,T,H,K,inner,mask", [(4, 16, 64, 256, 2, 128, 0.0), (1, 300, 1, 96, 7, 32, 0.0),
+                                                  (8, 64, 130, 160, 5, 96, 0.3), (2, 8, 700, 64, 3, 64, 0.1),
+                                                  (16, 4096, 20, 64, 8, 32, 0.0), (4, 8, 3, 320, 4, 160, 1.0)])
+def test_expert_ffn_is_its_operators(P, E, T, H, K, inner, mask):
+    """One chunk of tokens and many, experts without rows, tokens without experts: the same bits."""
+    w = inputs.make(P, E, T, H, K, seed=E + T, mask_frac=mask, expert_alignment=128)
+    w.topk_idx[::7] = -1
+    a, b, err_a, err_b = _ffn_both_ways(w, H, inner)
+    assert err_a == 0 and err_b == 0
+    np.testing.assert_array_equal(a, b)
+
+
+def test_expert_ffn_reports_ids_past_the_experts():
+    w = inputs.make(2, 8, 40, 64, 3, seed=1, expert_alignment=128)
+    w.topk_idx[5, 1] = 8
+    w.topk_idx[6, 0] = 2 ** 31 - 1
+    a, b, err_a, err_b = _ffn_both_ways(w, 64, 32)
+    assert err_a == moe.MOE_ERR_TOPK_OUT_OF_RANGE and err_b == moe.MOE_ERR_TOPK_OUT_OF_RANGE
+    np.testing.assert_array_equal(a, b)
 
 
 def test_same_bits_every_run_and_in_a_graph():
