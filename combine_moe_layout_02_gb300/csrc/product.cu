@@ -14,7 +14,7 @@
 // Warp 0 loads (TMA, 256 elements of K per stage, a ring of stages shared by
 // the pair: both CTAs' bytes count on the leading CTA's barrier), warp 1 of the
 // leading CTA copies the stage's scales to tensor memory and issues its four
-// products of K = 64, warps 4-7 of both CTAs take the sums out of tensor
+// products of K = 64, warps 4-11 of both CTAs take the sums out of tensor
 // memory (128 lanes = the CTA's weight rows, columns = the expert's rows),
 // turn them with transposing matrix stores in shared memory and write 64 bytes
 // (gated: 32) of a row per warp. Sums have two places in tensor memory, columns
@@ -29,13 +29,14 @@
 #include "fp4.cuh"
 
 #ifndef MOE_PRODUCT_QUAD_ROWS
-#define MOE_PRODUCT_QUAD_ROWS 128
+#define MOE_PRODUCT_QUAD_ROWS 256
 #endif
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kEpiWarps = 8;                 // two for each quarter of tensor memory's lanes
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kStages = 6;
 constexpr int kMTile = 256;                  // weight rows of a CTA pair
 constexpr int kStageK = 256;                 // elements of K per stage: one 128-byte swizzle row
@@ -46,7 +47,7 @@ constexpr uint32_t kScaleBox = 2 * kFp4ChunkBytes;  // 128 rows' scales of a sta
 constexpr uint32_t kOffX = kWBytes, kOffWS = kOffX + kXBytes, kOffXS = kOffWS + kScaleBox;
 constexpr uint32_t kStageBytes = kOffXS + 2 * kScaleBox;  // a multiple of 1024
 constexpr uint32_t kOutStride = 80;          // bytes per staged row: 64 and a shift of 4 banks per row
-constexpr uint32_t kOutBytes = 4 * 32 * kOutStride;
+constexpr uint32_t kOutBytes = kEpiWarps * 16 * kOutStride;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes;
 constexpr int kAcc1 = 224;                   // second place of the sums
@@ -187,15 +188,13 @@ __device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 lanes x 32 columns of tensor memory: v[4 i + j], column 8 i + 2 (lane % 4) + j % 2,
+// 16 lanes x 16 columns of tensor memory: v[4 i + j], column 8 i + 2 (lane % 4) + j % 2,
 // lane row lane / 4 + 8 (j / 2).
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(addr)
-        : "memory");
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Four 8 x 8 blocks of 16-bit values, transposed: lane 8 q + j gives the address
@@ -251,9 +250,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->acc_full[i], 1);
-            mbar_init(&bars->acc_empty[i], 8);  // 4 warps of 2 CTAs
+            mbar_init(&bars->acc_empty[i], 2 * kEpiWarps);
         }
-        mbar_init(&bars->shared_free, 8);
+        mbar_init(&bars->shared_free, 2 * kEpiWarps);
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         mbar_init_fence();
@@ -263,6 +262,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    if (warp == 3 && elected())
+        for (const CUtensorMap* map : {&wmap, &wsmap, &xmap, &xsmap})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -388,9 +390,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         }
         __syncwarp();
     } else if (warp >= 4) {
-        const int w = warp - 4;
-        const uint32_t stage = smem_addr(out_stage) + w * 32 * kOutStride;
-        const unsigned char* stage_ptr = out_stage + w * 32 * kOutStride;
+        const int w = warp & 3, half = (warp - 4) >> 2;  // lane quarter; which of every two chunks
+        unsigned char* stage_ptr = out_stage + (warp - 4) * 16 * kOutStride;
+        const uint32_t stage = smem_addr(stage_ptr);
         // stmatrix: block q of 8 lanes; ungated blocks are the warp's four
         // groups of 8 weight rows, gated two groups of each of two column blocks.
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
@@ -406,27 +408,28 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             tc_fence_after();
             const int m = t.m0 + static_cast<int>(rank) * 128 + w * 32;  // the warp's weight rows
             const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
-            const int chunks = static_cast<int>(mma_n(t.n) / 32);
+            const int chunks = static_cast<int>(mma_n(t.n) / 16);  // even: as many for either half
             // Place 0 has the shared columns at its end, place 1 at its start:
             // they are read first.
-            for (int q = 0; q < chunks; ++q) {
+            for (int q = half; q < chunks; q += 2) {
                 const int c = place ? q : chunks - 1 - q;
-                uint32_t v[2][16];
-                tmem_load(acc + 32 * c, v[0]);
-                tmem_load(acc + 32 * c + (16u << 16), v[1]);
+                uint32_t v[2][8];
+                tmem_load(acc + 16 * c, v[0]);
+                tmem_load(acc + 16 * c + (16u << 16), v[1]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (q == 0) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
-                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], lead));
+                    if (q == half) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
+                    if (q + 2 >= chunks) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], lead));
                 }
-                if (m >= a.N) continue;
-                const int c0 = 32 * c;  // first of the chunk's 32 rows
+                const int c0 = 16 * c;  // first of the chunk's rows
+                if (m >= a.N || c0 >= t.n) continue;
+                uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + (t.row + c0) * a.y_stride + (a.gated ? m : 2 * m);
                 if (a.gated) {
-                    uint32_t h[8];
+                    uint32_t h[4];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             h[2 * b + j] = bf16_pair(
@@ -434,19 +437,14 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                                 gate_times_up(__uint_as_float(v[0][4 * b + 2 * j + 1]),
                                               __uint_as_float(v[1][4 * b + 2 * j + 1])));
                     store_turned(to_gated, h[0], h[1], h[2], h[3]);
-                    store_turned(to_gated + 16 * kOutStride, h[4], h[5], h[6], h[7]);
                     __syncwarp();
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const int r = 16 * p + (lane >> 1);
-                        if (c0 + r < t.n)
-                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.y) + (t.row + c0 + r) * a.y_stride + m +
-                                                      (lane & 1) * 16) =
-                                *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 1) * 16);
-                    }
+                    const int r = lane >> 1;
+                    if (c0 + r < t.n)
+                        *reinterpret_cast<uint4*>(y + r * a.y_stride + (lane & 1) * 16) =
+                            *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 1) * 16);
                 } else {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    for (int b = 0; b < 2; ++b) {
                         uint32_t h[4];
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
@@ -456,11 +454,10 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
+                    for (int p = 0; p < 2; ++p) {
                         const int r = 8 * p + (lane >> 2);
                         if (c0 + r < t.n)
-                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.y) + (t.row + c0 + r) * a.y_stride +
-                                                      2 * m + (lane & 3) * 16) =
+                            *reinterpret_cast<uint4*>(y + r * a.y_stride + (lane & 3) * 16) =
                                 *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 3) * 16);
                     }
                 }
