@@ -313,10 +313,11 @@ moe_status moe_combine_expert(const moe_shape* shape, const void* y, int64_t y_r
  * moe_combine_grad / moe_combine_expert_grad -- the backward pass of
  * moe_combine / moe_combine_expert. With dout the gradient of out,
  *
- *   dy[row]  = bf16_rne( c * f32(dout[g]) ) for every row that token g's combine
- *              reads; c is that row's weight as in the forward call (rank
- *              layout: the sum, in ascending k, of the token's weights on the
- *              rank; 1 when topk_weights is NULL), one binary32 product;
+ *   dy[row]  = bf16_rne( c * f32(dout[g]) ) for every row that one of token g's
+ *              slots has (rank layout: the rows of its slots' ranks, where
+ *              send_head has one); c is that row's weight as in the forward call
+ *              (rank layout: the sum, in ascending k, of the token's weights on
+ *              the rank; 1 when topk_weights is NULL), one binary32 product;
  *   dw[g][k] = sum over h of f32(dout[g][h]) * f32(y[row of slot k][h]) in
  *              binary32; slots whose experts share a rank share its row (rank
  *              layout). 0 for a masked slot or a row that is skipped.
@@ -328,7 +329,7 @@ moe_status moe_combine_expert(const moe_shape* shape, const void* y, int64_t y_r
  *         arena's rows; NULL for no dy. Rows that no token owns (alignment gaps,
  *         rows past a partition's tokens) are not written. May not overlap y or dout.
  *   dw    float [S,K], every element written; NULL for no dw
- *   err   int32 device word or NULL (MOE_ERR_CAPACITY, MOE_ERR_INCONSISTENT)
+ *   err   int32 device word or NULL (MOE_ERR_CAPACITY)
  *
  * The backward pass of dispatch (each row a copy of x[g]) is the forward
  * combine without weights: moe_combine / moe_combine_expert with topk_weights =
