@@ -5,6 +5,10 @@
 
 #include "fp4.cuh"
 
+#ifndef MOE_FP4_DISPATCH_ROUNDS
+#define MOE_FP4_DISPATCH_ROUNDS 2
+#endif
+
 namespace moe {
 namespace {
 
@@ -278,10 +282,11 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
 }
 
 // ---------------------------------------------------------------------------
-// Expert-major dispatch with an MXFP4 payload. One warp per token: the row is
-// read once and rounded once, whatever the number of its slots; the packed row
-// is staged in shared memory and sent with one bulk store per slot, the scale
-// words go straight to the slots' chunks.
+// Expert-major dispatch with an MXFP4 payload. The unit of work is a token, or
+// a part of its columns when there are few tokens, and a warp takes one at a
+// time: the columns are read once and rounded once, whatever the number of the
+// token's slots; the packed columns are staged in shared memory and sent with
+// one bulk store per slot, the scale words go straight to the slots' chunks.
 
 constexpr int kFp4DispatchWarps = 8;
 
@@ -300,24 +305,30 @@ struct Fp4DispatchArgs {
     float* recv_weight;
     int32_t* err;
     int32_t qbytes, swords;  // packed row bytes, scale words per row
+    int32_t parts, part_cols;  // parts of a token, columns of each (a multiple of 512; the last one's may be fewer)
 };
 
-__host__ __device__ __forceinline__ size_t fp4_stage_bytes(int32_t H) {
-    return static_cast<size_t>(round_up(H / 2, 16) + round_up(ceil_div(H, kFp4Chunk) * 4, 16));
+// Staged codes and scale words of a part.
+__host__ __device__ __forceinline__ size_t fp4_stage_bytes(int32_t cols) {
+    return static_cast<size_t>(cols / 2 + cols / kFp4Chunk * 4);
 }
 
 __global__ void __launch_bounds__(kFp4DispatchWarps * 32) dispatch_fp4_kernel(const Fp4DispatchArgs a) {
     pdl_wait_then_release();
     extern __shared__ __align__(128) unsigned char smem_d4[];
     int64_t* prb = reinterpret_cast<int64_t*>(smem_d4);
-    const size_t stage = fp4_stage_bytes(a.H);
+    const size_t stage = fp4_stage_bytes(a.part_cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned char* own = smem_d4 + round_up((a.P + 1) * 8, 128) + 2 * stage * warp;
     for (int i = threadIdx.x; i <= a.P; i += blockDim.x) prb[i] = a.part_row_base[i];
     __syncthreads();
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kFp4DispatchWarps;
     int buf = 0;
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kFp4DispatchWarps + warp; g < a.S; g += warps) {
+    const int64_t units = a.S * a.parts;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kFp4DispatchWarps + warp; u < units; u += warps) {
+        const int64_t g = u / a.parts;
+        const int part = static_cast<int>(u - g * a.parts);
+        const int col0 = part * a.part_cols, cols = min(a.part_cols, a.H - col0);
         // Lane k < K: slot k's row, or -1.
         int64_t row = -1;
         if (lane < a.K) {
@@ -335,15 +346,16 @@ __global__ void __launch_bounds__(kFp4DispatchWarps * 32) dispatch_fp4_kernel(co
         uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
         if (live == 0) continue;
         unsigned char* q = own + buf * stage;
-        uint32_t* words = reinterpret_cast<uint32_t*>(q + round_up(a.qbytes, 16));
+        uint32_t* words = reinterpret_cast<uint32_t*>(q + a.part_cols / 2);
         bulk_wait_read<1>();  // the stores of two tokens ago have read this buffer
         __syncwarp();
-        const uint16_t* x = a.x + g * a.H;
+        const uint16_t* x = a.x + g * a.H + col0;
+        const int swords = (cols + kFp4Chunk - 1) / kFp4Chunk;
 #pragma unroll 2
-        for (int c0 = 0; c0 < a.H; c0 += 512) {
+        for (int c0 = 0; c0 < cols; c0 += 512) {
             const int col = c0 + lane * 16;
             uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-            if (col < a.H) {
+            if (col < cols) {
                 v0 = __ldg(reinterpret_cast<const uint4*>(x + col));
                 v1 = __ldg(reinterpret_cast<const uint4*>(x + col) + 1);
             }
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(kFp4DispatchWarps * 32) dispatch_fp4_kernel(co
             m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(m2, v1.x), v1.y), v1.z), v1.w);
             m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
             const uint32_t s = fp4_scale_code(max(m2 & 0xffffu, m2 >> 16));
-            if (col < a.H) {
+            if (col < cols) {
                 const float inv = fp4_inverse(s);
                 *reinterpret_cast<uint2*>(q + col / 2) = make_uint2(fp4_codes8(v0, inv), fp4_codes8(v1, inv));
             }
@@ -360,22 +372,23 @@ __global__ void __launch_bounds__(kFp4DispatchWarps * 32) dispatch_fp4_kernel(co
             word |= __shfl_xor_sync(0xffffffffu, word, 2);
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             const int c = (c0 >> 7) + (lane >> 3);
-            if ((lane & 7) == 0 && c < a.swords) words[c] = word;
+            if ((lane & 7) == 0 && c < swords) words[c] = word;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (row >= 0) {
-            bulk_store(a.q + row * a.qbytes, q, static_cast<uint32_t>(a.qbytes));
-            if (a.recv_src_idx) a.recv_src_idx[row] = static_cast<int32_t>(g % a.T);
-            if (a.recv_weight) a.recv_weight[row] = a.topk_weights ? __ldg(a.topk_weights + g * a.K + lane) : 1.f;
+            bulk_store(a.q + row * a.qbytes + col0 / 2, q, static_cast<uint32_t>(cols / 2));
+            if (part == 0 && a.recv_src_idx) a.recv_src_idx[row] = static_cast<int32_t>(g % a.T);
+            if (part == 0 && a.recv_weight) a.recv_weight[row] = a.topk_weights ? __ldg(a.topk_weights + g * a.K + lane) : 1.f;
         }
         bulk_commit();
         while (live) {
             const int k = __ffs(live) - 1;
             live &= live - 1;
             const int64_t dst = __shfl_sync(0xffffffffu, row, k);
-            uint8_t* base = a.sf + (dst / kFp4Tile) * a.swords * kFp4ChunkBytes + fp4_word_at(static_cast<int>(dst % kFp4Tile));
-            for (int c = lane; c < a.swords; c += 32)
+            uint8_t* base = a.sf + ((dst / kFp4Tile) * a.swords + col0 / kFp4Chunk) * kFp4ChunkBytes +
+                            fp4_word_at(static_cast<int>(dst % kFp4Tile));
+            for (int c = lane; c < swords; c += 32)
                 *reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(c) * kFp4ChunkBytes) = words[c];
         }
         __syncwarp();
@@ -441,12 +454,20 @@ cudaError_t launch_dispatch_fp4(const moe_shape& s, const uint16_t* x, const int
     a.err = err;
     a.qbytes = s.H / 2;
     a.swords = static_cast<int32_t>(ceil_div(s.H, kFp4Chunk));
-    const size_t smem = static_cast<size_t>(round_up((s.P + 1) * 8, 128)) + 2 * fp4_stage_bytes(s.H) * kFp4DispatchWarps;
+    // Parts: halve the columns while every warp of the device would have fewer
+    // than MOE_FP4_DISPATCH_ROUNDS parts.
+    const int64_t blocks512 = ceil_div(s.H, 512);
+    const int64_t warps = static_cast<int64_t>(device_sm_count()) * 4 * kFp4DispatchWarps;
+    int64_t parts = 1;
+    while (parts < blocks512 && s.S * parts < MOE_FP4_DISPATCH_ROUNDS * warps) parts *= 2;
+    a.part_cols = static_cast<int32_t>(ceil_div(blocks512, parts) * 512);
+    a.parts = static_cast<int32_t>(ceil_div(s.H, a.part_cols));
+    const size_t smem = static_cast<size_t>(round_up((s.P + 1) * 8, 128)) + 2 * fp4_stage_bytes(a.part_cols) * kFp4DispatchWarps;
     int per_sm = 0;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(dispatch_fp4_kernel), smem, kFp4DispatchWarps * 32, &per_sm);
     if (e != cudaSuccess) return e;
     int64_t grid = static_cast<int64_t>(device_sm_count()) * (per_sm < 1 ? 1 : per_sm);
-    const int64_t need = ceil_div(s.S, kFp4DispatchWarps);
+    const int64_t need = ceil_div(s.S * a.parts, kFp4DispatchWarps);
     if (grid > need) grid = need;
     return launch_pdl(dispatch_fp4_kernel, static_cast<unsigned>(grid), kFp4DispatchWarps * 32, smem, stream, a);
 }
