@@ -669,7 +669,8 @@ moe_status moe_expert_product_fp4(int32_t E, int32_t N, int32_t K, int32_t gated
         return MOE_ERR_INVALID_ARG;
     if (plan_ints < plan_tiles_at(E)) return MOE_ERR_INVALID_ARG;
     if (arena_rows == 0) return MOE_OK;
-    return from_cuda(launch_product(E, N, K, gated, wq, wsf, xq, xsf, arena_rows, plan, plan_ints, y, y_row_stride, err,
+    return from_cuda(launch_product(E, N, K, gated, wq, wsf, xq, xsf, arena_rows, plan, plan_ints, y, y_row_stride, nullptr,
+                                    nullptr, err,
                                     static_cast<cudaStream_t>(stream)));
 }
 

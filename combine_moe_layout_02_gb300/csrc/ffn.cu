@@ -1,8 +1,8 @@
 // ffn.cu -- moe_expert_ffn_fp4: the whole expert layer in one call. Routing
-// (expert.cu), the packing dispatch (fp4.cu), gate and up product with SwiGLU
-// (product.cu), packing of the inner rows, down product, weighted reduction
-// (combine.cu): seven launches (six for a batch of one routing chunk), each
-// overlapping the start of the next.
+// (expert.cu), the packing dispatch (fp4.cu), gate and up product with SwiGLU and
+// packing (product.cu), down product, weighted reduction (combine.cu): six
+// launches (five for a batch of one routing chunk), each overlapping the start
+// of the next.
 //
 // The call emulates no ranks: all experts' rows are one partition, which is
 // why the rank tables of moe_layout and moe_notify are not needed.
@@ -22,7 +22,7 @@ struct FfnBuffers {
     int64_t* base;
     void* scratch;
     uint8_t *xq, *xsf, *hq, *hsf;
-    uint16_t *h, *y;
+    uint16_t* y;
     int64_t rows, plan_ints, total;
 };
 
@@ -46,7 +46,6 @@ FfnBuffers carve(const moe_shape& s, int32_t inner, unsigned char* base) {
     b.xsf = static_cast<uint8_t*>(take(moe_fp4_scale_bytes(b.rows, s.H)));
     b.hq = static_cast<uint8_t*>(take(b.rows * (inner / 2)));
     b.hsf = static_cast<uint8_t*>(take(moe_fp4_scale_bytes(b.rows, inner)));
-    b.h = static_cast<uint16_t*>(take(b.rows * inner * 2));
     b.y = static_cast<uint16_t*>(take(b.rows * s.H * 2));
     b.total = off;
     return b;
@@ -95,7 +94,6 @@ moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint1
     FfnBuffers b = carve(s, inner, static_cast<unsigned char*>(workspace));
     if (workspace_bytes < b.total) return MOE_ERR_INVALID_ARG;
     if (s.S == 0) return MOE_OK;
-    if (h) b.h = h;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     moe_shape one = s;  // one partition
     one.P = 1;
@@ -103,15 +101,17 @@ moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint1
     if (e == cudaSuccess)
         e = launch_dispatch_fp4(one, x, topk_idx, topk_weights, b.slot_row, b.base, b.xq, b.xsf, b.rows, nullptr, nullptr,
                                 err, cs);
+    // The inner rows are packed as they come out of the first product; a caller
+    // that wants them in bf16 too has them written and packed by another launch.
     if (e == cudaSuccess)
-        e = launch_product(s.E, 2 * inner, s.H, 1, w1q, w1sf, b.xq, b.xsf, b.rows, b.plan, b.plan_ints, b.h,
-                           2 * static_cast<int64_t>(inner), err, cs);
-    if (e == cudaSuccess)
-        e = launch_fp4_pack(false, 1, b.rows, inner, 0, b.h, 2 * static_cast<int64_t>(inner), b.hq, b.hsf, b.plan, s.E,
+        e = launch_product(s.E, 2 * inner, s.H, 1, w1q, w1sf, b.xq, b.xsf, b.rows, b.plan, b.plan_ints, h,
+                           2 * static_cast<int64_t>(inner), h ? nullptr : b.hq, h ? nullptr : b.hsf, err, cs);
+    if (h && e == cudaSuccess)
+        e = launch_fp4_pack(false, 1, b.rows, inner, 0, h, 2 * static_cast<int64_t>(inner), b.hq, b.hsf, b.plan, s.E,
                             b.plan_ints, cs);
     if (e == cudaSuccess)
         e = launch_product(s.E, s.H, inner, 0, w2q, w2sf, b.hq, b.hsf, b.rows, b.plan, b.plan_ints, b.y,
-                           2 * static_cast<int64_t>(s.H), err, cs);
+                           2 * static_cast<int64_t>(s.H), nullptr, nullptr, err, cs);
     if (e == cudaSuccess) {
         CombineArgs c{};
         c.P = 1;

@@ -337,7 +337,8 @@ cudaError_t launch_dispatch_fp4(const moe_shape& s, const uint16_t* x, const int
                                 cudaStream_t stream);
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
-                           uint16_t* y, int64_t y_stride, int32_t* err, cudaStream_t stream);
+                           uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err,
+                           cudaStream_t stream);  // hq, hsf: packed gated rows instead of y
 
 int64_t notify_expert_scratch_bytes(const moe_shape& s);
 cudaError_t launch_notify_expert(const moe_shape& s, const int32_t* topk_idx, const int32_t* nrtpe,

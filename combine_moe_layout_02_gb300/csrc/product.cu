@@ -47,7 +47,9 @@ constexpr uint32_t kScaleBox = 2 * kFp4ChunkBytes;  // 128 rows' scales of a sta
 constexpr uint32_t kOffX = kWBytes, kOffWS = kOffX + kXBytes, kOffXS = kOffWS + kScaleBox;
 constexpr uint32_t kStageBytes = kOffXS + 2 * kScaleBox;  // a multiple of 1024
 constexpr uint32_t kOutStride = 80;          // bytes per staged row: 64 and a shift of 4 banks per row
+constexpr uint32_t kPackStride = 144;         // staged inner row of a CTA before packing: 128 bytes, shifted likewise
 constexpr uint32_t kOutBytes = kEpiWarps * 16 * kOutStride;
+static_assert(2 * 32 * kPackStride <= kOutBytes, "staging");
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes;
 constexpr int kAcc1 = 224;                   // second place of the sums
@@ -59,8 +61,13 @@ struct ProductArgs {
     const int32_t* plan;
     uint16_t* y;
     int64_t y_stride;
+    uint8_t* hq;   // kPacked: the inner rows as MXFP4
+    uint8_t* hsf;
     int32_t* err;
 };
+
+// What becomes of the sums: bf16; silu(gate) * up in bf16; that, packed to MXFP4.
+enum ProductMode { kPlain = 0, kGated = 1, kPacked = 2 };
 
 // Barriers of a CTA, and its abort flag.
 struct Bars {
@@ -230,7 +237,74 @@ __device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t
     return o;
 }
 
-template <int PAIRS>
+// kPacked: silu(gate) * up of the CTA's 64 inner columns for the tile's rows,
+// rounded to bf16 and then packed as moe_fp4_pack packs it. A block of 32 inner
+// columns comes out of two warps, so four warps stage 32 rows in shared memory
+// and 64 of their threads take a block each. `group`: which of every two
+// batches of 32 rows; its four warps meet at barrier 1 + group.
+__device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& t, uint32_t rank, uint32_t acc, int w,
+                                              int lane, int group, bool place, unsigned char* stage, Bars* bars,
+                                              uint32_t lead, uint64_t* acc_empty) {
+    const int inner = a.N / 2, h0 = t.m0 / 2 + static_cast<int>(rank) * 64;  // the CTA's first inner column
+    const int batches = static_cast<int>(mma_n(t.n) / 32);
+    const int64_t chunks = ceil_div(inner, kFp4Chunk);
+    const uint32_t to = smem_addr(stage) + ((lane & 7) + 8 * (lane >> 4)) * kPackStride + w * 32 + ((lane >> 3) & 1) * 16;
+    const int id = w * 32 + lane;  // of the group's 128 threads
+    for (int q = group; q < batches; q += 2) {
+        const int c = place ? q : batches - 1 - q;
+        uint32_t v[2][2][8];  // two halves of 16 columns, gate and up
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            tmem_load(acc + 32 * c + 16 * b, v[b][0]);
+            tmem_load(acc + 32 * c + 16 * b + (16u << 16), v[b][1]);
+        }
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (q == group) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
+            if (q + 2 >= batches) mbar_arrive_cluster(cluster_map(acc_empty, lead));
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // column block i / 2, inner columns 8 (i % 2) + lane / 4
+                h[i] = bf16_pair(gate_times_up(__uint_as_float(v[b][0][2 * i]), __uint_as_float(v[b][1][2 * i])),
+                                 gate_times_up(__uint_as_float(v[b][0][2 * i + 1]), __uint_as_float(v[b][1][2 * i + 1])));
+            store_turned(to + 16 * b * kPackStride, h[0], h[1], h[2], h[3]);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+        const int r = id >> 1, block = h0 / 32 + (id & 1);
+        if (id < 64 && 32 * c + r < t.n && block < 4 * chunks) {
+            const int64_t row = t.row + 32 * c + r;
+            uint32_t s = 0;  // scales past the width are 0
+            if (block < inner / 32) {
+                const uint4* src = reinterpret_cast<const uint4*>(stage + r * kPackStride + (id & 1) * 64);
+                uint4 x[4];
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = src[i];
+                    m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+                }
+                s = fp4_scale_code(max(m2 & 0xffffu, m2 >> 16));
+                const float inv = fp4_inverse(s);
+                *reinterpret_cast<uint4*>(a.hq + row * (inner / 2) + block * 16) =
+                    make_uint4(fp4_codes8(x[0], inv), fp4_codes8(x[1], inv), fp4_codes8(x[2], inv), fp4_codes8(x[3], inv));
+            }
+            a.hsf[((row / kFp4Tile) * chunks + block / 4) * kFp4ChunkBytes + fp4_word_at(static_cast<int>(row % kFp4Tile)) +
+                  (block & 3)] = static_cast<uint8_t>(s);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");  // the staged rows have been read
+    }
+    if (group >= batches && lane == 0) {  // nothing of this tile is this group's
+        mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
+        mbar_arrive_cluster(cluster_map(acc_empty, lead));
+    }
+}
+
+template <int PAIRS, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wsmap,
                const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xsmap) {
@@ -408,6 +482,12 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             tc_fence_after();
             const int m = t.m0 + static_cast<int>(rank) * 128 + w * 32;  // the warp's weight rows
             const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
+            if constexpr (MODE == kPacked) {
+                pack_tile_out(a, t, rank, acc, w, lane, half, place != 0, out_stage + half * 32 * kPackStride, bars, lead,
+                              &bars->acc_empty[place]);
+                ++i;
+                continue;
+            }
             const int chunks = static_cast<int>(mma_n(t.n) / 16);  // even: as many for either half
             // Place 0 has the shared columns at its end, place 1 at its start:
             // they are read first.
@@ -425,8 +505,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                 }
                 const int c0 = 16 * c;  // first of the chunk's rows
                 if (m >= a.N || c0 >= t.n) continue;
-                uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + (t.row + c0) * a.y_stride + (a.gated ? m : 2 * m);
-                if (a.gated) {
+                uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + (t.row + c0) * a.y_stride + (MODE == kGated ? m : 2 * m);
+                if constexpr (MODE == kGated) {
                     uint32_t h[4];
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
@@ -504,7 +584,7 @@ bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuui
 }
 
 // Clusters that can be resident at once on the current device (cached).
-template <int PAIRS>
+template <int PAIRS, int MODE>
 int resident_clusters() {
     static std::atomic<int> cache[64];
     int dev = 0;
@@ -523,29 +603,29 @@ int resident_clusters() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<PAIRS>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<PAIRS, MODE>, &cfg) != cudaSuccess || n < 1) return -1;
     if (slot) cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
-template <int PAIRS>
+template <int PAIRS, int MODE>
 cudaError_t launch_pairs(const ProductArgs& a, const CUtensorMap& wmap, const CUtensorMap& wsmap, const CUtensorMap& xmap,
                          const CUtensorMap& xsmap, cudaStream_t stream) {
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel<PAIRS>), kSmem, kThreads, nullptr);
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel<PAIRS, MODE>), kSmem, kThreads, nullptr);
     if (e != cudaSuccess) return e;
-    const int clusters = resident_clusters<PAIRS>();
+    const int clusters = resident_clusters<PAIRS, MODE>();
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     const int64_t most = a.tile_cap * ceil_div(a.N, kMTile * PAIRS);
     const unsigned grid = 2u * PAIRS * static_cast<unsigned>(most < clusters ? most : clusters);
-    return launch_pdl_cluster(product_kernel<PAIRS>, grid, kThreads, kSmem, 2u * PAIRS, stream, a, wmap, wsmap, xmap, xsmap);
+    return launch_pdl_cluster(product_kernel<PAIRS, MODE>, grid, kThreads, kSmem, 2u * PAIRS, stream, a, wmap, wsmap, xmap, xsmap);
 }
 
 }  // namespace
 
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
-                           uint16_t* y, int64_t y_stride, int32_t* err, cudaStream_t stream) {
-    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, err};
+                           uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
+    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err};
     if (a.tile_cap == 0) return cudaSuccess;
     if (encoder() == nullptr) return cudaErrorNotSupported;
     const cuuint64_t kb = static_cast<cuuint64_t>(K) / 2, chunks = static_cast<cuuint64_t>(ceil_div(K, kFp4Chunk));
@@ -571,8 +651,11 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
-    if (N > kMTile && per_expert >= MOE_PRODUCT_QUAD_ROWS) return launch_pairs<2>(a, wmap, wsmap, xmap, xsmap, stream);
-    return launch_pairs<1>(a, wmap, wsmap, xmap, xsmap, stream);
+    const bool two = N > kMTile && per_expert >= MOE_PRODUCT_QUAD_ROWS;
+    const auto launch = hq ? (two ? launch_pairs<2, kPacked> : launch_pairs<1, kPacked>)
+                           : gated ? (two ? launch_pairs<2, kGated> : launch_pairs<1, kGated>)
+                                   : (two ? launch_pairs<2, kPlain> : launch_pairs<1, kPlain>);
+    return launch(a, wmap, wsmap, xmap, xsmap, stream);
 }
 
 }  // namespace moe
