@@ -224,11 +224,20 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
 }
 
 // Unit u of the launch (the same in every lane), or none (n = 0) where the plan's tile is no tile of this arena.
+// Where experts have many rows (two pairs to a cluster) units run through groups
+// of four row tiles, the tiles of a group innermost: the clusters at work at one
+// time then read the same weights, of an expert or two, and the same few rows.
+// 262144 rows at the power cap: 2.55 ms; with one tile's units side by side 2.83,
+// groups of 2, 3, 8 and 12 tiles 2.67, 2.73, 2.62, 2.75. With few rows an expert is
+// one tile: its units side by side (4096 tokens' layer 1.200 ms, in fours 1.213).
 template <int PAIRS>
-__device__ __forceinline__ Unit unit_of(const ProductArgs& a, int64_t u, int64_t mtiles) {
-    const int64_t t = u / mtiles;
+__device__ __forceinline__ Unit unit_of(const ProductArgs& a, uint32_t u, uint32_t mtiles, uint32_t tiles) {
+    constexpr int kGroup = PAIRS == 2 ? 4 : 1;
+    const uint32_t group = u / (mtiles * kGroup), in = u - group * mtiles * kGroup;
+    const uint32_t size = min(static_cast<uint32_t>(kGroup), tiles - group * kGroup);
+    const uint32_t m = in / size, t = group * kGroup + in - m * size;
     const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
-    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(u - t * mtiles) * (kMTile * PAIRS)};
+    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(m) * (kMTile * PAIRS)};
     if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
         o.row + static_cast<int64_t>(o.n) > a.rows) {
         raise_error(a.err, MOE_ERR_CAPACITY);
@@ -346,11 +355,11 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     const uint32_t tmem = bars->tmem;
     pdl_wait_then_release();
 
-    int32_t tiles = __ldg(a.plan);
-    tiles = tiles < 0 ? 0 : (tiles > a.tile_cap ? a.tile_cap : tiles);
-    const int64_t mtiles = ceil_div(a.N, kMTile * PAIRS);
-    const int64_t units = uniform(tiles) * mtiles;
-    const int64_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
+    const int32_t planned = uniform(__ldg(a.plan));
+    const uint32_t tiles = planned < 0 ? 0 : (planned > a.tile_cap ? a.tile_cap : planned);
+    const uint32_t mtiles = (a.N + kMTile * PAIRS - 1) / (kMTile * PAIRS);
+    const uint32_t units = tiles * mtiles;  // the launch has checked that it fits, with a step to spare
+    const uint32_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
 
     if (warp == 0) {
@@ -358,8 +367,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
         bool ok = true;
-        for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles);
+        for (uint32_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n);
             const int boxes = static_cast<int>((n / 2 + 31) / 32);
@@ -409,8 +418,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
         uint32_t last_n = 0;
         bool ok = true;
-        for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles);
+        for (uint32_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n), place = i & 1;
             const uint32_t acc = tmem + (place ? kAcc1 : 0);
@@ -473,8 +482,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
         bool ok = true;
-        for (int64_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles);
+        for (uint32_t u = first; ok && u < units; u += step) {
+            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
             ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
@@ -627,6 +636,10 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
     ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err};
     if (a.tile_cap == 0) return cudaSuccess;
+    // Units and one step past them are counted in 32 bits; what a plan of this arena can hold is far below.
+    const int64_t most_tiles = rows / kFp4Tile + 1, room = (int64_t{1} << 31) / ceil_div(N, kMTile);
+    if (a.tile_cap > most_tiles) a.tile_cap = static_cast<int32_t>(most_tiles);
+    if (a.tile_cap > room) return cudaErrorInvalidValue;
     if (encoder() == nullptr) return cudaErrorNotSupported;
     const cuuint64_t kb = static_cast<cuuint64_t>(K) / 2, chunks = static_cast<cuuint64_t>(ceil_div(K, kFp4Chunk));
     const cuuint64_t wt = static_cast<cuuint64_t>(ceil_div(N, kFp4Tile));
