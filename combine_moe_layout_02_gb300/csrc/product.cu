@@ -636,6 +636,8 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
     ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err};
     if (a.tile_cap == 0) return cudaSuccess;
+    // Average rows per expert: a plan has one tile per expert and one per 256 rows.
+    const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
     // Units and one step past them are counted in 32 bits; what a plan of this arena can hold is far below.
     const int64_t most_tiles = rows / kFp4Tile + 1, room = (int64_t{1} << 31) / ceil_div(N, kMTile);
     if (a.tile_cap > most_tiles) a.tile_cap = static_cast<int32_t>(most_tiles);
@@ -663,7 +665,6 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         const cuuint32_t box[3] = {kFp4ChunkBytes / 4, 2, 1};
         if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
     const bool two = N > kMTile && per_expert >= MOE_PRODUCT_QUAD_ROWS;
     const auto launch = hq ? (two ? launch_pairs<2, kPacked> : launch_pairs<1, kPacked>)
                            : gated ? (two ? launch_pairs<2, kGated> : launch_pairs<1, kGated>)
