@@ -330,8 +330,11 @@ def moe_fp4_scale_bytes(rows: int, width: int) -> int:
     return int(lib().moe_fp4_scale_bytes(int(rows), int(width)))
 
 
+_NO_PLAN = (0, None, 0)
+
+
 def _plan_args(E, plan):
-    return (int(E), _ptr(plan), int(plan.numel())) if plan is not None else (0, None, 0)
+    return _NO_PLAN if plan is None else (int(E), _ptr(plan), int(plan.numel()))
 
 
 def moe_fp4_pack(groups, rows, width, gated, x, x_row_stride, q, sf, E=0, plan=None, stream=None):
@@ -421,19 +424,25 @@ class Fp4Rows:
         self.q = torch.empty((self.groups * self.rows, self.width // 2), dtype=torch.uint8, device=device)
         self.sf = torch.empty((self.groups * nbytes,), dtype=torch.uint8, device=device)
 
-        self._sizes = (self.groups, self.rows, self.width, int(self.gated))
-        self._q, self._sf = _ptr(self.q), _ptr(self.sf)
+        # What the calls take of this operand, once: a small call's time is its host time.
+        sizes, ptrs = (self.groups, self.rows, self.width, int(self.gated)), (_ptr(self.q), _ptr(self.sf))
+        self._pack_args, self._unpack_args = (sizes, (2 * self.width, *ptrs)), (*sizes, *ptrs)
+        self._lib = lib()
 
     def pack(self, x, E=0, plan=None, stream=None):
         """bf16 rows x [groups * rows, width] into this operand."""
-        _check(lib().moe_fp4_pack(*self._sizes, _ptr(x), 2 * self.width, self._q, self._sf, *_plan_args(E, plan),
-                                  _stream(stream)), "moe_fp4_pack")
+        head, tail = self._pack_args
+        st = self._lib.moe_fp4_pack(*head, _ptr(x), *tail, *_plan_args(E, plan), _stream(stream))
+        if st:
+            raise MoeError(st, "moe_fp4_pack")
         return self
 
     def unpack(self, out, E=0, plan=None, stream=None):
         """The bf16 values of this operand into out [groups * rows, width]."""
-        _check(lib().moe_fp4_unpack(*self._sizes, self._q, self._sf, _ptr(out), 2 * self.width, *_plan_args(E, plan),
-                                    _stream(stream)), "moe_fp4_unpack")
+        st = self._lib.moe_fp4_unpack(*self._unpack_args, _ptr(out), 2 * self.width, *_plan_args(E, plan),
+                                      _stream(stream))
+        if st:
+            raise MoeError(st, "moe_fp4_unpack")
         return out
 
 
