@@ -371,6 +371,8 @@ int device_sm_count();
 int device_optin_smem();
 // Shared memory of one SM (all its CTAs together), per current device.
 int device_sm_smem();
+// L2 cache of the current device, in bytes (cached).
+int device_l2_bytes();
 // Allow `fn` `smem` bytes of dynamic shared memory on the current device and,
 // if per_sm is given, return its resident blocks per SM for (threads, smem).
 // Both are cached per (kernel, device).
