@@ -266,18 +266,19 @@ expert_rows_kernel(int32_t P, int32_t E, int32_t K, int64_t S, int64_t chunks, i
                 cbase[e] = before;
                 total[e] = sum;
             }
-    } else
-    for (int e = tid; e < E; e += blockDim.x) {
-        int32_t acc = __ldg(reo + e);
-        const int32_t* row = ecount + static_cast<int64_t>(e) * chunks_pad;
-        int64_t c = 0;
+    } else {
+        for (int e = tid; e < E; e += blockDim.x) {
+            int32_t acc = __ldg(reo + e);
+            const int32_t* row = ecount + static_cast<int64_t>(e) * chunks_pad;
+            int64_t c = 0;
 #pragma unroll 16
-        for (; c + 4 <= chunk; c += 4) {
-            const int4 v = __ldg(reinterpret_cast<const int4*>(row + c));
-            acc += v.x + v.y + v.z + v.w;
+            for (; c + 4 <= chunk; c += 4) {
+                const int4 v = __ldg(reinterpret_cast<const int4*>(row + c));
+                acc += v.x + v.y + v.z + v.w;
+            }
+            for (; c < chunk; ++c) acc += __ldg(row + c);
+            cbase[e] = acc;
         }
-        for (; c < chunk; ++c) acc += __ldg(row + c);
-        cbase[e] = acc;
     }
     MOE_STAMP(1);
     for (int i = tid; i < nwarps * E; i += blockDim.x) {

@@ -21,6 +21,13 @@
 // 0 and 224 on, so that a tile's sums are written while the next tile's are
 // formed; two places of 256 columns and the scales' 24 would not fit the 512,
 // so the places share 32 columns, which are read first and given back early.
+//
+// Bound by the weights' bytes while experts have few rows (64 tokens over 256
+// experts of 7168 -> 4096: 506 us, 6.9 TB/s), by power and the SMs' intake when they
+// have many: 256 x 256 x 64 takes the pair 128 cycles, a stage 512, and brings
+// each SM 35 KB, 560 cycles at its 64 bytes per cycle (262144 rows: 2.65 ms, 5.8
+// PFLOP/s at 1.6 GHz). A pair is the smallest tile that keeps the intake near the
+// tensor pipe's pace; 256 columns are the widest instruction.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -556,7 +563,10 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         }
     }
 
-    // Neither CTA may leave while the other's copies, products or arrivals can reach it.
+    // After a failed wait: loads that nobody waits for land before the cluster ends.
+    if (*reinterpret_cast<volatile uint32_t*>(&bars->abort) != 0u)
+        for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    // No CTA may leave while another's copies, products or arrivals can reach it.
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
