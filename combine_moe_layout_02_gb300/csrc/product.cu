@@ -60,6 +60,7 @@ static_assert(2 * 32 * kPackStride <= kOutBytes, "staging");
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes;
 constexpr int kAcc1 = 224;                   // second place of the sums
+constexpr long long kWaitCycles = 1ll << 32;
 constexpr int kScaleCol = 480;               // scales of a stage: 8 columns of the weights', 16 of the rows'
 
 struct ProductArgs {
@@ -112,15 +113,28 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return done != 0;
 }
 
-// Bounded wait of a whole warp; false if it ran out or another role of the CTA gave up.
+// Bounded wait of a whole warp, by polls and by time (about two seconds: a poll
+// may itself sleep); false if it ran out or another role of the CTA gave up.
 __device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, int32_t* err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    const long long began = clock64();
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
         if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&b->abort) != 0u)) return false;
+        if (__any_sync(0xffffffffu, clock64() - began > kWaitCycles)) break;
     }
     *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
     raise_error(err, MOE_ERR_DEVICE_TIMEOUT);
     return false;
+}
+
+// After a failed wait: what is in flight ends within microseconds, or (a peer
+// gave up first) never.
+__device__ __forceinline__ void drained(uint64_t* bar, uint32_t parity) {
+    const long long began = clock64();
+    while (!__any_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity)) &&
+           !__any_sync(0xffffffffu, clock64() - began > kWaitCycles / 64)) {
+    }
 }
 
 // One lane of a converged warp. The loading and the issuing warp run their
@@ -417,7 +431,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             for (int i = 0; i < kStages && i < issued; ++i) {
                 s = s == 0 ? kStages - 1 : s - 1;
                 if (s == kStages - 1) phase ^= 1;
-                mbar_wait(&bars->full[s], phase);
+                drained(&bars->full[s], phase);
             }
         }
         __syncwarp();
@@ -476,7 +490,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                                  smem_addr(&bars->drain))
                              : "memory");
-            mbar_wait(&bars->drain, 0);
+            drained(&bars->drain, 0);
         }
         __syncwarp();
     } else if (warp >= 4) {
