@@ -252,9 +252,9 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
 // Where experts have many rows (two pairs to a cluster) units run through groups
 // of four row tiles, the tiles of a group innermost: the clusters at work at one
 // time then read the same weights, of an expert or two, and the same few rows.
-// 262144 rows at the power cap: 2.55 ms; with one tile's units side by side 2.83,
-// groups of 2, 3, 8 and 12 tiles 2.67, 2.73, 2.62, 2.75. With few rows an expert is
-// one tile: its units side by side (4096 tokens' layer 1.200 ms, in fours 1.213).
+// 262144 rows at the power cap: 2.54 ms; with one tile's units side by side 2.70,
+// groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. With few rows an expert is one tile:
+// its units side by side.
 template <int PAIRS>
 __device__ __forceinline__ Unit unit_of(const ProductArgs& a, uint32_t u, uint32_t mtiles, uint32_t tiles) {
     constexpr int kGroup = PAIRS == 2 ? 4 : 1;
