@@ -25,8 +25,8 @@
 // Bound by the weights' bytes while experts have few rows (64 tokens over 256
 // experts of 7168 -> 4096: 506 us, 6.9 TB/s), by power and the SMs' intake when they
 // have many: 256 x 256 x 64 takes the pair 128 cycles, a stage 512, and brings
-// each SM 35 KB, 560 cycles at its 64 bytes per cycle (262144 rows: 2.65 ms, 5.8
-// PFLOP/s at 1.6 GHz). A pair is the smallest tile that keeps the intake near the
+// each SM 35 KB, 560 cycles at its 64 bytes per cycle (262144 rows: 2.5 ms, 6.1
+// PFLOP/s at 1.55 GHz; 2.1 ms in bursts). A pair is the smallest tile that keeps the intake near the
 // tensor pipe's pace; 256 columns are the widest instruction.
 #include <cuda.h>
 #include <cuda_bf16.h>
