@@ -274,7 +274,7 @@ __device__ __forceinline__ Unit unit_of(const ProductArgs& a, uint32_t u, uint32
 // kPacked: silu(gate) * up of the CTA's 64 inner columns for the tile's rows,
 // rounded to bf16 and then packed as moe_fp4_pack packs it. A block of 32 inner
 // columns comes out of two warps, so four warps stage 32 rows in shared memory
-// and 64 of their threads take a block each. `group`: which of every two
+// and each of their threads takes half a block. `group`: which of every two
 // batches of 32 rows; its four warps meet at barrier 1 + group.
 __device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& t, uint32_t rank, uint32_t acc, int w,
                                               int lane, int group, bool place, unsigned char* stage, Bars* bars,
@@ -309,26 +309,24 @@ __device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& 
             store_turned(to + 16 * b * kPackStride, h[0], h[1], h[2], h[3]);
         }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-        const int r = id >> 1, block = h0 / 32 + (id & 1);
-        if (id < 64 && 32 * c + r < t.n && block < 4 * chunks) {
+        const int r = id >> 2, part = id & 3, block = h0 / 32 + (part >> 1);  // 16 of the row's 64 columns
+        const bool in = block < inner / 32;
+        const uint4* src = reinterpret_cast<const uint4*>(stage + r * kPackStride + part * 32);
+        const uint4 x0 = src[0], x1 = src[1];
+        uint32_t m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(0u, x0.x), x0.y), x0.z), x0.w);
+        m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(m2, x1.x), x1.y), x1.z), x1.w);
+        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+        const uint32_t s = in ? fp4_scale_code(max(m2 & 0xffffu, m2 >> 16)) : 0u;  // scales past the width are 0
+        if (32 * c + r < t.n) {
             const int64_t row = t.row + 32 * c + r;
-            uint32_t s = 0;  // scales past the width are 0
-            if (block < inner / 32) {
-                const uint4* src = reinterpret_cast<const uint4*>(stage + r * kPackStride + (id & 1) * 64);
-                uint4 x[4];
-                uint32_t m2 = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = src[i];
-                    m2 = fp4_absmax(fp4_absmax(fp4_absmax(fp4_absmax(m2, x[i].x), x[i].y), x[i].z), x[i].w);
-                }
-                s = fp4_scale_code(max(m2 & 0xffffu, m2 >> 16));
+            if (in) {
                 const float inv = fp4_inverse(s);
-                *reinterpret_cast<uint4*>(a.hq + row * (inner / 2) + block * 16) =
-                    make_uint4(fp4_codes8(x[0], inv), fp4_codes8(x[1], inv), fp4_codes8(x[2], inv), fp4_codes8(x[3], inv));
+                *reinterpret_cast<uint2*>(a.hq + row * (inner / 2) + h0 / 2 + part * 8) =
+                    make_uint2(fp4_codes8(x0, inv), fp4_codes8(x1, inv));
             }
-            a.hsf[((row / kFp4Tile) * chunks + block / 4) * kFp4ChunkBytes + fp4_word_at(static_cast<int>(row % kFp4Tile)) +
-                  (block & 3)] = static_cast<uint8_t>(s);
+            if ((part & 1) == 0 && block < 4 * chunks)
+                a.hsf[((row / kFp4Tile) * chunks + block / 4) * kFp4ChunkBytes + fp4_word_at(static_cast<int>(row % kFp4Tile)) +
+                      (block & 3)] = static_cast<uint8_t>(s);
         }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");  // the staged rows have been read
     }
