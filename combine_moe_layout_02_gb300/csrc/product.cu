@@ -595,7 +595,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoder, looked up once per process.
+// The CUDA driver's encoder, looked up once per process.
 EncodeTiled encoder() {
     static const EncodeTiled fn = [] {
         void* p = nullptr;

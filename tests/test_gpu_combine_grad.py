@@ -201,3 +201,45 @@ def test_dispatch_gradient_is_the_unweighted_combine():
             want[g] += g64[row]
             mag[g] += np.abs(g64[row])
     assert (np.abs(got - want) <= 2.0 ** -8 * (np.abs(want) + mag * 2.0 ** -22) + w.K * 2.0 ** -24 * mag).all()
+
+
+@pytest.mark.parametrize("layout", ["expert", "rank"])
+def test_ids_that_name_no_expert_and_rows_that_are_nobodys(layout):
+    """Ids past the experts give weights' gradients of 0 and no row; NaN in rows of the arena that no slot has reaches nothing."""
+    import torch
+
+    w = inputs.make(4, 8, 20, 64, 3, seed=11, mask_frac=0.1, expert_alignment=8)
+    base, routes = _tables(w, layout)
+    dev = torch.device("cuda", 0)
+    idx = w.topk_idx.copy()
+    idx[2, 1], idx[7, 0] = w.E, 2 ** 31 - 1
+    total = int(base[-1])
+    kept = w.topk_idx
+    w.topk_idx = idx  # the tables are those of the valid ids; these two slots now name no expert
+    rows = _routes(w, layout, base, routes)
+    if layout == "rank":  # a rank's row stays with the slots that still name it
+        rows = [[(row, slots) for row, slots in r if slots] for r in rows]
+    used = {row for r in rows for row, _ in r}
+    rng = np.random.default_rng(2)
+    y = f32_to_bf16_bits_torch(rng.standard_normal((total, w.H)))
+    y[[r for r in range(total) if r not in used]] = 0x7FC0
+    dout = f32_to_bf16_bits_torch(rng.standard_normal((w.S, w.H)))
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    dy = torch.full((total, w.H), 0x5555, dtype=torch.int16, device=dev)
+    dw = torch.full((w.S, w.K), -7.0, dtype=torch.float32, device=dev)
+    err = torch.zeros(4, dtype=torch.int32, device=dev)
+    call = moe.moe_combine_expert_grad if layout == "expert" else moe.moe_combine_grad
+    call(moe.make_shape(w.P, w.E, w.S, w.K, w.H, expert_alignment=8), up(dout.view(np.int16)), up(y.view(np.int16)), 2 * w.H,
+         up(base), total, up(routes), up(idx), up(w.topk_weights), dy, 2 * w.H, dw, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    got = dy.cpu().numpy().view(np.uint16)
+    for r in range(total):
+        assert (got[r] == 0x5555).all() == (r not in used), r
+    g = dw.cpu().numpy()
+    assert np.isfinite(g).all() and g[2, 1] == 0 and g[7, 0] == 0 and (g[kept < 0] == 0).all()
+    d64, y64 = bf16_bits_to_f32(dout).astype(np.float64), bf16_bits_to_f32(y).astype(np.float64)
+    for t, r in enumerate(rows):
+        for row, slots in r:
+            terms = d64[t] * y64[row]
+            assert (np.abs(g[t, slots] - terms.sum()) <= w.H * 2.0 ** -24 * np.abs(terms).sum()).all()

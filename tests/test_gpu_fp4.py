@@ -537,3 +537,27 @@ def test_example_runs():
     assert m.serve() < 0.02
     dw, dx = m.train()
     assert dw < 0.01 and dx < 0.01
+
+
+def test_expert_ffn_with_an_expert_twice_in_a_token():
+    w = inputs.make(2, 8, 90, 64, 4, seed=4, expert_alignment=128)
+    w.topk_idx[:, 2] = w.topk_idx[:, 0]
+    w.topk_idx[::3] = 5  # one expert four times: more rows than tokens
+    a, b, err_a, err_b = _ffn_both_ways(w, 64, 32)
+    assert err_a == 0 and err_b == 0
+    np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("S", [0, 1])
+def test_expert_ffn_of_no_token_and_of_one(S):
+    torch, dev = _torch()
+    E, H, K, inner = 5, 64, 2, 32
+    w1 = moe.Fp4Rows(2 * inner, H, dev, groups=E, gated=True).pack(_up(_rows(E * 2 * inner, H, 1)))
+    w2 = moe.Fp4Rows(H, inner, dev, groups=E).pack(_up(_rows(E * H, inner, 2)))
+    buf = moe.Buffers(moe.make_shape(1, E, S, K, H), dev, arena_rows=0, side_arrays=False)
+    x = _up(_rows(max(S, 1), H, 3))[:S].contiguous()
+    idx = torch.full((S, K), -1, dtype=torch.int32, device=dev)  # the one token reaches no expert: its result is 0
+    out = torch.full((S, H), 0x5555, dtype=torch.int16, device=dev)
+    buf.expert_ffn_fp4(x, idx, None, w1.q.view(E, -1, H // 2), w1.sf, w2.q.view(E, -1, inner // 2), w2.sf, out)
+    torch.cuda.synchronize()
+    assert int(buf.err[0]) == 0 and not out.any()
