@@ -11,7 +11,6 @@
 
 #include "fp4.cuh"
 #include "moe.h"
-#include "moe_device.cuh"
 
 namespace moe {
 namespace {

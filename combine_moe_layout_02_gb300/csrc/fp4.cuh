@@ -20,7 +20,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "moe_device.cuh"
+#include "experts.cuh"
 
 namespace moe {
 
