@@ -177,11 +177,14 @@ cudaError_t launch_pack_t(const PackArgs& a, int64_t units_max, cudaStream_t str
 }
 
 // ---------------------------------------------------------------------------
-// The experts' row tiles: one CTA. Counts are summed over the source ranks
-// (threads side by side on the experts, the ranks split over the thread groups
-// that are left), then first rows and tile numbers are exclusive scans.
+// The experts' row tiles: one CTA, a thread per expert (several from 1024 on).
+// Counts are summed over the source ranks, by the expert's thread where ranks
+// are few, else by threads side by side on the experts with the ranks split over
+// the thread groups that are left; then first rows and tile numbers are exclusive
+// scans. Latency-bound.
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanFewRanks = 32;
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_t* __restrict__ ntpe,
@@ -192,22 +195,34 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
     __shared__ int64_t row_part[32];
     __shared__ int32_t tile_part[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < E; e += kPlanThreads) counts[e] = 0;
-    __syncthreads();
-    const int lanes_e = E < kPlanThreads ? E : kPlanThreads;
-    const int parts = kPlanThreads / lanes_e;
-    const int part = tid / lanes_e;
-    if (part < parts) {
-        for (int e = tid % lanes_e; e < E; e += lanes_e) {
+    const int threads = blockDim.x;
+    // Thread t scans experts [t * per, (t + 1) * per).
+    const int per = (E + threads - 1) / threads;
+    if (P <= kPlanFewRanks) {
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e >= E) break;
             int32_t sum = 0;
 #pragma unroll 8
-            for (int s = part; s < P; s += parts) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
-            atomicAdd(counts + e, sum);  // integers: any order gives the same sum
+            for (int s = 0; s < P; ++s) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
+            counts[e] = sum;  // read by this thread only
         }
+    } else {
+        for (int e = tid; e < E; e += threads) counts[e] = 0;
+        __syncthreads();
+        const int lanes_e = E < threads ? E : threads;
+        const int parts = threads / lanes_e;
+        const int part = tid / lanes_e;
+        if (part < parts) {
+            for (int e = tid % lanes_e; e < E; e += lanes_e) {
+                int32_t sum = 0;
+#pragma unroll 8
+                for (int s = part; s < P; s += parts) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
+                atomicAdd(counts + e, sum);  // integers: any order gives the same sum
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    // Thread t scans experts [t * per, (t + 1) * per).
-    const int per = (E + kPlanThreads - 1) / kPlanThreads;
     int64_t rows = 0;
     int32_t tiles = 0;
     bool bad = false;
@@ -239,8 +254,8 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
     }
     __syncthreads();
     if (warp == 0) {
-        int64_t r = row_part[lane];
-        int32_t t = tile_part[lane];
+        int64_t r = lane < threads / 32 ? row_part[lane] : 0;
+        int32_t t = lane < threads / 32 ? tile_part[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t ru = __shfl_up_sync(0xffffffffu, r, o);
@@ -447,7 +462,8 @@ cudaError_t launch_expert_plan(const moe_shape& s, const int32_t* ntpe, int32_t*
     const size_t smem = static_cast<size_t>(s.E) * 4;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(plan_kernel), smem, kPlanThreads, nullptr);
     if (e != cudaSuccess) return e;
-    return launch_pdl(plan_kernel, 1u, kPlanThreads, smem, stream, s.P, s.E, s.expert_alignment,
+    const int64_t threads = s.P <= kPlanFewRanks && s.E < kPlanThreads ? round_up(s.E, 32) : kPlanThreads;
+    return launch_pdl(plan_kernel, 1u, static_cast<unsigned>(threads), smem, stream, s.P, s.E, s.expert_alignment,
                       static_cast<int64_t>(s.S) * s.K, ntpe, plan, plan_capacity(s.E, plan_ints), err);
 }
 
