@@ -35,10 +35,6 @@
 
 #include "fp4.cuh"
 
-#ifndef MOE_PRODUCT_QUAD_ROWS
-#define MOE_PRODUCT_QUAD_ROWS 256
-#endif
-
 namespace moe {
 namespace {
 
@@ -249,12 +245,13 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
 }
 
 // Unit u of the launch (the same in every lane), or none (n = 0) where the plan's tile is no tile of this arena.
-// Where experts have many rows (two pairs to a cluster) units run through groups
-// of four row tiles, the tiles of a group innermost: the clusters at work at one
-// time then read the same weights, of an expert or two, and the same few rows.
+// In clusters of two pairs units run through groups of four row tiles, the tiles
+// of a group innermost: the clusters at work at one time then read the same
+// weights, of an expert or two, and the same few rows.
 // 262144 rows at the power cap: 2.54 ms; with one tile's units side by side 2.70,
-// groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. With few rows an expert is one tile:
-// its units side by side.
+// groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. Single pairs are faster with one
+// tile's units side by side (9600 rows over 32 experts, 7168 -> 2048: 70 us against
+// 74 in fours).
 template <int PAIRS>
 __device__ __forceinline__ Unit unit_of(const ProductArgs& a, uint32_t u, uint32_t mtiles, uint32_t tiles) {
     constexpr int kGroup = PAIRS == 2 ? 4 : 1;
@@ -655,6 +652,25 @@ cudaError_t launch_pairs(const ProductArgs& a, const CUtensorMap& wmap, const CU
     return launch_pdl_cluster(product_kernel<PAIRS, MODE>, grid, kThreads, kSmem, 2u * PAIRS, stream, a, wmap, wsmap, xmap, xsmap);
 }
 
+// Average rows per expert from which several row tiles share an expert's weights.
+constexpr int64_t kManyRows = 256;
+
+// Whether clusters are of two pairs, which fetch the rows once for both, or of
+// one. One is faster while the SMs' own pace counts: it leaves no SM out (clusters
+// of four CTAs fit 144 of 152) and no pair idle at an odd number of weight tiles
+// (32 experts, 44800 rows 7168 -> 1280: 140 us against 156; 9600 rows 2048 -> 2048: 33
+// and 36). Two are faster where loads count: in calls long enough for the power
+// limit (262144 rows, 7168 -> 4096: 2.52 ms against 2.62), and where rows of codes
+// are no multiple of 128 bytes, so that each 128-byte load touches two lines of L2
+// (44800 rows 5984 -> 2048: 208 us against 244; 9600 rows 4128 -> 2048: 58 each, 2080
+// -> 2048: 41 and 38).
+bool two_pairs(double rows, int32_t N, int32_t K) {
+    const int64_t wtiles = ceil_div(N, kMTile);
+    const double flops = 2.0 * rows * N * K;
+    if (K % kStageK != 0) return wtiles >= 4 && flops >= 1.5e11;
+    return wtiles % 2 == 0 && flops >= 4e12;
+}
+
 }  // namespace
 
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
@@ -691,7 +707,7 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         const cuuint32_t box[3] = {kFp4ChunkBytes / 4, 2, 1};
         if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const bool two = N > kMTile && per_expert >= MOE_PRODUCT_QUAD_ROWS;
+    const bool two = per_expert >= kManyRows && two_pairs(static_cast<double>(per_expert) * E, N, K);
     const auto launch = hq ? (two ? launch_pairs<2, kPacked> : launch_pairs<1, kPacked>)
                            : gated ? (two ? launch_pairs<2, kGated> : launch_pairs<1, kGated>)
                                    : (two ? launch_pairs<2, kPlain> : launch_pairs<1, kPlain>);
