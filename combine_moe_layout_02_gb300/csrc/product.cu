@@ -244,29 +244,67 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
     return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
 }
 
-// Unit u of the launch (the same in every lane), or none (n = 0) where the plan's tile is no tile of this arena.
-// In clusters of two pairs units run through groups of four row tiles, the tiles
-// of a group innermost: the clusters at work at one time then read the same
-// weights, of an expert or two, and the same few rows.
-// 262144 rows at the power cap: 2.54 ms; with one tile's units side by side 2.70,
-// groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. Single pairs are faster with one
-// tile's units side by side (9600 rows over 32 experts, 7168 -> 2048: 70 us against
-// 74 in fours).
+// A cluster's units, first, first + step, .. of the launch's. In clusters of two
+// pairs units run through groups of four row tiles, the tiles of a group innermost:
+// the clusters at work at one time then read the same weights, of an expert or two,
+// and the same few rows. 262144 rows at the power cap: 2.54 ms; with one tile's
+// units side by side 2.70, groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. Single pairs
+// are faster with one tile's units side by side (9600 rows over 32 experts, 7168 ->
+// 2048: 70 us against 74 in fours).
+//
+// A role steps from unit to unit without a division and holds the next one's plan
+// words while it works on the current one. A unit of few stages is short of the time
+// to find the next: 256 experts of a row or so, 512 -> 7008, 62 us against 67 with
+// each unit found from its number; at width 256 50 against 51. A unit of a stage
+// pays for the step instead (64 experts, 96 -> 4096 gated, 24 us against 23), and
+// from width 1024 on the two are within 2%.
 template <int PAIRS>
-__device__ __forceinline__ Unit unit_of(const ProductArgs& a, uint32_t u, uint32_t mtiles, uint32_t tiles) {
-    constexpr int kGroup = PAIRS == 2 ? 4 : 1;
-    const uint32_t group = u / (mtiles * kGroup), in = u - group * mtiles * kGroup;
-    const uint32_t size = min(static_cast<uint32_t>(kGroup), tiles - group * kGroup);
-    const uint32_t m = in / size, t = group * kGroup + in - m * size;
-    const int4 p = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
-    Unit o{uniform(p.x), uniform(p.y), uniform(p.z), static_cast<int32_t>(m) * (kMTile * PAIRS)};
-    if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
-        o.row + static_cast<int64_t>(o.n) > a.rows) {
-        raise_error(a.err, MOE_ERR_CAPACITY);
-        o.n = 0;
+struct Units {
+    static constexpr uint32_t kGroup = PAIRS == 2 ? 4 : 1;
+    uint32_t tiles, per, group, in, step_group, step_in, left, m;
+    int4 tile;
+
+    __device__ __forceinline__ Units(const ProductArgs& a, uint32_t tiles_, uint32_t mtiles, uint32_t first, uint32_t step)
+        : tiles(tiles_), per(mtiles * kGroup), m(0), tile(make_int4(0, 0, 0, 0)) {
+        const uint32_t units = tiles * mtiles;
+        left = first < units ? (units - first - 1) / step + 1 : 0;
+        group = first / per;
+        in = first - group * per;
+        step_group = step / per;
+        step_in = step - step_group * per;
+        fetch(a);
     }
-    return o;
-}
+    __device__ __forceinline__ void fetch(const ProductArgs& a) {
+        if (left == 0) return;
+        uint32_t t = group;
+        m = in;
+        if (kGroup > 1) {
+            const uint32_t size = min(kGroup, tiles - group * kGroup);  // the last group may be short
+            m = size == kGroup ? in / kGroup : in / size;
+            t = group * kGroup + in - m * size;
+        }
+        tile = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
+    }
+    // The current unit, the same in every lane, or none (n = 0) where the plan's
+    // tile is no tile of this arena; then on to the next.
+    __device__ __forceinline__ Unit take(const ProductArgs& a) {
+        Unit o{uniform(tile.x), uniform(tile.y), uniform(tile.z), static_cast<int32_t>(m) * (kMTile * PAIRS)};
+        if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
+            o.row + static_cast<int64_t>(o.n) > a.rows) {
+            raise_error(a.err, MOE_ERR_CAPACITY);
+            o.n = 0;
+        }
+        --left;
+        group += step_group;
+        in += step_in;
+        if (in >= per) {
+            in -= per;
+            ++group;
+        }
+        fetch(a);
+        return o;
+    }
+};
 
 // kPacked: silu(gate) * up of the CTA's 64 inner columns for the tile's rows,
 // rounded to bf16 and then packed as moe_fp4_pack packs it. A block of 32 inner
@@ -378,7 +416,6 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     const int32_t planned = uniform(__ldg(a.plan));
     const uint32_t tiles = planned < 0 ? 0 : (planned > a.tile_cap ? a.tile_cap : planned);
     const uint32_t mtiles = (a.N + kMTile * PAIRS - 1) / (kMTile * PAIRS);
-    const uint32_t units = tiles * mtiles;  // the launch has checked that it fits, with a step to spare
     const uint32_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
 
@@ -387,8 +424,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
         bool ok = true;
-        for (uint32_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
+        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        while (ok && list.left > 0) {
+            const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n);
             const int boxes = static_cast<int>((n / 2 + 31) / 32);
@@ -438,8 +476,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
         uint32_t last_n = 0;
         bool ok = true;
-        for (uint32_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
+        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        while (ok && list.left > 0) {
+            const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n), place = i & 1;
             const uint32_t acc = tmem + (place ? kAcc1 : 0);
@@ -502,8 +541,9 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
         bool ok = true;
-        for (uint32_t u = first; ok && u < units; u += step) {
-            const Unit t = unit_of<PAIRS>(a, u, mtiles, tiles);
+        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        while (ok && list.left > 0) {
+            const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
             ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
@@ -680,7 +720,7 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
     if (a.tile_cap == 0) return cudaSuccess;
     // Average rows per expert: a plan has one tile per expert and one per 256 rows.
     const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
-    // Units and one step past them are counted in 32 bits; what a plan of this arena can hold is far below.
+    // Units are counted in 32 bits; what a plan of this arena can hold is far below.
     const int64_t most_tiles = rows / kFp4Tile + 1, room = (int64_t{1} << 31) / ceil_div(N, kMTile);
     if (a.tile_cap > most_tiles) a.tile_cap = static_cast<int32_t>(most_tiles);
     if (a.tile_cap > room) return cudaErrorInvalidValue;
