@@ -695,6 +695,12 @@ moe_status moe_test_fused_barrier(uint32_t spin_limit, int32_t skip_cta) {
     return MOE_OK;
 }
 
+moe_status moe_test_product_wait(uint32_t wait_cycles, int32_t quit_warp) {
+    if (wait_cycles == 0 || quit_warp < -1 || quit_warp >= kProductWarps) return MOE_ERR_INVALID_ARG;
+    arm_product_wait_test(wait_cycles, quit_warp);
+    return MOE_OK;
+}
+
 moe_status moe_pad_partitions(const moe_shape* shape, const int32_t* num_recv_tokens,
                               const int64_t* part_row_base, void* recv_arena, int64_t arena_rows,
                               int32_t* recv_src_idx, int32_t* recv_topk_idx, float* recv_topk_weights,

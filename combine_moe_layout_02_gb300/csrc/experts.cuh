@@ -41,6 +41,9 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err,
                            cudaStream_t stream);  // hq, hsf: packed gated rows instead of y
+// Test hook behind moe_test_product_wait (this host thread's next product).
+constexpr int kProductWarps = 12;  // warps of a product's CTA
+void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp);
 
 // Rows and plan of the expert layer from topk_idx alone (one partition, experts
 // at multiples of MOE_FP4_ROW_TILE rows).

@@ -68,6 +68,8 @@ struct ProductArgs {
     uint8_t* hq;   // kPacked: the inner rows as MXFP4
     uint8_t* hsf;
     int32_t* err;
+    int64_t wait_cycles;  // bound of a wait (kWaitCycles)
+    int32_t quit_warp;    // test hook: a warp of each CTA that acts as if its first wait had run out, or -1
 };
 
 // What becomes of the sums: bf16; silu(gate) * up in bf16; that, packed to MXFP4.
@@ -113,19 +115,38 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return done != 0;
 }
 
+// A wait has run out: the CTA's other roles are told, and the caller.
+__device__ __forceinline__ void give_up(Bars* b, const ProductArgs& a) {
+    *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
+    raise_error(a.err, MOE_ERR_DEVICE_TIMEOUT);
+}
+
 // Bounded wait of a whole warp, by polls and by time (about two seconds: a poll
 // may itself sleep); false if it ran out or another role of the CTA gave up.
-__device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, int32_t* err) {
+__device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, const ProductArgs& a) {
     if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
     const long long began = clock64();
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
         if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&b->abort) != 0u)) return false;
-        if (__any_sync(0xffffffffu, clock64() - began > kWaitCycles)) break;
+        if (__any_sync(0xffffffffu, clock64() - began > a.wait_cycles)) break;
     }
-    *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
-    raise_error(err, MOE_ERR_DEVICE_TIMEOUT);
+    give_up(b, a);
     return false;
+}
+
+// Whether all 128 threads that meet at barrier `id` say so.
+__device__ __forceinline__ bool all_agree(int id, bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(static_cast<uint32_t>(yes))
+        : "memory");
+    return all != 0;
 }
 
 // After a failed wait: what is in flight ends within microseconds, or (a peer
@@ -418,12 +439,13 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     const uint32_t mtiles = (a.N + kMTile * PAIRS - 1) / (kMTile * PAIRS);
     const uint32_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
+    if (warp == a.quit_warp) give_up(bars, a);
 
     if (warp == 0) {
         const int32_t wtiles = static_cast<int32_t>(ceil_div(a.N, kFp4Tile));
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
-        bool ok = true;
+        bool ok = warp != a.quit_warp;
         Units<PAIRS> list(a, tiles, mtiles, first, step);
         while (ok && list.left > 0) {
             const Unit t = list.take(a);
@@ -436,7 +458,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             const int32_t m0 = t.m0 + static_cast<int32_t>(rank) * 128;
             const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
             for (int k = 0; k < nstages; ++k) {
-                if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a.err)) {
+                if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a)) {
                     ok = false;
                     break;
                 }
@@ -475,7 +497,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
     } else if (warp == 1 && cta == 0) {
         uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
         uint32_t last_n = 0;
-        bool ok = true;
+        bool ok = warp != a.quit_warp;
         Units<PAIRS> list(a, tiles, mtiles, first, step);
         while (ok && list.left > 0) {
             const Unit t = list.take(a);
@@ -485,13 +507,13 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             // The place's last sums have been read; and, where this tile and
             // the one before it both reach the shared columns, that one's
             // part of them too.
-            if (i >= 2) ok = wait_for(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a.err);
+            if (i >= 2) ok = wait_for(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a);
             if (ok && i >= 1 && (place ? last_n : n) > static_cast<uint32_t>(kAcc1))
-                ok = wait_for(bars, &bars->shared_free, (i - 1) & 1, a.err);
+                ok = wait_for(bars, &bars->shared_free, (i - 1) & 1, a);
             tc_fence_after();
             last_n = n;
             for (int k = 0; ok && k < nstages; ++k) {
-                if (!wait_for(bars, &bars->full[s], phase, a.err)) {
+                if (!wait_for(bars, &bars->full[s], phase, a)) {
                     ok = false;
                     break;
                 }
@@ -540,13 +562,15 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
-        bool ok = true;
         Units<PAIRS> list(a, tiles, mtiles, first, step);
-        while (ok && list.left > 0) {
+        while (list.left > 0) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
-            ok = wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a.err);
+            bool ok = warp != a.quit_warp && wait_for(bars, &bars->acc_full[place], (i >> 1) & 1, a);
+            // Packing, four warps meet at barriers: they go on, or end, together. (One
+            // whose wait ran out while another's came true would leave that one there.)
+            if constexpr (MODE == kPacked) ok = all_agree(1 + half, ok);
             if (!ok) break;
             tc_fence_after();
             const int m = t.m0 + static_cast<int>(rank) * 128 + w * 32;  // the warp's weight rows
@@ -655,6 +679,10 @@ bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuui
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The next product of this host thread, when armed by moe_test_product_wait.
+thread_local uint32_t t_test_wait_cycles = 0;
+thread_local int32_t t_test_quit_warp = -1;
+
 // Clusters that can be resident at once on the current device (cached).
 template <int PAIRS, int MODE>
 int resident_clusters() {
@@ -713,10 +741,21 @@ bool two_pairs(double rows, int32_t N, int32_t K) {
 
 }  // namespace
 
+void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp) {
+    t_test_wait_cycles = wait_cycles;
+    t_test_quit_warp = quit_warp;
+}
+
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
-    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err};
+    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err, kWaitCycles, -1};
+    if (t_test_wait_cycles != 0) {  // one call armed by moe_test_product_wait
+        a.wait_cycles = t_test_wait_cycles;
+        a.quit_warp = t_test_quit_warp;
+        t_test_wait_cycles = 0;
+        t_test_quit_warp = -1;
+    }
     if (a.tile_cap == 0) return cudaSuccess;
     // Average rows per expert: a plan has one tile per expert and one per 256 rows.
     const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;

@@ -33,7 +33,7 @@ EXPORTS = ("moe_status_string", "moe_check_shape", "moe_slot_stride", "moe_scrat
            "moe_run_host_workspace_bytes", "moe_run_host", "moe_test_fused_barrier", "moe_exchange_plan",
            "moe_combine_grad", "moe_combine_expert_grad", "moe_fp4_scale_bytes", "moe_fp4_pack", "moe_fp4_unpack",
            "moe_expert_plan_ints", "moe_expert_plan", "moe_dispatch_expert_fp4", "moe_expert_product_fp4",
-           "moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows", "moe_expert_ffn_fp4")
+           "moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows", "moe_expert_ffn_fp4", "moe_test_product_wait")
 
 # moe_run_host flags (include/moe.h).
 MOE_RUN_FUSED = 1
@@ -127,6 +127,8 @@ def _open_lib() -> ctypes.CDLL:
     L.moe_run_host.argtypes = [sp, i32, vp, vp, vp, vp, vp, i64, i32, vp, i64, vp]
     L.moe_test_fused_barrier.restype = i32
     L.moe_test_fused_barrier.argtypes = [ctypes.c_uint32, i32]
+    L.moe_test_product_wait.restype = i32
+    L.moe_test_product_wait.argtypes = [ctypes.c_uint32, i32]
     L.moe_exchange_plan.restype = i32
     L.moe_exchange_plan.argtypes = [sp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in ("moe_combine_grad", "moe_combine_expert_grad"):
@@ -485,6 +487,12 @@ def moe_test_fused_barrier(spin_limit: int, skip_cta: int) -> None:
     barrier and (skip_cta >= 0) one CTA that leaves out its first arrival, so
     that its bounded waits run out (a test of the timeout path)."""
     _check(lib().moe_test_fused_barrier(int(spin_limit), int(skip_cta)), "moe_test_fused_barrier")
+
+
+def moe_test_product_wait(wait_cycles: int, quit_warp: int) -> None:
+    """Arm this thread's next product with short waits and (quit_warp >= 0) a warp
+    of each CTA that acts as if its first wait had run out (a test of the timeout path)."""
+    _check(lib().moe_test_product_wait(int(wait_cycles), int(quit_warp)), "moe_test_product_wait")
 
 
 def moe_exchange_plan(shape: moe_shape, self_rank: int, ntpr_all, ntpe_all) -> dict:

@@ -631,6 +631,19 @@ moe_status moe_exchange_plan(const moe_shape* shape, int32_t self, const int32_t
 moe_status moe_test_fused_barrier(uint32_t spin_limit, int32_t skip_cta);
 
 /*
+ * moe_test_product_wait -- test hook for the bounded waits of the experts'
+ * product. It arms the NEXT product of this host thread (moe_expert_product_fp4,
+ * or the first product of moe_expert_ffn_fp4; that one only): its waits give up
+ * after `wait_cycles` clock cycles (instead of 2^32), and if quit_warp >= 0 that
+ * warp of each CTA (0 loads, 1 issues, 4..11 take the sums out) acts as if its
+ * first wait had run out. The call records MOE_ERR_DEVICE_TIMEOUT in err, every
+ * role ends, what is in flight lands (bounded), and the context stays usable;
+ * results are undefined. Returns MOE_ERR_INVALID_ARG for wait_cycles = 0 or a
+ * quit_warp outside -1..11.
+ */
+moe_status moe_test_product_wait(uint32_t wait_cycles, int32_t quit_warp);
+
+/*
  * moe_profile_attach -- profile builds only (compiled with -DMOE_PROFILE into
  * libmoe_profile.so; the default libmoe.so has no such symbol and its kernels
  * record nothing). The pages' "Ascend DeepEP MoE Dispatch Optimization",
