@@ -25,9 +25,11 @@
 // Bound by the weights' bytes while experts have few rows (64 tokens over 256
 // experts of 7168 -> 4096: 506 us, 6.9 TB/s), by power and the SMs' intake when they
 // have many: 256 x 256 x 64 takes the pair 128 cycles, a stage 512, and brings
-// each SM 35 KB, 560 cycles at its 64 bytes per cycle (262144 rows: 2.5 ms, 6.1
-// PFLOP/s at 1.55 GHz; 2.1 ms in bursts). A pair is the smallest tile that keeps the intake near the
-// tensor pipe's pace; 256 columns are the widest instruction.
+// each SM 35 KB, 560 cycles at its 64 bytes per cycle (262144 rows: 2.53 ms, 6.1
+// PFLOP/s at 1.55 GHz). A pair is the smallest tile that keeps the intake near the
+// tensor pipe's pace; 256 columns are the widest instruction. Where rows of codes are
+// no multiple of 128 bytes each load touches two lines of L2: 44800 rows 5984 -> 2048
+// 226 us, 7168 -> 2048 214.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -60,7 +62,7 @@ constexpr long long kWaitCycles = 1ll << 32;
 constexpr int kScaleCol = 480;               // scales of a stage: 8 columns of the weights', 16 of the rows'
 
 struct ProductArgs {
-    int32_t E, N, K, gated, tile_cap;
+    int32_t E, N, K, tile_cap;
     int64_t rows;
     const int32_t* plan;
     uint16_t* y;
@@ -78,7 +80,7 @@ enum ProductMode { kPlain = 0, kGated = 1, kPacked = 2 };
 // Barriers of a CTA, and its abort flag.
 struct Bars {
     uint64_t full[kStages];   // leading CTA: both CTAs' loads of a stage have landed
-    uint64_t empty[kStages];  // each CTA: the cluster's products that read a stage are done
+    uint64_t empty[kStages];  // each CTA: the products that read a stage are done
     uint64_t acc_full[2];     // each CTA: a tile's sums are complete
     uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place
     uint64_t shared_free;     // leading CTA: both CTAs have read the tile's part of the shared columns
@@ -95,7 +97,7 @@ struct Unit {
 
 __device__ __forceinline__ uint32_t mma_n(int32_t rows) { return (rows + 31) & ~31; }
 
-// Arrival on a barrier of the cluster. What it hands over is tensor memory that
+// Arrival on a barrier of the leading CTA. What it hands over is tensor memory that
 // has been read (ordered by the tcgen05 fences), not data, so it releases at the
 // CTA's scope: at the cluster's it waited for the thread's global stores, about
 // a microsecond per tile (128 tokens, 1024 -> 14336: 456 us against 299).
@@ -172,21 +174,11 @@ __device__ __forceinline__ bool elected() {
 __device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // TMA tile loads into this CTA's shared memory, counted on the barrier of the
-// pair's leading CTA; with a mask, into the same place of every CTA in it, each
-// counted on its own pair's.
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar,
-                                       uint16_t mask) {
+// pair's leading CTA.
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "h"(mask)
-        : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                                       uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar),
-        "h"(mask)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -225,12 +217,12 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t col, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
 }
 
-// Arrives on `bar` of the mask's CTAs once every product and copy issued so far is done.
-__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
+// Arrives on `bar` of both CTAs once every product and copy issued so far is done.
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
-        "h"(mask)
+        "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 
@@ -265,13 +257,8 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
     return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
 }
 
-// A cluster's units, first, first + step, .. of the launch's. In clusters of two
-// pairs units run through groups of four row tiles, the tiles of a group innermost:
-// the clusters at work at one time then read the same weights, of an expert or two,
-// and the same few rows. 262144 rows at the power cap: 2.54 ms; with one tile's
-// units side by side 2.70, groups of 2, 8 and 12 tiles 2.57, 2.54, 2.71. Single pairs
-// are faster with one tile's units side by side (9600 rows over 32 experts, 7168 ->
-// 2048: 70 us against 74 in fours).
+// A pair's units, first, first + step, .. of the launch's. They run through groups of
+// GROUP row tiles, the tiles of a group innermost (the rule is at four_tiles).
 //
 // A role steps from unit to unit without a division and holds the next one's plan
 // words while it works on the current one. A unit of few stages is short of the time
@@ -279,14 +266,13 @@ __device__ __forceinline__ float gate_times_up(float g, float u) {
 // each unit found from its number; at width 256 50 against 51. A unit of a stage
 // pays for the step instead (64 experts, 96 -> 4096 gated, 24 us against 23), and
 // from width 1024 on the two are within 2%.
-template <int PAIRS>
+template <uint32_t GROUP>
 struct Units {
-    static constexpr uint32_t kGroup = PAIRS == 2 ? 4 : 1;
     uint32_t tiles, per, group, in, step_group, step_in, left, m;
     int4 tile;
 
     __device__ __forceinline__ Units(const ProductArgs& a, uint32_t tiles_, uint32_t mtiles, uint32_t first, uint32_t step)
-        : tiles(tiles_), per(mtiles * kGroup), m(0), tile(make_int4(0, 0, 0, 0)) {
+        : tiles(tiles_), per(mtiles * GROUP), m(0), tile(make_int4(0, 0, 0, 0)) {
         const uint32_t units = tiles * mtiles;
         left = first < units ? (units - first - 1) / step + 1 : 0;
         group = first / per;
@@ -299,17 +285,17 @@ struct Units {
         if (left == 0) return;
         uint32_t t = group;
         m = in;
-        if (kGroup > 1) {
-            const uint32_t size = min(kGroup, tiles - group * kGroup);  // the last group may be short
-            m = size == kGroup ? in / kGroup : in / size;
-            t = group * kGroup + in - m * size;
+        if (GROUP > 1) {
+            const uint32_t size = min(GROUP, tiles - group * GROUP);  // the last group may be short
+            m = size == GROUP ? in / GROUP : in / size;
+            t = group * GROUP + in - m * size;
         }
         tile = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + t);
     }
     // The current unit, the same in every lane, or none (n = 0) where the plan's
     // tile is no tile of this arena; then on to the next.
     __device__ __forceinline__ Unit take(const ProductArgs& a) {
-        Unit o{uniform(tile.x), uniform(tile.y), uniform(tile.z), static_cast<int32_t>(m) * (kMTile * PAIRS)};
+        Unit o{uniform(tile.x), uniform(tile.y), uniform(tile.z), static_cast<int32_t>(m) * kMTile};
         if (o.e < 0 || o.e >= a.E || o.row < 0 || o.row % kFp4Tile != 0 || o.n < 0 || o.n > kPlanTileRows ||
             o.row + static_cast<int64_t>(o.n) > a.rows) {
             raise_error(a.err, MOE_ERR_CAPACITY);
@@ -332,10 +318,10 @@ struct Units {
 // columns comes out of two warps, so four warps stage 32 rows in shared memory
 // and each of their threads takes half a block. `group`: which of every two
 // batches of 32 rows; its four warps meet at barrier 1 + group.
-__device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& t, uint32_t rank, uint32_t acc, int w,
+__device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& t, uint32_t cta, uint32_t acc, int w,
                                               int lane, int group, bool place, unsigned char* stage, Bars* bars,
-                                              uint32_t lead, uint64_t* acc_empty) {
-    const int inner = a.N / 2, h0 = t.m0 / 2 + static_cast<int>(rank) * 64;  // the CTA's first inner column
+                                              uint64_t* acc_empty) {
+    const int inner = a.N / 2, h0 = t.m0 / 2 + static_cast<int>(cta) * 64;  // the CTA's first inner column
     const int batches = static_cast<int>(mma_n(t.n) / 32);
     const int64_t chunks = ceil_div(inner, kFp4Chunk);
     const uint32_t to = smem_addr(stage) + ((lane & 7) + 8 * (lane >> 4)) * kPackStride + w * 32 + ((lane >> 3) & 1) * 16;
@@ -352,8 +338,8 @@ __device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            if (q == group) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
-            if (q + 2 >= batches) mbar_arrive_cluster(cluster_map(acc_empty, lead));
+            if (q == group) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
+            if (q + 2 >= batches) mbar_arrive_cluster(cluster_map(acc_empty, 0));
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -387,28 +373,27 @@ __device__ __forceinline__ void pack_tile_out(const ProductArgs& a, const Unit& 
         asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");  // the staged rows have been read
     }
     if (group >= batches && lane == 0) {  // nothing of this tile is this group's
-        mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
-        mbar_arrive_cluster(cluster_map(acc_empty, lead));
+        mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
+        mbar_arrive_cluster(cluster_map(acc_empty, 0));
     }
 }
 
-template <int PAIRS, int MODE>
+template <uint32_t GROUP, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wsmap,
                const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xsmap) {
     extern __shared__ unsigned char smem_raw[];
-    // The same offset in every CTA of the cluster (their shared windows are alike).
+    // The same offset in both CTAs of the pair (their shared windows are alike).
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     unsigned char* out_stage = smem + kStages * kStageBytes;
     Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank(), cta = rank & 1, pair = rank >> 1, lead = rank & ~1u;
-    const uint16_t all = static_cast<uint16_t>((1u << (2 * PAIRS)) - 1);
+    const uint32_t cta = cluster_ctarank();  // of the pair; 0 leads
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], PAIRS);
+            mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->acc_full[i], 1);
@@ -436,8 +421,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
 
     const int32_t planned = uniform(__ldg(a.plan));
     const uint32_t tiles = planned < 0 ? 0 : (planned > a.tile_cap ? a.tile_cap : planned);
-    const uint32_t mtiles = (a.N + kMTile * PAIRS - 1) / (kMTile * PAIRS);
-    const uint32_t step = gridDim.x / (2 * PAIRS), first = blockIdx.x / (2 * PAIRS);
+    const uint32_t mtiles = (a.N + kMTile - 1) / kMTile;
+    const uint32_t step = gridDim.x / 2, first = blockIdx.x / 2;
     const int nstages = static_cast<int>(ceil_div(a.K, kStageK));
     if (warp == a.quit_warp) give_up(bars, a);
 
@@ -446,7 +431,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
         bool ok = warp != a.quit_warp;
-        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        Units<GROUP> list(a, tiles, mtiles, first, step);
         while (ok && list.left > 0) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -455,7 +440,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             const int halves = n > 128 ? 2 : 1;
             const uint32_t bytes = 2 * (kWBytes + boxes * kXBox + kScaleBox + halves * kScaleBox);
             const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
-            const int32_t m0 = t.m0 + static_cast<int32_t>(rank) * 128;
+            const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
             const int32_t wtile = t.e * wtiles + m0 / kFp4Tile;
             for (int k = 0; k < nstages; ++k) {
                 if (issued >= kStages && !wait_for(bars, &bars->empty[s], phase ^ 1, a)) {
@@ -463,21 +448,18 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                     break;
                 }
                 const uint32_t base = smem_addr(smem + s * kStageBytes);
-                const uint32_t bar = cluster_map(&bars->full[s], lead);
+                const uint32_t bar = cluster_map(&bars->full[s], 0);
                 if (elected()) {
                     if (cta == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
                     tma_3d(base, &wmap, k * 128, m0, t.e, bar);
-                    // The CTAs with the same half of the rows load its boxes by turns, for all of them.
-                    const uint16_t mine = static_cast<uint16_t>(PAIRS == 1 ? 1u << rank : 5u << cta);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < boxes && i % PAIRS == static_cast<int>(pair))
-                            tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar, mine);
+                        if (i < boxes) tma_2d(base + kOffX + i * kXBox, &xmap, k * 128, x0 + 32 * i, bar);
                     tma_3d(base + kOffWS, &wsmap, 0, 2 * k, wtile, bar);
-                    // The rows' scales go to every CTA: each half is loaded by one.
-                    if (static_cast<int>(rank) < halves)
-                        tma_3d(base + kOffXS + rank * kScaleBox, &xsmap, 0, 2 * k,
-                               t.row / kFp4Tile + static_cast<int32_t>(rank), bar, all);
+                    // Each CTA's tensor memory holds the scales of all the tile's rows.
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (h < halves) tma_3d(base + kOffXS + h * kScaleBox, &xsmap, 0, 2 * k, t.row / kFp4Tile + h, bar);
                 }
                 ++issued;
                 if (++s == kStages) {
@@ -498,7 +480,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         uint32_t s = 0, phase = 0, i = 0;  // i: tiles so far
         uint32_t last_n = 0;
         bool ok = warp != a.quit_warp;
-        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        Units<GROUP> list(a, tiles, mtiles, first, step);
         while (ok && list.left > 0) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -534,8 +516,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                         if (j < left)
                             mma(acc, desc_rows(base) + 2 * j, desc_rows(base + kOffX) + 2 * j, instr(n, j & 1),
                                 tmem + kScaleCol + 4 * (j >> 1), tmem + kScaleCol + 8 + 8 * (j >> 1), k > 0 || j > 0);
-                    commit_to(&bars->empty[s], all);
-                    if (k == nstages - 1) commit_to(&bars->acc_full[place], static_cast<uint16_t>(3u << lead));
+                    commit_to(&bars->empty[s]);
+                    if (k == nstages - 1) commit_to(&bars->acc_full[place]);
                 }
                 __syncwarp();
                 if (++s == kStages) {
@@ -562,7 +544,7 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
-        Units<PAIRS> list(a, tiles, mtiles, first, step);
+        Units<GROUP> list(a, tiles, mtiles, first, step);
         while (list.left > 0) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -573,10 +555,10 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
             if constexpr (MODE == kPacked) ok = all_agree(1 + half, ok);
             if (!ok) break;
             tc_fence_after();
-            const int m = t.m0 + static_cast<int>(rank) * 128 + w * 32;  // the warp's weight rows
+            const int m = t.m0 + static_cast<int>(cta) * 128 + w * 32;  // the warp's weight rows
             const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
             if constexpr (MODE == kPacked) {
-                pack_tile_out(a, t, rank, acc, w, lane, half, place != 0, out_stage + half * 32 * kPackStride, bars, lead,
+                pack_tile_out(a, t, cta, acc, w, lane, half, place != 0, out_stage + half * 32 * kPackStride, bars,
                               &bars->acc_empty[place]);
                 ++i;
                 continue;
@@ -593,8 +575,8 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (q == half) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
-                    if (q + 2 >= chunks) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], lead));
+                    if (q == half) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
+                    if (q + 2 >= chunks) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], 0));
                 }
                 const int c0 = 16 * c;  // first of the chunk's rows
                 if (m >= a.N || c0 >= t.n) continue;
@@ -683,61 +665,52 @@ bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuui
 thread_local uint32_t t_test_wait_cycles = 0;
 thread_local int32_t t_test_quit_warp = -1;
 
-// Clusters that can be resident at once on the current device (cached).
-template <int PAIRS, int MODE>
-int resident_clusters() {
+// Pairs that can be resident at once on the current device (cached).
+template <uint32_t GROUP, int MODE>
+int resident_pairs() {
     static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     const bool slot = dev >= 0 && dev < 64;
     if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * PAIRS);
+    cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * PAIRS;
+    attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<PAIRS, MODE>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<GROUP, MODE>, &cfg) != cudaSuccess || n < 1) return -1;
     if (slot) cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
-template <int PAIRS, int MODE>
+template <uint32_t GROUP, int MODE>
 cudaError_t launch_pairs(const ProductArgs& a, const CUtensorMap& wmap, const CUtensorMap& wsmap, const CUtensorMap& xmap,
                          const CUtensorMap& xsmap, cudaStream_t stream) {
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel<PAIRS, MODE>), kSmem, kThreads, nullptr);
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(product_kernel<GROUP, MODE>), kSmem, kThreads, nullptr);
     if (e != cudaSuccess) return e;
-    const int clusters = resident_clusters<PAIRS, MODE>();
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    const int64_t most = a.tile_cap * ceil_div(a.N, kMTile * PAIRS);
-    const unsigned grid = 2u * PAIRS * static_cast<unsigned>(most < clusters ? most : clusters);
-    return launch_pdl_cluster(product_kernel<PAIRS, MODE>, grid, kThreads, kSmem, 2u * PAIRS, stream, a, wmap, wsmap, xmap, xsmap);
+    const int pairs = resident_pairs<GROUP, MODE>();
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    const int64_t most = a.tile_cap * ceil_div(a.N, kMTile);
+    const unsigned grid = 2u * static_cast<unsigned>(most < pairs ? most : pairs);
+    return launch_pdl_cluster(product_kernel<GROUP, MODE>, grid, kThreads, kSmem, 2u, stream, a, wmap, wsmap, xmap, xsmap);
 }
 
-// Average rows per expert from which several row tiles share an expert's weights.
-constexpr int64_t kManyRows = 256;
-
-// Whether clusters are of two pairs, which fetch the rows once for both, or of
-// one. One is faster while the SMs' own pace counts: it leaves no SM out (clusters
-// of four CTAs fit 144 of 152) and no pair idle at an odd number of weight tiles
-// (32 experts, 44800 rows 7168 -> 1280: 140 us against 156; 9600 rows 2048 -> 2048: 33
-// and 36). Two are faster where loads count: in calls long enough for the power
-// limit (262144 rows, 7168 -> 4096: 2.52 ms against 2.62), and where rows of codes
-// are no multiple of 128 bytes, so that each 128-byte load touches two lines of L2
-// (44800 rows 5984 -> 2048: 208 us against 244; 9600 rows 4128 -> 2048: 58 each, 2080
-// -> 2048: 41 and 38).
-bool two_pairs(double rows, int32_t N, int32_t K) {
-    const int64_t wtiles = ceil_div(N, kMTile);
-    const double flops = 2.0 * rows * N * K;
-    if (K % kStageK != 0) return wtiles >= 4 && flops >= 1.5e11;
-    return wtiles % 2 == 0 && flops >= 4e12;
-}
+// Whether four row tiles' units lie side by side, or one's. Four, whose pairs share
+// an expert's weights, are faster in long calls: 262144 rows spread evenly over 256
+// experts, 7168 -> 4096 2.46 ms against 2.63, 7168 -> 2048 1.31 against 1.37, 5984 ->
+// 4096 2.76 against 2.97, 2048 -> 7168 1.49 against 1.51 (unevenly, 512 to 1536 rows
+// each: 2.52 both, 2.86 against 2.93, 1.57 against 1.55). In shorter ones the order
+// that spreads the short tiles better is the faster: 98304 rows over 128 experts 7168 ->
+// 4096 1.06 ms against one's 1.02, 44800 rows over 32 experts 5984 -> 2048 232 us
+// against 226, 65536 rows over 64 experts 7168 -> 4096 622 us against 630.
+bool four_tiles(double rows, int32_t N, int32_t K) { return 2.0 * rows * N * K >= 7e12; }
 
 }  // namespace
 
@@ -749,7 +722,7 @@ void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp) {
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
-    ProductArgs a{E, N, K, gated, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err, kWaitCycles, -1};
+    ProductArgs a{E, N, K, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err, kWaitCycles, -1};
     if (t_test_wait_cycles != 0) {  // one call armed by moe_test_product_wait
         a.wait_cycles = t_test_wait_cycles;
         a.quit_warp = t_test_quit_warp;
@@ -757,8 +730,8 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         t_test_quit_warp = -1;
     }
     if (a.tile_cap == 0) return cudaSuccess;
-    // Average rows per expert: a plan has one tile per expert and one per 256 rows.
-    const int64_t per_expert = static_cast<int64_t>(a.tile_cap - E) * kPlanTileRows / E;
+    // Rows that the plan has room for: it has one tile per expert and one per 256 rows.
+    const bool four = four_tiles(static_cast<double>(a.tile_cap - E) * kPlanTileRows, N, K);
     // Units are counted in 32 bits; what a plan of this arena can hold is far below.
     const int64_t most_tiles = rows / kFp4Tile + 1, room = (int64_t{1} << 31) / ceil_div(N, kMTile);
     if (a.tile_cap > most_tiles) a.tile_cap = static_cast<int32_t>(most_tiles);
@@ -786,10 +759,9 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
         const cuuint32_t box[3] = {kFp4ChunkBytes / 4, 2, 1};
         if (!encode(side ? &xsmap : &wsmap, false, side ? xsf : wsf, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const bool two = per_expert >= kManyRows && two_pairs(static_cast<double>(per_expert) * E, N, K);
-    const auto launch = hq ? (two ? launch_pairs<2, kPacked> : launch_pairs<1, kPacked>)
-                           : gated ? (two ? launch_pairs<2, kGated> : launch_pairs<1, kGated>)
-                                   : (two ? launch_pairs<2, kPlain> : launch_pairs<1, kPlain>);
+    const auto launch = hq ? (four ? launch_pairs<4, kPacked> : launch_pairs<1, kPacked>)
+                           : gated ? (four ? launch_pairs<4, kGated> : launch_pairs<1, kGated>)
+                                   : (four ? launch_pairs<4, kPlain> : launch_pairs<1, kPlain>);
     return launch(a, wmap, wsmap, xmap, xsmap, stream);
 }
 
