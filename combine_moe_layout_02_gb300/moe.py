@@ -411,9 +411,10 @@ def moe_expert_ffn_fp4(shape, inner, x, topk_idx, topk_weights, w1q, w1sf, w2q, 
 class Fp4Rows:
     """MXFP4 operands of `groups` matrices of rows x width, allocated with torch.
 
-    ``q`` holds the codes, ``sf`` the scales in the products' layout. With
-    groups = E and rows = N these are the experts' weights; ``gated`` takes
-    them from [gate rows, up rows] order (see include/moe.h).
+    ``q`` holds the codes, ``sf`` the scales in the products' layout; either may
+    be replaced by another uint8 tensor of its size. With groups = E and rows = N
+    these are the experts' weights; ``gated`` takes them from [gate rows, up rows]
+    order (see include/moe.h).
     """
 
     def __init__(self, rows: int, width: int, device="cuda", groups: int = 1, gated: bool = False):
@@ -423,26 +424,48 @@ class Fp4Rows:
         nbytes = moe_fp4_scale_bytes(rows, width)
         if nbytes < 0:
             raise MoeError(MOE_ERR_INVALID_ARG, "moe_fp4_scale_bytes")
-        self.q = torch.empty((self.groups * self.rows, self.width // 2), dtype=torch.uint8, device=device)
-        self.sf = torch.empty((self.groups * nbytes,), dtype=torch.uint8, device=device)
+        self._q = torch.empty((self.groups * self.rows, self.width // 2), dtype=torch.uint8, device=device)
+        self._sf = torch.empty((self.groups * nbytes,), dtype=torch.uint8, device=device)
+        _ptr(self._q), _ptr(self._sf)  # refuses a device that is not a GPU
+        # What the calls look at every time: a small call's time is its host time. The
+        # tensors' addresses are taken at each call.
+        self._sizes = (self.groups, self.rows, self.width, int(self.gated))
+        self._stride = 2 * self.width
 
-        # What the calls take of this operand, once: a small call's time is its host time.
-        sizes, ptrs = (self.groups, self.rows, self.width, int(self.gated)), (_ptr(self.q), _ptr(self.sf))
-        self._pack_args, self._unpack_args = (sizes, (2 * self.width, *ptrs)), (*sizes, *ptrs)
-        self._lib = lib()
+    @staticmethod
+    def _like(t, old):
+        if t.dtype != old.dtype or t.numel() != old.numel() or t.device != old.device or not t.is_contiguous():
+            raise ValueError("expected a contiguous %s tensor of %d elements on %s" % (old.dtype, old.numel(), old.device))
+        return t
+
+    @property
+    def q(self):
+        return self._q
+
+    @q.setter
+    def q(self, t):
+        self._q = self._like(t, self._q)
+
+    @property
+    def sf(self):
+        return self._sf
+
+    @sf.setter
+    def sf(self, t):
+        self._sf = self._like(t, self._sf)
 
     def pack(self, x, E=0, plan=None, stream=None):
         """bf16 rows x [groups * rows, width] into this operand."""
-        head, tail = self._pack_args
-        st = self._lib.moe_fp4_pack(*head, _ptr(x), *tail, *_plan_args(E, plan), _stream(stream))
+        st = lib().moe_fp4_pack(*self._sizes, _ptr(x), self._stride, self._q.data_ptr(), self._sf.data_ptr(),
+                                *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:
             raise MoeError(st, "moe_fp4_pack")
         return self
 
     def unpack(self, out, E=0, plan=None, stream=None):
         """The bf16 values of this operand into out [groups * rows, width]."""
-        st = self._lib.moe_fp4_unpack(*self._unpack_args, _ptr(out), 2 * self.width, *_plan_args(E, plan),
-                                      _stream(stream))
+        st = lib().moe_fp4_unpack(*self._sizes, self._q.data_ptr(), self._sf.data_ptr(), _ptr(out), self._stride,
+                                  *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:
             raise MoeError(st, "moe_fp4_unpack")
         return out
