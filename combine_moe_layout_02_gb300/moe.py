@@ -430,13 +430,23 @@ class Fp4Rows:
         # What the calls look at every time: a small call's time is its host time. The
         # tensors' addresses are taken at each call.
         self._sizes = (self.groups, self.rows, self.width, int(self.gated))
-        self._stride = 2 * self.width
+        self._bf16, self._values, self._stride = torch.bfloat16, self.groups * self.rows * self.width, 2 * self.width
 
     @staticmethod
     def _like(t, old):
         if t.dtype != old.dtype or t.numel() != old.numel() or t.device != old.device or not t.is_contiguous():
             raise ValueError("expected a contiguous %s tensor of %d elements on %s" % (old.dtype, old.numel(), old.device))
         return t
+
+    def _check_rows(self, t):
+        """bf16 values or their bit patterns, the operand's or more rows of its width."""
+        import torch
+
+        if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+            raise ValueError("expected bfloat16 rows, got %s" % t.dtype)
+        n = t.numel()
+        if n < self._values or (n > self._values and t.shape[-1] != self.width):
+            raise ValueError("expected %d rows of %d, got %s" % (self.groups * self.rows, self.width, tuple(t.shape)))
 
     @property
     def q(self):
@@ -456,6 +466,8 @@ class Fp4Rows:
 
     def pack(self, x, E=0, plan=None, stream=None):
         """bf16 rows x [groups * rows, width] into this operand."""
+        if x.dtype is not self._bf16 or x.numel() != self._values:
+            self._check_rows(x)
         st = lib().moe_fp4_pack(*self._sizes, _ptr(x), self._stride, self._q.data_ptr(), self._sf.data_ptr(),
                                 *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:
@@ -464,6 +476,8 @@ class Fp4Rows:
 
     def unpack(self, out, E=0, plan=None, stream=None):
         """The bf16 values of this operand into out [groups * rows, width]."""
+        if out.dtype is not self._bf16 or out.numel() != self._values:
+            self._check_rows(out)
         st = lib().moe_fp4_unpack(*self._sizes, self._q.data_ptr(), self._sf.data_ptr(), _ptr(out), self._stride,
                                   *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:

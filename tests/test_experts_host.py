@@ -98,3 +98,16 @@ def test_operand_refuses_other_tensors_in_its_place(recorder):
             op.q = bad
     with pytest.raises(ValueError):
         op.sf = torch.zeros(512, dtype=torch.uint8)
+
+
+def test_operand_refuses_rows_of_another_type_or_size(recorder):
+    op = moe.Fp4Rows(3, 64, "cpu", groups=2)
+    for call in (op.pack, op.unpack):
+        for bad in (torch.zeros((6, 64)), torch.zeros((6, 64), dtype=torch.float16), torch.zeros((5, 64), dtype=torch.bfloat16),
+                    torch.zeros((6, 96), dtype=torch.bfloat16), torch.zeros((6, 32), dtype=torch.bfloat16)):
+            with pytest.raises(ValueError):
+                call(bad)
+        assert not recorder.calls
+        call(torch.zeros((2, 3, 64), dtype=torch.int16))
+        call(torch.zeros((8, 64), dtype=torch.bfloat16))  # rows to spare
+        recorder.calls.clear()
