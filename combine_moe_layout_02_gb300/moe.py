@@ -760,18 +760,35 @@ class Buffers:
         to MXFP4 before each product; the products' results are bf16. h: optional bf16 rows for the inner results
         (moe_expert_ffn_fp4_rows of them).
         """
+        inner = w2.shape[-1] * 2
+        handle = _stream(stream)
+        workspace = self._ffn_workspace(inner, handle)
+        moe_expert_ffn_fp4(self.shape, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, workspace, self.err, h,
+                           handle)
+        return out
+
+    def _ffn_workspace(self, inner, handle):
+        """The workspace of this inner width, kept as long as these buffers are (kernels in flight and captured graphs
+        use it). torch's allocator is told of every stream that it is used on: its memory then serves nobody else
+        before that stream's work is done."""
         import torch
 
-        inner = w2.shape[-1] * 2
-        if getattr(self, "ffn_inner", None) != inner:
+        kept = self.__dict__.setdefault("_ffn_workspaces", {})
+        got = kept.get(inner)
+        if got is not None and handle in got[1]:
+            return got[0]
+        device = torch.device(self.device)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        if got is None:
             n = moe_expert_ffn_fp4_workspace_bytes(self.shape, inner)
             if n < 0:
                 raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_ffn_fp4_workspace_bytes")
-            self.ffn_workspace = torch.empty((n,), dtype=torch.uint8, device=self.device)
-            self.ffn_inner = inner
-        moe_expert_ffn_fp4(self.shape, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, self.ffn_workspace,
-                           self.err, h, stream)
-        return out
+            with torch.cuda.stream(stream):
+                got = kept[inner] = torch.empty((n,), dtype=torch.uint8, device=device), set()
+        else:
+            got[0].record_stream(stream)
+        got[1].add(handle)
+        return got[0]
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):
         """layout + notify + dispatch in one launch (small shapes only)."""
