@@ -408,6 +408,24 @@ def moe_expert_ffn_fp4(shape, inner, x, topk_idx, topk_weights, w1q, w1sf, w2q, 
     _check(st, "moe_expert_ffn_fp4")
 
 
+# The types of a layer call's batch tensors; 16-bit whole numbers are bf16 bit patterns.
+_BATCH_TYPES = {"topk_idx": ("int32",), "topk_weights": ("float32",)}
+_BATCH_TYPE_SETS = {}
+
+
+def _check_batch(t, rows, width, name):
+    """t holds `rows` rows of `width` values of the type that the call reads, or more such rows."""
+    types = _BATCH_TYPE_SETS.get(name)
+    if types is None:
+        import torch
+
+        types = _BATCH_TYPE_SETS[name] = tuple(getattr(torch, n) for n in _BATCH_TYPES.get(name, ("bfloat16", "int16", "uint16")))
+    n = t.numel()
+    if t.dtype not in types or (n != rows * width and (n < rows * width or t.shape[-1] != width)):
+        raise ValueError("expected %s of %d rows of %d in %s, got %s in %s" % (
+            name, rows, width, " or ".join(str(v) for v in types), tuple(t.shape), t.dtype))
+
+
 class Fp4Rows:
     """MXFP4 operands of `groups` matrices of rows x width, allocated with torch.
 
@@ -438,16 +456,6 @@ class Fp4Rows:
             raise ValueError("expected a contiguous %s tensor of %d elements on %s" % (old.dtype, old.numel(), old.device))
         return t
 
-    def _check_rows(self, t):
-        """bf16 values or their bit patterns, the operand's or more rows of its width."""
-        import torch
-
-        if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
-            raise ValueError("expected bfloat16 rows, got %s" % t.dtype)
-        n = t.numel()
-        if n < self._values or (n > self._values and t.shape[-1] != self.width):
-            raise ValueError("expected %d rows of %d, got %s" % (self.groups * self.rows, self.width, tuple(t.shape)))
-
     @property
     def q(self):
         return self._q
@@ -467,7 +475,7 @@ class Fp4Rows:
     def pack(self, x, E=0, plan=None, stream=None):
         """bf16 rows x [groups * rows, width] into this operand."""
         if x.dtype is not self._bf16 or x.numel() != self._values:
-            self._check_rows(x)
+            _check_batch(x, self.groups * self.rows, self.width, "x")
         st = lib().moe_fp4_pack(*self._sizes, _ptr(x), self._stride, self._q.data_ptr(), self._sf.data_ptr(),
                                 *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:
@@ -477,7 +485,7 @@ class Fp4Rows:
     def unpack(self, out, E=0, plan=None, stream=None):
         """The bf16 values of this operand into out [groups * rows, width]."""
         if out.dtype is not self._bf16 or out.numel() != self._values:
-            self._check_rows(out)
+            _check_batch(out, self.groups * self.rows, self.width, "out")
         st = lib().moe_fp4_unpack(*self._sizes, self._q.data_ptr(), self._sf.data_ptr(), _ptr(out), self._stride,
                                   *(_NO_PLAN if plan is None else _plan_args(E, plan)), _stream(stream))
         if st:
@@ -762,13 +770,28 @@ class Buffers:
         """
         inner = w2.shape[-1] * 2
         handle = _stream(stream)
-        workspace = self._ffn_workspace(inner, handle)
+        workspace, sizes, (values, slots, bf16, i32, f32) = self._ffn_workspace(inner, handle)
+        if (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes) != sizes:
+            raise ValueError("expected weights of (w1, w1_sf, w2, w2_sf) = %s bytes, got %s" % (
+                sizes, (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes)))
+        # the usual batch here, all others (16-bit patterns, rows to spare, what is refused) in _check_batch
+        s = self.shape
+        if x.dtype is not bf16 or out.dtype is not bf16 or x.numel() != values or out.numel() != values:
+            _check_batch(x, s.S, s.H, "x")
+            _check_batch(out, s.S, s.H, "out")
+        if topk_idx.dtype is not i32 or topk_idx.numel() != slots:
+            _check_batch(topk_idx, s.S, s.K, "topk_idx")
+        if topk_weights is not None and (topk_weights.dtype is not f32 or topk_weights.numel() != slots):
+            _check_batch(topk_weights, s.S, s.K, "topk_weights")
+        if h is not None:
+            _check_batch(h, moe_expert_ffn_fp4_rows(s, inner), inner, "h")
         moe_expert_ffn_fp4(self.shape, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, workspace, self.err, h,
                            handle)
         return out
 
     def _ffn_workspace(self, inner, handle):
-        """The workspace of this inner width, kept as long as these buffers are (kernels in flight and captured graphs
+        """The workspace of this inner width, and what a call's tensors are held to: the weights' bytes (w1, w1_sf, w2,
+        w2_sf), the batch's sizes and types. It is kept as long as these buffers are (kernels in flight and captured graphs
         use it). torch's allocator is told of every stream that it is used on: its memory then serves nobody else
         before that stream's work is done."""
         import torch
@@ -776,19 +799,23 @@ class Buffers:
         kept = self.__dict__.setdefault("_ffn_workspaces", {})
         got = kept.get(inner)
         if got is not None and handle in got[1]:
-            return got[0]
+            return got[0], got[2], got[3]
         device = torch.device(self.device)
         stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
         if got is None:
             n = moe_expert_ffn_fp4_workspace_bytes(self.shape, inner)
             if n < 0:
                 raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_ffn_fp4_workspace_bytes")
+            s = self.shape
+            sizes = (s.E * inner * s.H, s.E * moe_fp4_scale_bytes(2 * inner, s.H), s.E * s.H * inner // 2,
+                     s.E * moe_fp4_scale_bytes(s.H, inner))
+            batch = s.S * s.H, s.S * s.K, torch.bfloat16, torch.int32, torch.float32
             with torch.cuda.stream(stream):
-                got = kept[inner] = torch.empty((n,), dtype=torch.uint8, device=device), set()
+                got = kept[inner] = torch.empty((n,), dtype=torch.uint8, device=device), set(), sizes, batch
         else:
             got[0].record_stream(stream)
         got[1].add(handle)
-        return got[0]
+        return got[0], got[2], got[3]
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):
         """layout + notify + dispatch in one launch (small shapes only)."""

@@ -111,3 +111,41 @@ def test_operand_refuses_rows_of_another_type_or_size(recorder):
         call(torch.zeros((2, 3, 64), dtype=torch.int16))
         call(torch.zeros((8, 64), dtype=torch.bfloat16))  # rows to spare
         recorder.calls.clear()
+
+
+def _layer(E=4, S=6, K=2, H=64, inner=96):
+    """Buffers without a GPU, and a layer call's arguments by name."""
+    buf = moe.Buffers.__new__(moe.Buffers)
+    buf.shape, buf.device, buf.err = moe.make_shape(1, E, S, K, H), "cpu", torch.zeros(4, dtype=torch.int32)
+    sizes = (E * inner * H, E * moe.moe_fp4_scale_bytes(2 * inner, H), E * H * inner // 2, E * moe.moe_fp4_scale_bytes(H, inner))
+    buf._ffn_workspaces = {inner: (torch.zeros(64, dtype=torch.uint8), {0}, sizes,
+                                    (S * H, S * K, torch.bfloat16, torch.int32, torch.float32))}
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    args = dict(x=torch.zeros((S, H), dtype=torch.bfloat16), topk_idx=torch.zeros((S, K), dtype=torch.int32),
+                topk_weights=torch.zeros((S, K)), w1=u8(E, 2 * inner, H // 2), w1_sf=u8(sizes[1]), w2=u8(E, H, inner // 2),
+                w2_sf=u8(sizes[3]), out=torch.zeros((S, H), dtype=torch.bfloat16))
+    return buf, args, inner
+
+
+def test_layer_refuses_tensors_that_are_not_its_own(recorder):
+    buf, args, inner = _layer()
+    call = lambda **k: buf.expert_ffn_fp4(**{**args, **k}, stream=0)
+    call()
+    call(topk_weights=None)
+    call(x=args["x"].view(torch.int16), out=torch.zeros((9, 64), dtype=torch.int16))  # rows to spare
+    call(w1=args["w1"].reshape(-1), w2=args["w2"].view(-1, inner // 2))
+    call(h=torch.zeros((moe.moe_expert_ffn_fp4_rows(buf.shape, inner), inner), dtype=torch.bfloat16))
+    assert [n for n, _ in recorder.calls] == ["moe_expert_ffn_fp4"] * 5
+    recorder.calls.clear()
+    half = lambda t: t.reshape(-1)[: t.numel() // 2]
+    bad = [dict(w1=args["w1"][:, : inner]), dict(w1=args["w1"][:3]), dict(w1_sf=half(args["w1_sf"])),
+           dict(w2_sf=half(args["w2_sf"])), dict(w2=args["w2"][:3]), dict(w1=torch.zeros((4, 2 * inner, 64), dtype=torch.uint8)),
+           dict(w1=args["w1"].to(torch.bfloat16)), dict(x=args["x"].float()), dict(x=args["x"][:5]),
+           dict(x=torch.zeros((6, 96), dtype=torch.bfloat16)), dict(x=args["x"].half()), dict(out=args["out"].float()),
+           dict(out=args["out"][:5]), dict(topk_idx=args["topk_idx"].long()), dict(topk_idx=args["topk_idx"][:, :1]),
+           dict(topk_weights=args["topk_weights"].bfloat16()), dict(topk_weights=args["topk_weights"][:3]),
+           dict(h=torch.zeros((6, inner), dtype=torch.bfloat16))]
+    for k in bad:
+        with pytest.raises(ValueError):
+            call(**k)
+    assert not recorder.calls
