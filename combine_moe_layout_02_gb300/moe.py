@@ -708,34 +708,62 @@ class Buffers:
         self.slot_row = torch.empty((s.S, s.K), dtype=torch.int32, device=dev)
         self.expert_part_base = torch.empty((s.P + 1,), dtype=torch.int64, device=dev)
 
+    def _set_expert_rows(self, arena_rows=None):
+        if getattr(self, "expert_rows", None) is None:
+            self.expert_rows = moe_max_expert_rows(self.shape) if arena_rows is None else int(arena_rows)
+
     def _expert_buffers(self, arena_rows=None):
+        """The expert-major arena and its side arrays, made when something first reads or writes them."""
         import torch
 
-        if getattr(self, "expert_arena", None) is not None:
+        if getattr(self, "_expert_arena", None) is not None:
             return
-        s, dev = self.shape, self.device
+        dev = self.device
         self._slot_tables()
-        self.expert_rows = moe_max_expert_rows(s) if arena_rows is None else int(arena_rows)
+        self._set_expert_rows(arena_rows)
         rows = max(self.expert_rows, 1)
-        self.expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
-        self.expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
-        self.expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
+        self._expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
+        self._expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
+        self._expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
+
+    @property
+    def expert_arena(self):
+        self._expert_buffers()
+        return self._expert_arena
+
+    @property
+    def expert_src_idx(self):
+        self._expert_buffers()
+        return self._expert_src_idx
+
+    @property
+    def expert_weight(self):
+        self._expert_buffers()
+        return self._expert_weight
 
     def notify_expert(self, topk_idx, stream=None, arena_rows=None):
-        self._expert_buffers(arena_rows)
+        """Rows of every slot. arena_rows: rows of the arena that dispatch_expert makes (default: always enough)."""
+        self._slot_tables()
+        self._set_expert_rows(arena_rows)
         moe_notify_expert(self.shape, topk_idx, self.num_recv_tokens_per_expert, self.recv_expert_offset,
                           self.slot_row, self.expert_part_base, self.scratch, stream)
 
     def dispatch_expert(self, x, topk_idx, topk_weights, stream=None):
+        self._expert_buffers()
         moe_dispatch_expert(self.shape, x, topk_idx, topk_weights, self.slot_row, self.expert_part_base,
-                            self.expert_arena, self.expert_rows, self.expert_src_idx, self.expert_weight,
+                            self._expert_arena, self.expert_rows, self._expert_src_idx, self._expert_weight,
                             self.err, stream)
 
     def combine_expert(self, out, topk_idx, topk_weights, y=None, y_row_stride=None, stream=None):
-        """Per-slot combine; by default y is the expert-major arena (identity experts)."""
+        """Per-slot combine; by default y is the expert-major arena (identity experts). Of a tensor y the rows that it
+        holds are read (rows past them raise MOE_ERR_CAPACITY)."""
+        self._set_expert_rows()
+        rows = self.expert_rows
         if y is None:
             y, y_row_stride = self.expert_arena, self.stride
-        moe_combine_expert(self.shape, y, y_row_stride, self.expert_part_base, self.expert_rows,
+        elif not isinstance(y, int) and y_row_stride:
+            rows = max(0, (y.nbytes - 2 * self.shape.H) // int(y_row_stride) + 1)
+        moe_combine_expert(self.shape, y, y_row_stride, self.expert_part_base, rows,
                            self.slot_row, topk_idx, topk_weights, out, self.err, stream)
 
     # ---- MXFP4 experts (after layout, notify and notify_expert; expert_alignment a

@@ -42,7 +42,7 @@ class _Recorder:
         self.real = moe.lib()
 
     def __getattr__(self, name):
-        if not name.startswith("moe_") or name.endswith(("_bytes", "_rows", "_ints")):
+        if not name.startswith("moe_") or name.endswith(("_bytes", "_rows", "_ints", "_stride")):
             return getattr(self.real, name)
         return lambda *args: self.calls.append((name, args)) or 0
 
@@ -149,3 +149,59 @@ def test_layer_refuses_tensors_that_are_not_its_own(recorder):
         with pytest.raises(ValueError):
             call(**k)
     assert not recorder.calls
+
+
+def _fp4_path(buf, idx, x):
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx)
+    buf.expert_plan()
+    buf.dispatch_expert_fp4(x, idx, None)
+
+
+def test_the_4_bit_path_makes_no_bf16_arena(recorder, monkeypatch):
+    """notify_expert makes the tables of the slots; the arena comes with the calls that use it."""
+    P, E, S, K, H = 2, 8, 64, 2, 512
+    shape = moe.make_shape(P, E, S, K, H, expert_alignment=128)
+    arena = moe.moe_max_expert_rows(shape) * moe.moe_slot_stride(H, 0)
+    made, real = [], torch.empty
+
+    def empty(*args, **kw):
+        t = real(*args, **kw)
+        made.append(t.nbytes)
+        return t
+
+    monkeypatch.setattr(torch, "empty", empty)
+    buf = moe.Buffers(shape, "cpu", arena_rows=0, side_arrays=False)
+    idx, x = torch.zeros((S, K), dtype=torch.int32), torch.zeros((S, H), dtype=torch.bfloat16)
+    _fp4_path(buf, idx, x)
+    assert max(made) < arena // 2
+    buf.dispatch_expert(x, idx, None)
+    assert max(made) == arena
+    name, args = recorder.calls[-1]
+    assert name == "moe_dispatch_expert" and args[6] == buf.expert_arena.data_ptr() and args[7] == buf.expert_rows
+    assert args[8:10] == (buf.expert_src_idx.data_ptr(), buf.expert_weight.data_ptr())
+
+
+@pytest.mark.parametrize("arena_rows", [None, 0])
+def test_combine_reads_the_rows_that_it_is_given(recorder, arena_rows):
+    P, E, S, K, H = 2, 8, 64, 2, 512
+    buf = moe.Buffers(moe.make_shape(P, E, S, K, H, expert_alignment=128), "cpu", arena_rows=0, side_arrays=False)
+    idx, x = torch.zeros((S, K), dtype=torch.int32), torch.zeros((S, H), dtype=torch.bfloat16)
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx, arena_rows=arena_rows)
+    buf.expert_plan()
+    buf.dispatch_expert_fp4(x, idx, None)
+    rows_of = lambda: recorder.calls[-1][1][4]
+    out = torch.empty_like(x)
+    buf.combine_expert(out, idx, None, y=torch.zeros((buf.fp4_rows, H), dtype=torch.bfloat16), y_row_stride=2 * H)
+    assert recorder.calls[-1][0] == "moe_combine_expert" and rows_of() == buf.fp4_rows
+    buf.combine_expert(out, idx, None, y=torch.zeros((100, H + 8), dtype=torch.bfloat16), y_row_stride=2 * H + 16)
+    assert rows_of() == 100
+    buf.combine_expert(out, idx, None, y=torch.zeros(100 * (H + 8) - 8, dtype=torch.bfloat16), y_row_stride=2 * H + 16)
+    assert rows_of() == 100  # the last row ends where the tensor does
+    buf.combine_expert(out, idx, None, y=torch.zeros(0, dtype=torch.bfloat16), y_row_stride=2 * H)
+    assert rows_of() == 0
+    buf.combine_expert(out, idx, None, y=1 << 20, y_row_stride=2 * H)  # an address: as many as the arena's
+    assert rows_of() == (moe.moe_max_expert_rows(buf.shape) if arena_rows is None else arena_rows)

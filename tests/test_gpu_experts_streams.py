@@ -201,3 +201,33 @@ def test_a_captured_layer_on_changed_inputs():
         torch.cuda.synchronize()
         assert int(buf.err[0]) == 0 and int(fresh.err[0]) == 0
         assert torch.equal(got, out)
+
+
+def test_the_4_bit_path_by_its_public_methods():
+    """Step by step without a bf16 arena: the layer's own bits, combine reading the down product's rows."""
+    import torch
+
+    S, inner, P = 640, 160, 4
+    shape = moe.make_shape(P, E, S, K, H, expert_alignment=128)
+    (x, idx, wts), (w1, w1sf, w2, w2sf) = _batch(S, 5), _weights(inner, 7)
+    want = torch.empty_like(x)
+    _buffers(S).expert_ffn_fp4(x, idx, wts, w1, w1sf, w2, w2sf, want)
+    buf = moe.Buffers(shape, "cuda", arena_rows=0, side_arrays=False, bits=False)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    buf.layout(idx)
+    buf.notify()
+    buf.notify_expert(idx)
+    buf.expert_plan()
+    buf.dispatch_expert_fp4(x, idx, wts)
+    assert torch.cuda.max_memory_allocated() - before < moe.moe_max_expert_rows(shape) * moe.moe_slot_stride(H, 0)
+    rows = buf.fp4_rows
+    h, y, out = (torch.zeros((n, m), dtype=torch.int16, device="cuda") for n, m in ((rows, inner), (rows, H), (S, H)))
+    moe.moe_expert_product_fp4(E, 2 * inner, H, 1, w1, w1sf, buf.fp4.q, buf.fp4.sf, rows, buf.plan, h, buf.err)
+    hq = moe.Fp4Rows(rows, inner).pack(h, E, buf.plan)
+    moe.moe_expert_product_fp4(E, H, inner, 0, w2, w2sf, hq.q, hq.sf, rows, buf.plan, y, buf.err)
+    buf.combine_expert(out, idx, wts, y=y, y_row_stride=2 * H)
+    torch.cuda.synchronize()
+    assert int(buf.err[0]) == 0
+    assert torch.equal(out, want)
