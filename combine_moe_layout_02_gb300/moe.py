@@ -201,6 +201,25 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _torch_stream(handle, device):
+    """torch's stream object of a handle."""
+    import torch
+
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+def _made_on(stream, device):
+    """Context in which torch allocates for a call on `stream`: what it hands out may still be in use by queued work of
+    another stream, so memory that a call makes for itself comes from the call's own."""
+    import contextlib
+
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+
+    return torch.cuda.stream(_torch_stream(_stream(stream), torch.device(device)))
+
+
 def _check(status, where):
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -699,32 +718,34 @@ class Buffers:
                            self.recv_topk_weights, stream)
 
     # ---- expert-major layout (after layout and notify) --------------------
-    def _slot_tables(self):
+    def _slot_tables(self, stream=None):
         import torch
 
         if getattr(self, "slot_row", None) is not None:
             return
         s, dev = self.shape, self.device
-        self.slot_row = torch.empty((s.S, s.K), dtype=torch.int32, device=dev)
-        self.expert_part_base = torch.empty((s.P + 1,), dtype=torch.int64, device=dev)
+        with _made_on(stream, dev):
+            self.slot_row = torch.empty((s.S, s.K), dtype=torch.int32, device=dev)
+            self.expert_part_base = torch.empty((s.P + 1,), dtype=torch.int64, device=dev)
 
     def _set_expert_rows(self, arena_rows=None):
         if getattr(self, "expert_rows", None) is None:
             self.expert_rows = moe_max_expert_rows(self.shape) if arena_rows is None else int(arena_rows)
 
-    def _expert_buffers(self, arena_rows=None):
+    def _expert_buffers(self, arena_rows=None, stream=None):
         """The expert-major arena and its side arrays, made when something first reads or writes them."""
         import torch
 
         if getattr(self, "_expert_arena", None) is not None:
             return
         dev = self.device
-        self._slot_tables()
+        self._slot_tables(stream)
         self._set_expert_rows(arena_rows)
         rows = max(self.expert_rows, 1)
-        self._expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
-        self._expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
-        self._expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
+        with _made_on(stream, dev):
+            self._expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
+            self._expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
+            self._expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
 
     @property
     def expert_arena(self):
@@ -743,13 +764,13 @@ class Buffers:
 
     def notify_expert(self, topk_idx, stream=None, arena_rows=None):
         """Rows of every slot. arena_rows: rows of the arena that dispatch_expert makes (default: always enough)."""
-        self._slot_tables()
+        self._slot_tables(stream)
         self._set_expert_rows(arena_rows)
         moe_notify_expert(self.shape, topk_idx, self.num_recv_tokens_per_expert, self.recv_expert_offset,
                           self.slot_row, self.expert_part_base, self.scratch, stream)
 
     def dispatch_expert(self, x, topk_idx, topk_weights, stream=None):
-        self._expert_buffers()
+        self._expert_buffers(stream=stream)
         moe_dispatch_expert(self.shape, x, topk_idx, topk_weights, self.slot_row, self.expert_part_base,
                             self._expert_arena, self.expert_rows, self._expert_src_idx, self._expert_weight,
                             self.err, stream)
@@ -760,7 +781,8 @@ class Buffers:
         self._set_expert_rows()
         rows = self.expert_rows
         if y is None:
-            y, y_row_stride = self.expert_arena, self.stride
+            self._expert_buffers(stream=stream)
+            y, y_row_stride = self._expert_arena, self.stride
         elif not isinstance(y, int) and y_row_stride:
             rows = max(0, (y.nbytes - 2 * self.shape.H) // int(y_row_stride) + 1)
         moe_combine_expert(self.shape, y, y_row_stride, self.expert_part_base, rows,
@@ -768,24 +790,24 @@ class Buffers:
 
     # ---- MXFP4 experts (after layout, notify and notify_expert; expert_alignment a
     # multiple of MOE_FP4_ROW_TILE) ------------------------------------------------
-    def _fp4_buffers(self):
-        import torch
-
+    def _fp4_buffers(self, stream=None):
         if getattr(self, "plan", None) is not None:
             return
         s, dev = self.shape, self.device
-        self.plan = expert_plan_buffer(s, dev)
+        self._slot_tables(stream)
         t = MOE_FP4_ROW_TILE
-        self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
-        self.fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
-        self._slot_tables()
+        with _made_on(stream, dev):
+            plan = expert_plan_buffer(s, dev)
+            self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
+            self.fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
+        self.plan = plan
 
     def expert_plan(self, stream=None):
-        self._fp4_buffers()
+        self._fp4_buffers(stream)
         moe_expert_plan(self.shape, self.num_tokens_per_expert, self.plan, self.err, stream)
 
     def dispatch_expert_fp4(self, x, topk_idx, topk_weights, stream=None, recv_src_idx=None, recv_weight=None):
-        self._fp4_buffers()
+        self._fp4_buffers(stream)
         moe_dispatch_expert_fp4(self.shape, x, topk_idx, topk_weights, self.slot_row, self.expert_part_base,
                                 self.fp4.q, self.fp4.sf, self.fp4_rows, recv_src_idx, recv_weight, self.err, stream)
 
@@ -829,7 +851,7 @@ class Buffers:
         if got is not None and handle in got[1]:
             return got[0], got[2], got[3]
         device = torch.device(self.device)
-        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        stream = _torch_stream(handle, device)
         if got is None:
             n = moe_expert_ffn_fp4_workspace_bytes(self.shape, inner)
             if n < 0:

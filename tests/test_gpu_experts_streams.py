@@ -231,3 +231,43 @@ def test_the_4_bit_path_by_its_public_methods():
     torch.cuda.synchronize()
     assert int(buf.err[0]) == 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("what", ["fp4", "arena"])
+def test_first_calls_make_their_memory_on_their_stream(what):
+    """As the workspace: operands and arenas that a first call makes on a side stream."""
+    import torch
+
+    S = 4000
+    x, idx, wts = _batch(S, 1)
+    side = torch.cuda.Stream()
+    buf = moe.Buffers(moe.make_shape(1, E, S, K, H, expert_alignment=128), "cuda", arena_rows=0, side_arrays=False)
+    rows = (moe.moe_max_expert_rows(buf.shape) + 127) // 128 * 128
+    n = rows * (H // 2) if what == "fp4" else moe.moe_max_expert_rows(buf.shape) * buf.stride
+
+    def calls(b):
+        b.notify_expert(idx, stream=side)
+        if what == "fp4":
+            b.expert_plan(stream=side)
+            b.dispatch_expert_fp4(x, idx, wts, stream=side)
+        else:
+            b.dispatch_expert(x, idx, wts, stream=side)
+
+    first = moe.Buffers(buf.shape, "cuda", arena_rows=0, side_arrays=False)
+    for b in (first, buf):
+        b.layout(idx)
+        b.notify()
+    calls(first)  # a kernel's first use waits for the device
+    torch.cuda.synchronize()
+    del b, first
+    torch.cuda.empty_cache()
+    old = torch.full((n,), 0x2A, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    still = old.clone()  # queued behind the sleep: reads `old` then
+    del old
+    calls(buf)
+    assert (buf.fp4.q if what == "fp4" else buf.expert_arena).nbytes == n
+    torch.cuda.synchronize()
+    assert int(buf.err[0]) == 0
+    assert (still == 0x2A).all()
