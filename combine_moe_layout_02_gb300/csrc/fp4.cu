@@ -269,19 +269,19 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
         tile_part[lane] = t;
     }
     __syncthreads();
-    int64_t row = rincl - rows + (warp ? row_part[warp - 1] : 0);
-    int32_t tile = tincl - tiles + (warp ? tile_part[warp - 1] : 0);
+    // More rows than any routing of the shape needs: no plan. Else rows fit 32 bits (the
+    // shape's own rule), and so do tile numbers.
+    const bool none = row_part[31] > max_slots + static_cast<int64_t>(E) * (align - 1);
+    bad |= none;
+    int64_t row = none ? 0 : rincl - rows + (warp ? row_part[warp - 1] : 0);
+    int32_t tile = none ? 0 : tincl - tiles + (warp ? tile_part[warp - 1] : 0);
     int4* list = reinterpret_cast<int4*>(plan + plan_tiles_at(E));
     const int e4 = static_cast<int>(round_up(E, 4));
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
         if (e >= E) break;
-        int32_t n = counts[e];
-        if (row + n > INT32_MAX) {
-            bad = true;
-            n = 0;
-        }
-        plan[4 + e] = static_cast<int32_t>(row > INT32_MAX ? INT32_MAX : row);
+        const int32_t n = none ? 0 : counts[e];
+        plan[4 + e] = static_cast<int32_t>(row);
         plan[4 + e4 + e] = n;
         for (int32_t at = 0; at < n; at += kPlanTileRows, ++tile) {
             if (tile >= tile_cap) {
@@ -294,8 +294,8 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
     }
     if (bad) raise_error(err, MOE_ERR_INCONSISTENT);
     if (tid == 0) {
-        plan[0] = tile_part[31] < tile_cap ? tile_part[31] : tile_cap;
-        plan[1] = static_cast<int32_t>(row_part[31] > INT32_MAX ? INT32_MAX : row_part[31]);
+        plan[0] = none ? 0 : tile_part[31] < tile_cap ? tile_part[31] : tile_cap;
+        plan[1] = none ? 0 : static_cast<int32_t>(row_part[31]);
         plan[2] = E;
         plan[3] = 0;
     }

@@ -405,7 +405,9 @@ moe_status moe_fp4_unpack(int32_t groups, int64_t rows, int32_t width, int32_t g
  *          [E4], rows of each expert [E4], and the tiles [.., 4]: expert, first arena
  *          row, rows (1..MOE_PLAN_TILE_ROWS), 0
  *   err    int32 device word or NULL: MOE_ERR_INCONSISTENT if the counts are not
- *          those of a routing of this shape (negative, or more than S * K)
+ *          those of a routing of this shape: an expert's sum over the ranks negative
+ *          or more than S * K (it then has no rows), or more rows in all than
+ *          moe_max_expert_rows (no expert then has any), or more tiles than fit
  */
 #define MOE_PLAN_TILE_ROWS 256
 int64_t moe_expert_plan_ints(const moe_shape* shape);
