@@ -237,8 +237,9 @@ template <int MAXR, bool EXPERT>
 cudaError_t launch_grad_w(const CombineGradArgs& a, cudaStream_t stream) {
     // Four warps per token from kTeamHidden on, where each still has four rounds
     // of columns: fewer rows open at once per SM (131072 rows of 7168: 612 us,
-    // one warp per token 640, eight 613; of 1024: 393 us against one's 362), and
-    // for few tokens, which would leave SMs idle with a warp each.
+    // one warp per token 640, eight 613; 262144 of 4096 688 against one's 709; 524288 of
+    // 2048 697 against 714; 1048576 of 1024 774 against 712), and for few tokens, which
+    // would leave SMs idle with a warp each (304 tokens of 1024 3.8 us against 6.2).
     const bool team = a.H >= kTeamHidden || a.S < static_cast<int64_t>(device_sm_count()) * kGradWarps;
     return team ? launch_grad_t<MAXR, EXPERT, kTeam>(a, stream) : launch_grad_t<MAXR, EXPERT, 1>(a, stream);
 }

@@ -5,10 +5,6 @@
 
 #include "fp4.cuh"
 
-#ifndef MOE_FP4_DISPATCH_ROUNDS
-#define MOE_FP4_DISPATCH_ROUNDS 2
-#endif
-
 namespace moe {
 namespace {
 
@@ -177,14 +173,14 @@ cudaError_t launch_pack_t(const PackArgs& a, int64_t units_max, cudaStream_t str
 }
 
 // ---------------------------------------------------------------------------
-// The experts' row tiles: one CTA, a thread per expert (several from 1024 on).
-// Counts are summed over the source ranks, by the expert's thread where ranks
-// are few, else by threads side by side on the experts with the ranks split over
-// the thread groups that are left; then first rows and tile numbers are exclusive
-// scans. Latency-bound.
+// The experts' row tiles: one CTA, a thread per expert (several from 1024 on), no
+// more threads than the experts need. A thread sums its expert's counts over the
+// source ranks; then first rows and tile numbers are exclusive scans. Latency-bound:
+// 8 ranks of 256 experts 2.2 us, 64 3.7, 128 5.2, 1024 of 1024 33. (1024 threads with
+// the ranks split among those that the experts leave over, joined by shared atomics:
+// 3.3, 5.7, 8.5 and 178.)
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanFewRanks = 32;
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_t* __restrict__ ntpe,
@@ -198,30 +194,13 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
     const int threads = blockDim.x;
     // Thread t scans experts [t * per, (t + 1) * per).
     const int per = (E + threads - 1) / threads;
-    if (P <= kPlanFewRanks) {
-        for (int i = 0; i < per; ++i) {
-            const int e = tid * per + i;
-            if (e >= E) break;
-            int32_t sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e >= E) break;
+        int32_t sum = 0;
 #pragma unroll 8
-            for (int s = 0; s < P; ++s) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
-            counts[e] = sum;  // read by this thread only
-        }
-    } else {
-        for (int e = tid; e < E; e += threads) counts[e] = 0;
-        __syncthreads();
-        const int lanes_e = E < threads ? E : threads;
-        const int parts = threads / lanes_e;
-        const int part = tid / lanes_e;
-        if (part < parts) {
-            for (int e = tid % lanes_e; e < E; e += lanes_e) {
-                int32_t sum = 0;
-#pragma unroll 8
-                for (int s = part; s < P; s += parts) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
-                atomicAdd(counts + e, sum);  // integers: any order gives the same sum
-            }
-        }
-        __syncthreads();
+        for (int s = 0; s < P; ++s) sum += __ldg(ntpe + static_cast<int64_t>(s) * E + e);
+        counts[e] = sum;  // read by this thread only
     }
     int64_t rows = 0;
     int32_t tiles = 0;
@@ -314,6 +293,10 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
 // words are what is left).
 
 constexpr int kFp4DispatchWarps = 8;
+// Units of work that every warp should have (8 slots, H = 7168, in a graph: 64 tokens
+// 4.0 us, whole tokens 12.5; 2048 20.8 us, one unit per warp 21.4, four 30.7; 4096 35.7,
+// 42.9 and 42.3; 1024 16.8, 11.6 and 16.8: one is better there alone).
+constexpr int kFp4DispatchRounds = 2;
 
 struct Fp4DispatchArgs {
     int32_t P, E, K, H, epr;
@@ -462,7 +445,7 @@ cudaError_t launch_expert_plan(const moe_shape& s, const int32_t* ntpe, int32_t*
     const size_t smem = static_cast<size_t>(s.E) * 4;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(plan_kernel), smem, kPlanThreads, nullptr);
     if (e != cudaSuccess) return e;
-    const int64_t threads = s.P <= kPlanFewRanks && s.E < kPlanThreads ? round_up(s.E, 32) : kPlanThreads;
+    const int64_t threads = s.E < kPlanThreads ? round_up(s.E, 32) : kPlanThreads;
     return launch_pdl(plan_kernel, 1u, static_cast<unsigned>(threads), smem, stream, s.P, s.E, s.expert_alignment,
                       static_cast<int64_t>(s.S) * s.K, ntpe, plan, plan_capacity(s.E, plan_ints), err);
 }
@@ -495,12 +478,12 @@ cudaError_t launch_dispatch_fp4(const moe_shape& s, const uint16_t* x, const int
     a.swords = static_cast<int32_t>(ceil_div(s.H, kFp4Chunk));
     const int64_t moved = static_cast<int64_t>(s.S) * (2 * s.H + static_cast<int64_t>(s.K) * a.qbytes);
     a.keep_scales = moved > device_l2_bytes();
-    // Parts: halve the columns while every warp of the device would have fewer
-    // than MOE_FP4_DISPATCH_ROUNDS parts.
+    // Parts: halve the columns while every warp of the device would have fewer than
+    // kFp4DispatchRounds of them.
     const int64_t blocks512 = ceil_div(s.H, 512);
     const int64_t warps = static_cast<int64_t>(device_sm_count()) * 4 * kFp4DispatchWarps;
     int64_t parts = 1;
-    while (parts < blocks512 && s.S * parts < MOE_FP4_DISPATCH_ROUNDS * warps) parts *= 2;
+    while (parts < blocks512 && s.S * parts < kFp4DispatchRounds * warps) parts *= 2;
     a.part_cols = static_cast<int32_t>(ceil_div(blocks512, parts) * 512);
     a.parts = static_cast<int32_t>(ceil_div(s.H, a.part_cols));
     const size_t smem = static_cast<size_t>(round_up((s.P + 1) * 8, 128)) + 2 * fp4_stage_bytes(a.part_cols) * kFp4DispatchWarps;
