@@ -820,7 +820,7 @@ class Buffers:
         """
         inner = w2.shape[-1] * 2
         handle = _stream(stream)
-        workspace, sizes, (values, slots, bf16, i32, f32) = self._ffn_workspace(inner, handle)
+        workspace, sizes, (values, slots, bf16, i32, f32) = self._ffn_workspace(inner, handle, stream)
         if (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes) != sizes:
             raise ValueError("expected weights of (w1, w1_sf, w2, w2_sf) = %s bytes, got %s" % (
                 sizes, (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes)))
@@ -839,15 +839,23 @@ class Buffers:
                            handle)
         return out
 
-    def _ffn_workspace(self, inner, handle):
+    def _ffn_workspace(self, inner, handle, stream=None):
         """The workspace of this inner width, and what a call's tensors are held to: the weights' bytes (w1, w1_sf, w2,
         w2_sf), the batch's sizes and types. It is kept as long as these buffers are (kernels in flight and captured graphs
         use it). torch's allocator is told of every stream that it is used on: its memory then serves nobody else
-        before that stream's work is done."""
-        import torch
-
+        before that stream's work is done. A stream that is not torch's may be gone by then, so it has a workspace of
+        its own instead."""
         kept = self.__dict__.setdefault("_ffn_workspaces", {})
         got = kept.get(inner)
+        if got is not None and handle in got[1]:
+            return got[0], got[2], got[3]
+        import torch
+
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        # an external stream's number is its handle; one that is given as a handle alone may be anybody's
+        key = (inner, handle) if handle and getattr(stream, "stream_id", handle) == handle else inner
+        got = kept.get(key)
         if got is not None and handle in got[1]:
             return got[0], got[2], got[3]
         device = torch.device(self.device)
@@ -861,7 +869,7 @@ class Buffers:
                      s.E * moe_fp4_scale_bytes(s.H, inner))
             batch = s.S * s.H, s.S * s.K, torch.bfloat16, torch.int32, torch.float32
             with torch.cuda.stream(stream):
-                got = kept[inner] = torch.empty((n,), dtype=torch.uint8, device=device), set(), sizes, batch
+                got = kept[key] = torch.empty((n,), dtype=torch.uint8, device=device), set(), sizes, batch
         else:
             got[0].record_stream(stream)
         got[1].add(handle)

@@ -271,3 +271,44 @@ def test_first_calls_make_their_memory_on_their_stream(what):
     torch.cuda.synchronize()
     assert int(buf.err[0]) == 0
     assert (still == 0x2A).all()
+
+
+@pytest.mark.parametrize("how", ["handle", "external", "current"])
+def test_a_stream_that_is_not_torchs_may_go_first(how):
+    """A stream made and destroyed by the program itself: buffers that were used on it are dropped afterwards."""
+    import ctypes
+    import gc
+
+    import torch
+
+    cuda = moe.lib()  # finds the CUDA runtime that the library is linked to
+    cuda.cudaStreamCreateWithFlags.argtypes = [ctypes.c_void_p, ctypes.c_uint]
+    cuda.cudaStreamDestroy.argtypes = cuda.cudaStreamSynchronize.argtypes = [ctypes.c_void_p]
+    S = 200
+    batch, w = _batch(S, 1), _weights(608, 2)
+    want, out = torch.empty_like(batch[0]), torch.empty_like(batch[0])
+    buf = _buffers(S)
+    buf.expert_ffn_fp4(*batch, *w, want)  # torch's own stream first
+    torch.cuda.synchronize()
+    raw = ctypes.c_void_p()
+    assert cuda.cudaStreamCreateWithFlags(ctypes.byref(raw), 1) == 0
+    for _ in range(2):
+        out.zero_()
+        torch.cuda.synchronize()
+        if how == "handle":
+            buf.expert_ffn_fp4(*batch, *w, out, stream=raw.value)
+        elif how == "external":
+            buf.expert_ffn_fp4(*batch, *w, out, stream=torch.cuda.ExternalStream(raw.value))
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(raw.value)):
+                buf.expert_ffn_fp4(*batch, *w, out)
+        assert cuda.cudaStreamSynchronize(raw) == 0
+        assert torch.equal(out, want)
+    assert int(buf.err[0]) == 0
+    assert cuda.cudaStreamDestroy(raw) == 0
+    del buf
+    gc.collect()
+    again = _buffers(S)
+    again.expert_ffn_fp4(*batch, *w, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
