@@ -288,7 +288,7 @@ plan_kernel(int32_t P, int32_t E, int32_t align, int64_t max_slots, const int32_
 // one bulk store per slot, the scale words go straight to the slots' chunks.
 //
 // Bound by memory: S rows of 2H bytes in, a packed row per slot out. Measured (8
-// slots per token, H = 7168): 4096 tokens 38 us, 4.9 TB/s; 32768 tokens 304 us, 4.8
+// slots per token, H = 7168): 4096 tokens 36 us, 5.1 TB/s; 32768 tokens 299 us, 4.9
 // TB/s (331 before the scale words were kept in L2; without them at all 226: 4-byte
 // words are what is left).
 

@@ -371,7 +371,8 @@ int64_t moe_fp4_scale_bytes(int64_t rows, int32_t width);
 
 /*
  * moe_fp4_pack / moe_fp4_unpack -- bf16 rows to MXFP4, and back to the bf16
- * values they stand for (every one is exact in bf16).
+ * values they stand for (exact for every scale code that packing gives; under the
+ * codes 253 and 254 the largest values are past bf16's range and become infinite).
  *
  *   groups, rows   groups >= 0 operands of rows >= 0 rows each; x and q hold
  *                  groups * rows rows, sf groups * moe_fp4_scale_bytes(rows, width) bytes
@@ -442,7 +443,8 @@ moe_status moe_dispatch_expert_fp4(const moe_shape* shape, const uint16_t* x, co
  *   E, N, K     experts, weight rows per expert and row width: N and K multiples of
  *               32, N <= MOE_FP4_MAX_WIDTH * 2, K <= MOE_FP4_MAX_WIDTH
  *   wq, wsf     the weights' E operands of N x K
- *   xq, xsf     the rows' operand of arena_rows x K (arena_rows a multiple of 128)
+ *   xq, xsf     the rows' operand of arena_rows x K (arena_rows a multiple of 128; with
+ *               0 rows nothing is enqueued, and err is not written)
  *   plan        moe_expert_plan's, plan_ints words
  *   y           bf16 rows of the same arena, y_row_stride bytes apart (a multiple of
  *               16, at least 2 bytes per value); rows that are no expert's are not written
