@@ -728,6 +728,8 @@ class Buffers:
             self.slot_row = torch.empty((s.S, s.K), dtype=torch.int32, device=dev)
             self.expert_part_base = torch.empty((s.P + 1,), dtype=torch.int64, device=dev)
 
+    _expert_arena = _expert_src_idx = _expert_weight = None
+
     def _set_expert_rows(self, arena_rows=None):
         if getattr(self, "expert_rows", None) is None:
             self.expert_rows = moe_max_expert_rows(self.shape) if arena_rows is None else int(arena_rows)
@@ -736,31 +738,46 @@ class Buffers:
         """The expert-major arena and its side arrays, made when something first reads or writes them."""
         import torch
 
-        if getattr(self, "_expert_arena", None) is not None:
+        if self._expert_arena is not None and self._expert_src_idx is not None and self._expert_weight is not None:
             return
         dev = self.device
         self._slot_tables(stream)
         self._set_expert_rows(arena_rows)
         rows = max(self.expert_rows, 1)
         with _made_on(stream, dev):
-            self._expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
-            self._expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
-            self._expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
+            if self._expert_src_idx is None:
+                self._expert_src_idx = torch.empty((rows,), dtype=torch.int32, device=dev)
+            if self._expert_weight is None:
+                self._expert_weight = torch.empty((rows,), dtype=torch.float32, device=dev)
+            if self._expert_arena is None:
+                self._expert_arena = torch.empty((rows, self.stride), dtype=torch.uint8, device=dev)
 
     @property
     def expert_arena(self):
         self._expert_buffers()
         return self._expert_arena
 
+    @expert_arena.setter
+    def expert_arena(self, t):
+        self._expert_arena = t
+
     @property
     def expert_src_idx(self):
         self._expert_buffers()
         return self._expert_src_idx
 
+    @expert_src_idx.setter
+    def expert_src_idx(self, t):
+        self._expert_src_idx = t
+
     @property
     def expert_weight(self):
         self._expert_buffers()
         return self._expert_weight
+
+    @expert_weight.setter
+    def expert_weight(self, t):
+        self._expert_weight = t
 
     def notify_expert(self, topk_idx, stream=None, arena_rows=None):
         """Rows of every slot. arena_rows: rows of the arena that dispatch_expert makes (default: always enough)."""
@@ -819,8 +836,7 @@ class Buffers:
         (moe_expert_ffn_fp4_rows of them).
         """
         inner = w2.shape[-1] * 2
-        handle = _stream(stream)
-        workspace, sizes, (values, slots, bf16, i32, f32) = self._ffn_workspace(inner, handle, stream)
+        sizes, values, slots, bf16, i32, f32 = self._ffn_sizes(inner)
         if (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes) != sizes:
             raise ValueError("expected weights of (w1, w1_sf, w2, w2_sf) = %s bytes, got %s" % (
                 sizes, (w1.nbytes, w1_sf.nbytes, w2.nbytes, w2_sf.nbytes)))
@@ -835,20 +851,35 @@ class Buffers:
             _check_batch(topk_weights, s.S, s.K, "topk_weights")
         if h is not None:
             _check_batch(h, moe_expert_ffn_fp4_rows(s, inner), inner, "h")
-        moe_expert_ffn_fp4(self.shape, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out, workspace, self.err, h,
-                           handle)
+        handle = _stream(stream)
+        moe_expert_ffn_fp4(s, inner, x, topk_idx, topk_weights, w1, w1_sf, w2, w2_sf, out,
+                           self._ffn_workspace(inner, handle, stream), self.err, h, handle)
         return out
 
+    def _ffn_sizes(self, inner):
+        """What a call's tensors are held to: the weights' bytes (w1, w1_sf, w2, w2_sf), the batch's sizes and types."""
+        known = self.__dict__.setdefault("_ffn_known", {})
+        got = known.get(inner)
+        if got is None:
+            import torch
+
+            s = self.shape
+            if moe_expert_ffn_fp4_workspace_bytes(s, inner) < 0:
+                raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_ffn_fp4_workspace_bytes")
+            sizes = (s.E * inner * s.H, s.E * moe_fp4_scale_bytes(2 * inner, s.H), s.E * s.H * inner // 2,
+                     s.E * moe_fp4_scale_bytes(s.H, inner))
+            got = known[inner] = sizes, s.S * s.H, s.S * s.K, torch.bfloat16, torch.int32, torch.float32
+        return got
+
     def _ffn_workspace(self, inner, handle, stream=None):
-        """The workspace of this inner width, and what a call's tensors are held to: the weights' bytes (w1, w1_sf, w2,
-        w2_sf), the batch's sizes and types. It is kept as long as these buffers are (kernels in flight and captured graphs
-        use it). torch's allocator is told of every stream that it is used on: its memory then serves nobody else
+        """The workspace of this inner width. It is kept as long as these buffers are (kernels in flight and captured
+        graphs use it). torch's allocator is told of every stream that it is used on: its memory then serves nobody else
         before that stream's work is done. A stream that is not torch's may be gone by then, so it has a workspace of
         its own instead."""
         kept = self.__dict__.setdefault("_ffn_workspaces", {})
         got = kept.get(inner)
         if got is not None and handle in got[1]:
-            return got[0], got[2], got[3]
+            return got[0]
         import torch
 
         if stream is None:
@@ -857,23 +888,17 @@ class Buffers:
         key = (inner, handle) if handle and getattr(stream, "stream_id", handle) == handle else inner
         got = kept.get(key)
         if got is not None and handle in got[1]:
-            return got[0], got[2], got[3]
+            return got[0]
         device = torch.device(self.device)
         stream = _torch_stream(handle, device)
         if got is None:
             n = moe_expert_ffn_fp4_workspace_bytes(self.shape, inner)
-            if n < 0:
-                raise MoeError(MOE_ERR_INVALID_ARG, "moe_expert_ffn_fp4_workspace_bytes")
-            s = self.shape
-            sizes = (s.E * inner * s.H, s.E * moe_fp4_scale_bytes(2 * inner, s.H), s.E * s.H * inner // 2,
-                     s.E * moe_fp4_scale_bytes(s.H, inner))
-            batch = s.S * s.H, s.S * s.K, torch.bfloat16, torch.int32, torch.float32
             with torch.cuda.stream(stream):
-                got = kept[key] = torch.empty((n,), dtype=torch.uint8, device=device), set(), sizes, batch
+                got = kept[key] = torch.empty((n,), dtype=torch.uint8, device=device), set()
         else:
             got[0].record_stream(stream)
         got[1].add(handle)
-        return got[0], got[2], got[3]
+        return got[0]
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):
         """layout + notify + dispatch in one launch (small shapes only)."""

@@ -42,7 +42,7 @@ class _Recorder:
         self.real = moe.lib()
 
     def __getattr__(self, name):
-        if not name.startswith("moe_") or name.endswith(("_bytes", "_rows", "_ints", "_stride")):
+        if not name.startswith("moe_") or name.endswith(("_bytes", "_rows", "_ints", "_stride", "_string")):
             return getattr(self.real, name)
         return lambda *args: self.calls.append((name, args)) or 0
 
@@ -118,8 +118,7 @@ def _layer(E=4, S=6, K=2, H=64, inner=96):
     buf = moe.Buffers.__new__(moe.Buffers)
     buf.shape, buf.device, buf.err = moe.make_shape(1, E, S, K, H), "cpu", torch.zeros(4, dtype=torch.int32)
     sizes = (E * inner * H, E * moe.moe_fp4_scale_bytes(2 * inner, H), E * H * inner // 2, E * moe.moe_fp4_scale_bytes(H, inner))
-    buf._ffn_workspaces = {inner: (torch.zeros(64, dtype=torch.uint8), {0}, sizes,
-                                    (S * H, S * K, torch.bfloat16, torch.int32, torch.float32))}
+    buf._ffn_workspaces = {inner: (torch.zeros(64, dtype=torch.uint8), {0})}
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
     args = dict(x=torch.zeros((S, H), dtype=torch.bfloat16), topk_idx=torch.zeros((S, K), dtype=torch.int32),
                 topk_weights=torch.zeros((S, K)), w1=u8(E, 2 * inner, H // 2), w1_sf=u8(sizes[1]), w2=u8(E, H, inner // 2),
@@ -148,7 +147,10 @@ def test_layer_refuses_tensors_that_are_not_its_own(recorder):
     for k in bad:
         with pytest.raises(ValueError):
             call(**k)
-    assert not recorder.calls
+    for k in (dict(w2=torch.zeros((4, 64, 24), dtype=torch.uint8)), dict(w2=torch.zeros((4, 64, 0), dtype=torch.uint8))):
+        with pytest.raises(moe.MoeError):  # no inner width
+            call(**k)
+    assert not recorder.calls and list(buf._ffn_workspaces) == [inner]  # nothing was made for what is refused
 
 
 def _fp4_path(buf, idx, x):
@@ -205,3 +207,17 @@ def test_combine_reads_the_rows_that_it_is_given(recorder, arena_rows):
     assert rows_of() == 0
     buf.combine_expert(out, idx, None, y=1 << 20, y_row_stride=2 * H)  # an address: as many as the arena's
     assert rows_of() == (moe.moe_max_expert_rows(buf.shape) if arena_rows is None else arena_rows)
+
+
+def test_an_arena_of_the_programs_own(recorder):
+    """The arena and its side arrays may be replaced, before they are made as well."""
+    buf = moe.Buffers(moe.make_shape(2, 8, 64, 2, 64), "cpu", arena_rows=0, side_arrays=False)
+    idx, x = torch.zeros((64, 2), dtype=torch.int32), torch.zeros((64, 64), dtype=torch.bfloat16)
+    buf.notify_expert(idx)
+    arena = buf.expert_arena = torch.zeros((buf.expert_rows, buf.stride), dtype=torch.uint8)
+    buf.dispatch_expert(x, idx, None)
+    assert recorder.calls[-1][1][6] == arena.data_ptr() and buf.expert_arena is arena
+    assert recorder.calls[-1][1][8] == buf.expert_src_idx.data_ptr()
+    weight = buf.expert_weight = torch.zeros(buf.expert_rows)
+    buf.dispatch_expert(x, idx, None)
+    assert recorder.calls[-1][1][9] == weight.data_ptr()
