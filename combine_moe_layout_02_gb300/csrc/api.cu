@@ -677,6 +677,261 @@ moe_status moe_expert_product_fp4(int32_t E, int32_t N, int32_t K, int32_t gated
                                     static_cast<cudaStream_t>(stream)));
 }
 
+int64_t moe_gate_scratch_bytes(const moe_shape* s) {
+    if (moe_check_shape(s) != MOE_OK) return -1;
+    return round_up(static_cast<int64_t>(kGateParts) * s->E * 4, 256) + round_up(static_cast<int64_t>(kGateParts) * (s->E + 1) * 4, 256);
+}
+
+namespace {
+
+// Rows of `bytes` each, `stride` bytes apart.
+bool ok_stride(int64_t stride, int64_t bytes, int64_t align) { return stride >= bytes && stride % align == 0; }
+
+moe_status gate_args(const moe_shape* shape, int32_t type, const void* logits, int64_t row_stride, const uint8_t* mask,
+                     int32_t normalize, GateArgs* a) {
+    const moe_status st = moe_check_shape(shape);
+    if (st != MOE_OK) return st;
+    const moe_shape& s = *shape;
+    if ((type != MOE_F32 && type != MOE_BF16) || (normalize != 0 && normalize != 1)) return MOE_ERR_INVALID_ARG;
+    const int64_t elt = type == MOE_BF16 ? 2 : 4;
+    if (!ok_ptr(logits, s.S, 16) || !ok_stride(row_stride, s.E * elt, elt)) return MOE_ERR_INVALID_ARG;
+    a->E = s.E;
+    a->K = s.K;
+    a->S = s.S;
+    a->bf16 = type == MOE_BF16;
+    a->normalize = normalize;
+    a->logits = logits;
+    a->row_stride = row_stride;
+    a->mask = mask;
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_gate(const moe_shape* shape, int32_t type, const void* logits, int64_t row_stride, const uint8_t* mask,
+                    int32_t normalize, float scale, float balance, int32_t* topk_idx, float* topk_weights,
+                    int32_t* expert_count, float* expert_prob, float* loss, void* scratch, int64_t scratch_bytes,
+                    void* stream) {
+    GateArgs a{};
+    const moe_status st = gate_args(shape, type, logits, row_stride, mask, normalize, &a);
+    if (st != MOE_OK) return st;
+    const int64_t slots = a.S * a.K;
+    if (!ok_ptr(topk_idx, slots, 16) || !ok_ptr(topk_weights, slots, 16) || !ok_ptr(expert_count, 1, 16) ||
+        !ok_opt(expert_prob, 16) || !ok_opt(loss, 4) || !ok_ptr(scratch, 1, 256) ||
+        scratch_bytes < moe_gate_scratch_bytes(shape))
+        return MOE_ERR_INVALID_ARG;
+    a.scale = scale;
+    a.balance = balance;
+    a.topk_idx = topk_idx;
+    a.topk_weights = topk_weights;
+    a.expert_count = expert_count;
+    a.expert_prob = expert_prob;
+    a.loss = loss;
+    a.part_prob = static_cast<float*>(scratch);
+    a.part_count = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(scratch) + round_up(static_cast<int64_t>(kGateParts) * a.E * 4, 256));
+    return from_cuda(launch_gate(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logits, int64_t row_stride,
+                         const uint8_t* mask, int32_t normalize, float scale, float balance, const int32_t* topk_idx,
+                         const int32_t* expert_count, const float* dweights, const float* dloss, void* dlogits,
+                         int64_t dlogits_stride, void* stream) {
+    GateArgs a{};
+    const moe_status st = gate_args(shape, type, logits, row_stride, mask, normalize, &a);
+    if (st != MOE_OK) return st;
+    const int64_t slots = a.S * a.K, elt = a.bf16 ? 2 : 4;
+    if (!ok_ptr(topk_idx, slots, 16) || !ok_ptr(expert_count, 1, 16) || !ok_opt(dweights, 16) || !ok_opt(dloss, 4) ||
+        !ok_ptr(dlogits, a.S, 16) || !ok_stride(dlogits_stride, a.E * elt, elt))
+        return MOE_ERR_INVALID_ARG;
+    a.scale = scale;
+    a.balance = balance;
+    a.topk_idx = const_cast<int32_t*>(topk_idx);
+    a.expert_count = const_cast<int32_t*>(expert_count);
+    a.dweights = dweights;
+    a.dloss = dloss;
+    a.dlogits = dlogits;
+    a.dlogits_stride = dlogits_stride;
+    return from_cuda(launch_gate_grad(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Rows and width of the norm, and eps.
+moe_status norm_shape(int64_t rows, int32_t H, float eps) {
+    if (rows < 0 || H < 8 || H % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (H > MOE_MAX_HIDDEN || rows > (int64_t{1} << 40)) return MOE_ERR_UNSUPPORTED;
+    return eps >= 0x1p-126f && eps <= 3.402823466e38f ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+// An optional array of rows.
+bool ok_rows(const void* p, int64_t stride, int64_t bytes) { return p == nullptr || (aligned(p, 16) && ok_stride(stride, bytes, 16)); }
+
+}  // namespace
+
+moe_status moe_rms_norm(int64_t rows, int32_t H, float eps, const uint16_t* x, int64_t x_stride,
+                        const uint16_t* residual, int64_t residual_stride, const uint16_t* weight, uint16_t* sum,
+                        int64_t sum_stride, uint16_t* y, int64_t y_stride, int8_t* q, int64_t q_stride, float* q_scale,
+                        int64_t q_scale_stride, void* stream) {
+    const moe_status st = norm_shape(rows, H, eps);
+    if (st != MOE_OK) return st;
+    const int64_t bytes = 2 * static_cast<int64_t>(H);
+    if (rows == 0) return MOE_OK;
+    if (x == nullptr || !ok_rows(x, x_stride, bytes) || !ok_rows(residual, residual_stride, bytes) || !ok_ptr(weight, 1, 16) ||
+        !ok_rows(sum, sum_stride, bytes) || !ok_rows(y, y_stride, bytes) || !ok_rows(q, q_stride, H))
+        return MOE_ERR_INVALID_ARG;
+    if ((!sum && !y && !q) || !q != !q_scale || (y && y == sum)) return MOE_ERR_INVALID_ARG;
+    if (q && (H % 16 != 0 || !aligned(q_scale, 4) || !ok_stride(q_scale_stride, 4, 4))) return MOE_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.rows = rows;
+    a.H = H;
+    a.eps = eps;
+    a.x = reinterpret_cast<const uint8_t*>(x);
+    a.x_stride = x_stride;
+    a.residual = reinterpret_cast<const uint8_t*>(residual);
+    a.residual_stride = residual_stride;
+    a.weight = reinterpret_cast<const uint8_t*>(weight);
+    a.sum = reinterpret_cast<uint8_t*>(sum);
+    a.sum_stride = sum_stride;
+    a.y = reinterpret_cast<uint8_t*>(y);
+    a.y_stride = y_stride;
+    a.q = reinterpret_cast<uint8_t*>(q);
+    a.q_stride = q_stride;
+    a.q_scale = reinterpret_cast<uint8_t*>(q_scale);
+    a.q_scale_stride = q_scale_stride;
+    return from_cuda(launch_rms_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_rms_norm_grad_scratch_bytes(int64_t rows, int32_t H) {
+    if (norm_shape(rows, H, 1.f) != MOE_OK) return -1;
+    const int64_t bytes = (rows < kNormParts ? rows : kNormParts) * H * 4;
+    return bytes > 256 ? round_up(bytes, 256) : 256;
+}
+
+moe_status moe_rms_norm_grad(int64_t rows, int32_t H, float eps, const uint16_t* dy, int64_t dy_stride,
+                             const uint16_t* h, int64_t h_stride, const uint16_t* weight, const uint16_t* dsum,
+                             int64_t dsum_stride, uint16_t* dh, int64_t dh_stride, float* dweight, void* scratch,
+                             int64_t scratch_bytes, void* stream) {
+    const moe_status st = norm_shape(rows, H, eps);
+    if (st != MOE_OK) return st;
+    const int64_t bytes = 2 * static_cast<int64_t>(H);
+    if (rows > 0 && (dy == nullptr || h == nullptr || dh == nullptr || !ok_rows(dy, dy_stride, bytes) ||
+                     !ok_rows(h, h_stride, bytes) || !ok_rows(dh, dh_stride, bytes) || !ok_rows(dsum, dsum_stride, bytes)))
+        return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(weight, 1, 16) || !ok_opt(dweight, 16)) return MOE_ERR_INVALID_ARG;
+    if (dweight && (!ok_ptr(scratch, 1, 256) || scratch_bytes < moe_rms_norm_grad_scratch_bytes(rows, H))) return MOE_ERR_INVALID_ARG;
+    NormGradArgs a{};
+    a.rows = rows;
+    a.H = H;
+    a.eps = eps;
+    a.dy = reinterpret_cast<const uint8_t*>(dy);
+    a.dy_stride = dy_stride;
+    a.h = reinterpret_cast<const uint8_t*>(h);
+    a.h_stride = h_stride;
+    a.weight = reinterpret_cast<const uint8_t*>(weight);
+    a.dsum = reinterpret_cast<const uint8_t*>(dsum);
+    a.dsum_stride = dsum_stride;
+    a.dh = reinterpret_cast<uint8_t*>(dh);
+    a.dh_stride = dh_stride;
+    a.parts = dweight ? static_cast<float*>(scratch) : nullptr;
+    return from_cuda(launch_rms_norm_grad(a, dweight, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Arguments of packing and unpacking int8 rows alike.
+moe_status int8_rows_args(int32_t groups, int64_t rows, int32_t width, int32_t gated, const void* x, int64_t x_stride,
+                          const void* q, int64_t q_stride, const void* scale, int64_t scale_stride, int32_t E,
+                          const int32_t* plan, int64_t plan_ints, NormArgs* a) {
+    if (groups < 0 || rows < 0 || width < 1 || width % 16 != 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+    if (width > MOE_INT8_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    if (rows > (int64_t{1} << 40) || (groups > 0 && rows > (int64_t{1} << 40) / groups)) return MOE_ERR_UNSUPPORTED;
+    if (gated && rows % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (!ok_stride(x_stride, 2 * static_cast<int64_t>(width), 16) || !ok_stride(q_stride, width, 16) || !ok_stride(scale_stride, 4, 4))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t n = groups * rows;
+    if (!ok_ptr(x, n, 16) || !ok_ptr(q, n, 16) || !ok_ptr(scale, n, 4)) return MOE_ERR_INVALID_ARG;
+    if (plan) {
+        if (groups != 1 || gated || E < 1 || E > MOE_MAX_EXPERTS || rows > INT32_MAX) return MOE_ERR_INVALID_ARG;
+        if (!aligned(plan, 16) || plan_ints < plan_tiles_at(E)) return MOE_ERR_INVALID_ARG;
+        a->plan = plan;
+        a->E = E;
+        a->tile_cap = plan_tiles_cap(E, plan_ints, rows);
+    }
+    a->rows = n;
+    a->H = width;
+    a->gated = gated;
+    a->group_rows = rows;
+    a->q_stride = q_stride;
+    a->q_scale_stride = scale_stride;
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_int8_pack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint16_t* x,
+                         int64_t x_row_stride, int8_t* q, int64_t q_row_stride, float* scale, int64_t scale_stride,
+                         int32_t E, const int32_t* plan, int64_t plan_ints, void* stream) {
+    NormArgs a{};
+    const moe_status st = int8_rows_args(groups, rows, width, gated, x, x_row_stride, q, q_row_stride, scale, scale_stride, E,
+                                         plan, plan_ints, &a);
+    if (st != MOE_OK) return st;
+    a.x = reinterpret_cast<const uint8_t*>(x);
+    a.x_stride = x_row_stride;
+    a.q = reinterpret_cast<uint8_t*>(q);
+    a.q_scale = reinterpret_cast<uint8_t*>(scale);
+    return from_cuda(launch_int8_pack(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_int8_unpack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const int8_t* q,
+                           int64_t q_row_stride, const float* scale, int64_t scale_stride, uint16_t* x,
+                           int64_t x_row_stride, int32_t E, const int32_t* plan, int64_t plan_ints, void* stream) {
+    NormArgs a{};
+    const moe_status st = int8_rows_args(groups, rows, width, gated, x, x_row_stride, q, q_row_stride, scale, scale_stride, E,
+                                         plan, plan_ints, &a);
+    if (st != MOE_OK) return st;
+    a.y = reinterpret_cast<uint8_t*>(x);
+    a.y_stride = x_row_stride;
+    a.q = reinterpret_cast<uint8_t*>(const_cast<int8_t*>(q));
+    a.q_scale = reinterpret_cast<uint8_t*>(const_cast<float*>(scale));
+    return from_cuda(launch_int8_unpack(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_expert_product_int8(int32_t E, int32_t N, int32_t K, int32_t gated, const int8_t* wq, const float* ws,
+                                   const int8_t* xq, int64_t x_row_stride, const float* xs, int64_t xs_stride,
+                                   int64_t rows, const int32_t* plan, int64_t plan_ints, uint16_t* y,
+                                   int64_t y_row_stride, int32_t* err, void* stream) {
+    if (E < 1 || N < 1 || K < 1 || N % 32 != 0 || K % 16 != 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || N > 2 * MOE_INT8_MAX_WIDTH || K > MOE_INT8_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    if (rows < 0) return MOE_ERR_INVALID_ARG;
+    if (rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!ok_stride(y_row_stride, gated ? N : 2 * static_cast<int64_t>(N), 16) || !ok_stride(x_row_stride, K, 16) ||
+        !ok_stride(xs_stride, 4, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(wq, 1, 16) || !ok_ptr(ws, 1, 16) || !ok_ptr(xq, rows, 16) || !ok_ptr(xs, rows, 4) || !ok_ptr(y, rows, 16) ||
+        !ok_opt(err, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (plan ? !aligned(plan, 16) || plan_ints < plan_tiles_at(E) : E != 1) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    ProductInt8Args a{};
+    a.E = E;
+    a.N = N;
+    a.K = K;
+    a.gated = gated;
+    a.tile_cap = plan ? plan_tiles_cap(E, plan_ints, rows) : static_cast<int32_t>(ceil_div(rows, kPlanTileRows));
+    a.rows = rows;
+    a.wq = wq;
+    a.ws = ws;
+    a.xq = xq;
+    a.x_stride = x_row_stride;
+    a.xs = reinterpret_cast<const uint8_t*>(xs);
+    a.xs_stride = xs_stride;
+    a.plan = plan;
+    a.y = y;
+    a.y_stride = y_row_stride;
+    a.err = err;
+    return from_cuda(launch_product_int8(a, static_cast<cudaStream_t>(stream)));
+}
+
 #ifdef MOE_PROFILE
 moe_status moe_profile_attach(void* slots, int64_t bytes) {
     const int64_t need = static_cast<int64_t>(kProfKernels) * kProfCtas * kProfPhases * 8;

@@ -1,6 +1,6 @@
-// experts.cuh -- launchers of the experts' operators (combine_grad.cu, fp4.cu,
-// product.cu, expert.cu), called by the C-ABI layer and by ffn.cu. Arguments are
-// validated before these run.
+// experts.cuh -- launchers of the operators around the experts (combine_grad.cu,
+// fp4.cu, product.cu, expert.cu, gate.cu, norm.cu, product_int8.cu), called by the
+// C-ABI layer and by ffn.cu. Arguments are validated before these run.
 #pragma once
 
 #include "moe_device.cuh"
@@ -50,6 +50,91 @@ void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp);
 int64_t expert_route_scratch_bytes(const moe_shape& s);
 cudaError_t launch_expert_route(const moe_shape& s, const int32_t* topk_idx, int32_t* slot_row, int64_t* base,
                                 int32_t* plan, int64_t plan_ints, int32_t* err, void* scratch, cudaStream_t stream);
+
+// The router's gate and its gradient (gate.cu).
+constexpr int kGateParts = 608;  // most blocks that leave sums in the scratch
+struct GateArgs {
+    int32_t E, K, bf16, normalize;
+    int64_t S;
+    float scale, balance;
+    const void* logits;
+    int64_t row_stride;
+    const uint8_t* mask;
+    int32_t* topk_idx;  // read by the gradient
+    float* topk_weights;
+    int32_t* expert_count;  // [E + 1]; read by the gradient
+    float* expert_prob;
+    float* loss;
+    float* part_prob;     // [kGateParts][E]
+    int32_t* part_count;  // [kGateParts][E + 1]
+    const float* dweights;
+    const float* dloss;
+    void* dlogits;
+    int64_t dlogits_stride;
+};
+cudaError_t launch_gate(const GateArgs& a, cudaStream_t stream);
+cudaError_t launch_gate_grad(const GateArgs& a, cudaStream_t stream);
+
+// Root-mean-square norm, int8 rows (norm.cu). Strides are in bytes.
+constexpr int kNormParts = 608;  // most blocks that leave sums in the gradient's scratch
+struct NormArgs {
+    int64_t rows;
+    int32_t H;
+    float eps;
+    const uint8_t* x;  // packing: the rows; unpacking: not used
+    int64_t x_stride;
+    const uint8_t* residual;
+    int64_t residual_stride;
+    const uint8_t* weight;
+    uint8_t* sum;
+    int64_t sum_stride;
+    uint8_t* y;  // unpacking: the values
+    int64_t y_stride;
+    uint8_t* q;
+    int64_t q_stride;
+    uint8_t* q_scale;
+    int64_t q_scale_stride;
+    int32_t gated;       // packing: operands of group_rows rows whose gate and up rows go by turns
+    int64_t group_rows;
+    const int32_t* plan;  // packing: only the rows that it gives to experts
+    int32_t E, tile_cap;
+};
+struct NormGradArgs {
+    int64_t rows;
+    int32_t H;
+    float eps;
+    const uint8_t* dy;
+    int64_t dy_stride;
+    const uint8_t* h;
+    int64_t h_stride;
+    const uint8_t* weight;
+    const uint8_t* dsum;
+    int64_t dsum_stride;
+    uint8_t* dh;
+    int64_t dh_stride;
+    float* parts;  // [kNormParts][H], or NULL: no gradient of the weight
+};
+cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_rms_norm_grad(const NormGradArgs& a, float* dweight, cudaStream_t stream);
+cudaError_t launch_int8_pack(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_int8_unpack(const NormArgs& a, cudaStream_t stream);
+
+// Product of int8 operands (product_int8.cu). Strides are in bytes.
+struct ProductInt8Args {
+    int32_t E, N, K, gated, tile_cap;
+    int64_t rows;
+    const int8_t* wq;
+    const float* ws;
+    const int8_t* xq;
+    int64_t x_stride;
+    const uint8_t* xs;
+    int64_t xs_stride;
+    const int32_t* plan;  // NULL: all rows are the one expert's
+    uint16_t* y;
+    int64_t y_stride;
+    int32_t* err;
+};
+cudaError_t launch_product_int8(const ProductInt8Args& a, cudaStream_t stream);
 
 // L2 cache of the current device, in bytes (cached).
 int device_l2_bytes();

@@ -38,6 +38,13 @@ __host__ __device__ __forceinline__ int32_t plan_capacity(int32_t E, int64_t int
     return n < 0 ? 0 : (n > INT32_MAX ? INT32_MAX : static_cast<int32_t>(n));
 }
 
+// Row tiles that a plan of `ints` words can give of `rows` rows: experts' rows start at
+// multiples of kFp4Tile, so no more tiles than that have any.
+__host__ __forceinline__ int32_t plan_tiles_cap(int32_t E, int64_t ints, int64_t rows) {
+    const int64_t n = plan_capacity(E, ints), most = rows / kFp4Tile + 1;
+    return static_cast<int32_t>(n < most ? n : most);
+}
+
 // Byte of row m's scale word inside its chunk.
 __host__ __device__ __forceinline__ int fp4_word_at(int m) { return (m & 31) * 16 + ((m >> 5) & 3) * 4; }
 

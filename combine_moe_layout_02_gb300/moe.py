@@ -33,7 +33,9 @@ EXPORTS = ("moe_status_string", "moe_check_shape", "moe_slot_stride", "moe_scrat
            "moe_run_host_workspace_bytes", "moe_run_host", "moe_test_fused_barrier", "moe_exchange_plan",
            "moe_combine_grad", "moe_combine_expert_grad", "moe_fp4_scale_bytes", "moe_fp4_pack", "moe_fp4_unpack",
            "moe_expert_plan_ints", "moe_expert_plan", "moe_dispatch_expert_fp4", "moe_expert_product_fp4",
-           "moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows", "moe_expert_ffn_fp4", "moe_test_product_wait")
+           "moe_expert_ffn_fp4_workspace_bytes", "moe_expert_ffn_fp4_rows", "moe_expert_ffn_fp4", "moe_test_product_wait",
+           "moe_gate_scratch_bytes", "moe_gate", "moe_gate_grad", "moe_rms_norm", "moe_rms_norm_grad_scratch_bytes",
+           "moe_rms_norm_grad", "moe_int8_pack", "moe_int8_unpack", "moe_expert_product_int8")
 
 # moe_run_host flags (include/moe.h).
 MOE_RUN_FUSED = 1
@@ -152,6 +154,24 @@ def _open_lib() -> ctypes.CDLL:
         getattr(L, name).argtypes = [sp, i32]
     L.moe_expert_ffn_fp4.restype = i32
     L.moe_expert_ffn_fp4.argtypes = [sp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+    f32 = ctypes.c_float
+    L.moe_gate_scratch_bytes.restype = i64
+    L.moe_gate_scratch_bytes.argtypes = [sp]
+    L.moe_gate.restype = i32
+    L.moe_gate.argtypes = [sp, i32, vp, i64, vp, i32, f32, f32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.moe_gate_grad.restype = i32
+    L.moe_gate_grad.argtypes = [sp, i32, vp, i64, vp, i32, f32, f32, vp, vp, vp, vp, vp, i64, vp]
+    L.moe_rms_norm.restype = i32
+    L.moe_rms_norm.argtypes = [i64, i32, f32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.moe_rms_norm_grad_scratch_bytes.restype = i64
+    L.moe_rms_norm_grad_scratch_bytes.argtypes = [i64, i32]
+    L.moe_rms_norm_grad.restype = i32
+    L.moe_rms_norm_grad.argtypes = [i64, i32, f32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp]
+    for name in ("moe_int8_pack", "moe_int8_unpack"):
+        getattr(L, name).restype = i32
+        getattr(L, name).argtypes = [i32, i64, i32, i32, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp]
+    L.moe_expert_product_int8.restype = i32
+    L.moe_expert_product_int8.argtypes = [i32, i32, i32, i32, vp, vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp]
     L.moe_expert_product_fp4.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp]
     _lib = L
     return L
@@ -425,6 +445,221 @@ def moe_expert_ffn_fp4(shape, inner, x, topk_idx, topk_weights, w1q, w1sf, w2q, 
                                   _ptr(w1sf), _ptr(w2q), _ptr(w2sf), _ptr(h), _ptr(out), _ptr(workspace),
                                   workspace.numel(), _ptr(err), _stream(stream))
     _check(st, "moe_expert_ffn_fp4")
+
+
+def _cuda_tensor(t, dtypes, name):
+    """t's address; t is of one of the types and on the current device, where the call's stream is."""
+    import torch
+
+    if t.dtype not in dtypes:
+        raise ValueError("expected %s in %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    return t.data_ptr()
+
+
+def _flat(t, n, dtypes, name):
+    """Address of a contiguous tensor of n elements (None -> NULL)."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("expected %s contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
+    return _cuda_tensor(t, dtypes, name)
+
+
+def _rows_of(t, rows, width, dtypes, name):
+    """(address, bytes from row to row) of a tensor [rows, width] whose rows may be apart (None -> NULL)."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != (rows, width) or (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < width):
+        raise ValueError("expected %s of shape %s with unit column stride, got %s with strides %s" % (
+            name, (rows, width), tuple(t.shape), t.stride()))
+    size = t.element_size()
+    # one row's stride says nothing
+    return _cuda_tensor(t, dtypes, name), size * (t.stride(0) if rows > 1 else -(-width * size // 16) * 16 // size)
+
+
+_DTYPES = {}
+
+
+def _dtypes(*names):
+    got = _DTYPES.get(names)
+    if got is None:
+        import torch
+
+        got = _DTYPES[names] = tuple(getattr(torch, n) for n in names)
+    return got
+
+
+class Gate:
+    """The router's gate of one shape and its gradient, with their buffers (include/moe.h, moe_gate).
+
+    ``forward`` fills ``topk_idx`` int32 [S,K], ``topk_weights`` float32 [S,K], ``expert_count`` int32 [E + 1] (the last:
+    tokens routed), ``expert_prob`` float32 [E] and ``loss`` float32 [1]; ``backward`` reads ids and counts of the last
+    forward call. Calls in flight at once need a Gate each.
+    """
+
+    def __init__(self, shape: moe_shape, device="cuda", normalize: bool = True, scale: float = 1.0, balance: float = 0.0):
+        import torch
+
+        nbytes = int(lib().moe_gate_scratch_bytes(ctypes.byref(shape)))
+        if nbytes < 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_gate_scratch_bytes")
+        self.shape, self.normalize, self.scale, self.balance = shape, bool(normalize), float(scale), float(balance)
+        S, E, K = shape.S, shape.E, shape.K
+        self.topk_idx = torch.empty((S, K), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((S, K), dtype=torch.float32, device=device)
+        self.expert_count = torch.empty((E + 1,), dtype=torch.int32, device=device)
+        self.expert_prob = torch.empty((E,), dtype=torch.float32, device=device)
+        self.loss = torch.empty((1,), dtype=torch.float32, device=device)
+        self.scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+    def _logits(self, t, name):
+        ptr, stride = _rows_of(t, self.shape.S, self.shape.E, _dtypes("float32", "bfloat16"), name)
+        return int(t.element_size() == 2), ptr, stride
+
+    def _mask(self, mask):
+        return _flat(mask, self.shape.S, _dtypes("uint8", "bool"), "mask")
+
+    def forward(self, logits, mask=None, stream=None):
+        """Routes logits [S,E] (float32 or bfloat16, rows may be apart); mask [S] uint8 or bool: 0 for tokens left out."""
+        kind, ptr, stride = self._logits(logits, "logits")
+        st = lib().moe_gate(ctypes.byref(self.shape), kind, ptr, stride, self._mask(mask), self.normalize, self.scale,
+                            self.balance, self.topk_idx.data_ptr(), self.topk_weights.data_ptr(),
+                            self.expert_count.data_ptr(), self.expert_prob.data_ptr(), self.loss.data_ptr(),
+                            self.scratch.data_ptr(), self.scratch.numel(), _stream(stream))
+        _check(st, "moe_gate")
+        return self.topk_idx, self.topk_weights
+
+    def backward(self, logits, dweights=None, dloss=None, mask=None, dlogits=None, stream=None):
+        """The logits' gradient from those of topk_weights [S,K] and of the loss [1] (float32; None: 0). logits and mask
+        as in the forward call; dlogits: rows for the result, of logits' type (made where it is None)."""
+        import torch
+
+        s = self.shape
+        kind, ptr, stride = self._logits(logits, "logits")
+        if dlogits is None:
+            with _made_on(stream, logits.device):
+                dlogits = torch.empty((s.S, s.E), dtype=logits.dtype, device=logits.device)
+        elif dlogits.dtype != logits.dtype:
+            raise ValueError("expected dlogits in %s, got %s" % (logits.dtype, dlogits.dtype))
+        _, out, out_stride = self._logits(dlogits, "dlogits")
+        st = lib().moe_gate_grad(ctypes.byref(s), kind, ptr, stride, self._mask(mask), self.normalize, self.scale,
+                                 self.balance, self.topk_idx.data_ptr(), self.expert_count.data_ptr(),
+                                 _flat(dweights, s.S * s.K, _dtypes("float32"), "dweights"),
+                                 _flat(dloss, 1, _dtypes("float32"), "dloss"), out, out_stride, _stream(stream))
+        _check(st, "moe_gate_grad")
+        return dlogits
+
+
+def moe_rms_norm(x, weight, eps, y=None, residual=None, sum_out=None, q=None, q_scale=None, stream=None):
+    """Root-mean-square norm of x + residual [rows, H] in bf16 (include/moe.h): y and sum_out bf16 rows, q int8 rows with
+    q_scale float32 [rows] (or [rows, 1], a column of any row-strided tensor). Rows may be apart."""
+    rows, H = x.shape
+    bf16 = _dtypes("bfloat16")
+    args = []
+    for t, name in ((x, "x"), (residual, "residual")):
+        args += _rows_of(t, rows, H, bf16, name)
+    args.append(_flat(weight, H, bf16, "weight"))
+    for t, name in ((sum_out, "sum_out"), (y, "y")):
+        args += _rows_of(t, rows, H, bf16, name)
+    args += _rows_of(q, rows, H, _dtypes("int8"), "q")
+    args += _scales_of(q_scale, rows, "q_scale")
+    _check(lib().moe_rms_norm(rows, H, float(eps), *args, _stream(stream)), "moe_rms_norm")
+
+
+def _scales_of(t, rows, name):
+    """(address, bytes from one to the next) of rows float32 scales (None -> NULL)."""
+    if t is None:
+        return None, 0
+    if t.numel() != rows or t.dim() < 1 or t.shape[0] != rows:
+        raise ValueError("expected %s of %d scales, got %s" % (name, rows, tuple(t.shape)))
+    if rows > 1 and t.stride(0) < 1:
+        raise ValueError("expected %s with a stride of its own for every row" % name)
+    return _cuda_tensor(t, _dtypes("float32"), name), 4 * t.stride(0) if rows > 1 else 4
+
+
+def moe_rms_norm_grad_scratch_bytes(rows: int, H: int) -> int:
+    return int(lib().moe_rms_norm_grad_scratch_bytes(int(rows), int(H)))
+
+
+def rms_norm_grad_scratch(rows: int, H: int, device="cuda"):
+    """Scratch for moe_rms_norm_grad with dweight: a uint8 tensor that calls in flight do not share."""
+    import torch
+
+    n = moe_rms_norm_grad_scratch_bytes(rows, H)
+    if n < 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_rms_norm_grad_scratch_bytes")
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def moe_rms_norm_grad(dy, h, weight, eps, dh, dweight=None, dsum=None, scratch=None, stream=None):
+    """Gradient of moe_rms_norm at h, the sum as it was kept: dh [rows, H] bf16 and dweight [H] float32 (needs scratch)
+    from dy and dsum (bf16 rows, dsum the gradient of the sum passed on). Rows may be apart."""
+    rows, H = h.shape
+    bf16 = _dtypes("bfloat16")
+    if dweight is not None and scratch is None:
+        raise ValueError("dweight needs scratch (rms_norm_grad_scratch)")
+    args = [*_rows_of(dy, rows, H, bf16, "dy"), *_rows_of(h, rows, H, bf16, "h"), _flat(weight, H, bf16, "weight"),
+            *_rows_of(dsum, rows, H, bf16, "dsum"), *_rows_of(dh, rows, H, bf16, "dh"),
+            _flat(dweight, H, _dtypes("float32"), "dweight")]
+    if scratch is not None:
+        args += [_flat(scratch, scratch.numel(), _dtypes("uint8"), "scratch"), scratch.numel()]
+    else:
+        args += [None, 0]
+    _check(lib().moe_rms_norm_grad(rows, H, float(eps), *args, _stream(stream)), "moe_rms_norm_grad")
+
+
+class Int8Rows:
+    """int8 rows of `groups` operands of rows x width with a float32 scale each, allocated with torch.
+
+    ``q`` int8 [groups * rows, width], ``scale`` float32 [groups * rows]. With groups = E and rows = N these are the
+    experts' weights, a scale per output channel; ``gated`` takes them from [gate rows, up rows] order (see include/moe.h).
+    """
+
+    def __init__(self, rows: int, width: int, device="cuda", groups: int = 1, gated: bool = False):
+        import torch
+
+        self.rows, self.width, self.groups, self.gated = int(rows), int(width), int(groups), bool(gated)
+        if self.rows < 0 or self.groups < 0 or self.width < 16 or self.width % 16 or (self.gated and self.rows % 32):
+            raise ValueError("expected a width that is a multiple of 16, and of gated rows a multiple of 32")
+        n = self.groups * self.rows
+        self.q = torch.empty((n, self.width), dtype=torch.int8, device=device)
+        self.scale = torch.empty((n,), dtype=torch.float32, device=device)
+
+    def _call(self, pack, x, E, plan, stream):
+        n = self.groups * self.rows
+        b = _rows_of(x, n, self.width, _dtypes("bfloat16"), "x" if pack else "out")
+        q = _rows_of(self.q, n, self.width, _dtypes("int8"), "q")
+        s = _scales_of(self.scale, n, "scale")
+        name = "moe_int8_pack" if pack else "moe_int8_unpack"
+        st = getattr(lib(), name)(self.groups, self.rows, self.width, self.gated, *((*b, *q, *s) if pack else (*q, *s, *b)),
+                                  *_plan_args(E, plan), _stream(stream))
+        _check(st, name)
+
+    def pack(self, x, E=0, plan=None, stream=None):
+        """bf16 rows x [groups * rows, width] into these; with a plan, only the experts' rows."""
+        self._call(True, x, E, plan, stream)
+        return self
+
+    def unpack(self, out, E=0, plan=None, stream=None):
+        """The values, rounded to bf16, into out [groups * rows, width]."""
+        self._call(False, out, E, plan, stream)
+        return out
+
+
+def moe_expert_product_int8(E, N, K, gated, wq, ws, xq, xs, rows, plan, y, err, x_row_stride=None, xs_stride=4,
+                            y_row_stride=None, stream=None):
+    """y's rows of every expert (plan None, E 1: of all rows) from int8 weights and rows (include/moe.h). Rows of xq are
+    packed, scales of xs one after another and y rows packed unless the strides (bytes) say otherwise."""
+    if y_row_stride is None:
+        y_row_stride = (N // 2 if gated else N) * 2
+    st = lib().moe_expert_product_int8(int(E), int(N), int(K), int(gated), _ptr(wq), _ptr(ws), _ptr(xq),
+                                       int(K if x_row_stride is None else x_row_stride), _ptr(xs), int(xs_stride), int(rows),
+                                       *_plan_args(E, plan)[1:], _ptr(y), int(y_row_stride), _ptr(err), _stream(stream))
+    _check(st, "moe_expert_product_int8")
 
 
 # The types of a layer call's batch tensors; 16-bit whole numbers are bf16 bit patterns.
@@ -807,20 +1042,40 @@ class Buffers:
 
     # ---- MXFP4 experts (after layout, notify and notify_expert; expert_alignment a
     # multiple of MOE_FP4_ROW_TILE) ------------------------------------------------
+    _fp4 = None
+
+    def _plan_buffer(self, stream=None):
+        if getattr(self, "plan", None) is None:
+            with _made_on(stream, self.device):
+                self.plan = expert_plan_buffer(self.shape, self.device)
+
     def _fp4_buffers(self, stream=None):
-        if getattr(self, "plan", None) is not None:
+        if getattr(self, "plan", None) is not None and self._fp4 is not None:
             return
         s, dev = self.shape, self.device
         self._slot_tables(stream)
+        self._plan_buffer(stream)
         t = MOE_FP4_ROW_TILE
-        with _made_on(stream, dev):
-            plan = expert_plan_buffer(s, dev)
-            self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
-            self.fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
-        self.plan = plan
+        self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
+        if self._fp4 is None:
+            with _made_on(stream, dev):
+                self._fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
+
+    @property
+    def fp4(self):
+        """The arena's rows as MXFP4. With the int8 payload they are made when something first uses them."""
+        self._fp4_buffers()
+        return self._fp4
+
+    @fp4.setter
+    def fp4(self, rows):
+        self._fp4 = rows
 
     def expert_plan(self, stream=None):
-        self._fp4_buffers(stream)
+        if self.shape.quant:
+            self._plan_buffer(stream)
+        else:
+            self._fp4_buffers(stream)
         moe_expert_plan(self.shape, self.num_tokens_per_expert, self.plan, self.err, stream)
 
     def dispatch_expert_fp4(self, x, topk_idx, topk_weights, stream=None, recv_src_idx=None, recv_weight=None):
@@ -899,6 +1154,24 @@ class Buffers:
             got[0].record_stream(stream)
         got[1].add(handle)
         return got[0]
+
+    # ---- int8 experts (quant = 1, after layout, notify, notify_expert, expert_plan and dispatch_expert) ----
+    def expert_product_int8(self, weights: Int8Rows, y, stream=None):
+        """y's rows of every expert from the int8 slots that dispatch_expert filled: weights groups = E operands of N x H
+        (gated: y rows are silu(gate) * up), y bf16 [expert_rows, N or N / 2], rows contiguous."""
+        s = self.shape
+        if not s.quant:
+            raise ValueError("expected the int8 payload (quant = 1)")
+        if weights.groups != s.E or weights.width != s.H:
+            raise ValueError("expected weights of %d experts of width %d, got %d of %d" % (s.E, s.H, weights.groups, weights.width))
+        if self._expert_arena is None or getattr(self, "plan", None) is None:
+            raise ValueError("expected dispatch_expert and expert_plan before the product")
+        N = weights.rows
+        out = _flat(y, self.expert_rows * (N // 2 if weights.gated else N), _dtypes("bfloat16"), "y")
+        arena = self._expert_arena
+        moe_expert_product_int8(s.E, N, s.H, weights.gated, weights.q, weights.scale, arena,
+                                arena.data_ptr() + (s.H + 31) // 32 * 32, self.expert_rows, self.plan, out, self.err,
+                                x_row_stride=self.stride, xs_stride=self.stride, stream=stream)
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):
         """layout + notify + dispatch in one launch (small shapes only)."""

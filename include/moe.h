@@ -489,6 +489,165 @@ moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint1
                               int64_t workspace_bytes, int32_t* err, void* stream);
 
 /*
+ * moe_gate -- the router: Top-K experts, their weights, the experts' counts and
+ * the balance loss, from the gate's logits. For token g, z = logits[g],
+ * p = softmax(z):
+ *
+ *   topk_idx[g][k]     = the expert of the k-th largest logit; equal logits by
+ *                        ascending expert (-0 equals 0)
+ *   topk_weights[g][k] = scale * p[i_k] / D,  D = the sum of the token's chosen p
+ *                        (normalize = 1) or 1 (normalize = 0)
+ *   expert_count[e]    = slots that chose e;  expert_count[E] = n, tokens routed
+ *   expert_prob[e]     = (sum over routed tokens of p[e]) / n, 0 for n = 0
+ *   loss               = balance * E * sum over e of
+ *                        (expert_count[e] / (K n)) * expert_prob[e], 0 for n = 0
+ *
+ * A token is not routed where mask[g] is 0 or all its logits are -infinity: its
+ * ids are -1, its weights 0 and it is in no sum. An expert whose logit is
+ * -infinity is not chosen: slots that find no expert hold -1 and 0. NaN counts as
+ * the largest logit; a row with a NaN or +infinity has valid ids and weights NaN
+ * (and makes expert_prob and the loss NaN).
+ *
+ *   shape        E, S and K are used; the rest is only checked
+ *   type         of the logits (and of their gradient): MOE_F32 or MOE_BF16
+ *   row_stride   bytes from row to row, a multiple of the element's size
+ *   mask         uint8 [S] or NULL (all tokens)
+ *   topk_idx     int32 [S,K]; topk_weights float [S,K]; expert_count int32 [E + 1]
+ *   expert_prob  float [E] or NULL; loss float [1] or NULL
+ *   scratch      >= moe_gate_scratch_bytes(shape) bytes, 256-byte aligned; its
+ *                contents do not carry over between calls
+ *
+ * moe_gate_grad -- the gradient of the logits, from the gradients of the weights
+ * (as combine's gradient gives them) and of the loss. Ids and counts are
+ * constants of it:
+ *
+ *   a_k     = scale / D * (dw_k - (normalize ? sum over j of dw_j p[i_j] / D : 0))
+ *   c[e]    = dloss * balance * E * expert_count[e] / (K n) / n
+ *   dz[e]   = p[e] * (c[e] + sum over k with i_k = e of a_k - T),
+ *   T       = sum over e of p[e] c[e] + sum over k of p[i_k] a_k
+ *
+ * and 0 for a token that is not routed. Slots with an id outside [0, E) take no
+ * part (the forward call's -1, or slots that a program has dropped since: D is
+ * then the sum over the others); an id that is there twice counts twice.
+ *
+ *   logits, mask, normalize, scale, balance   as in the forward call
+ *   topk_idx, expert_count                    its results
+ *   dweights     float [S,K] or NULL (0); dloss float [1] or NULL (0)
+ *   dlogits      rows of `type`, dlogits_stride bytes apart; may not overlap logits
+ */
+#define MOE_F32 0
+#define MOE_BF16 1
+int64_t moe_gate_scratch_bytes(const moe_shape* shape);
+moe_status moe_gate(const moe_shape* shape, int32_t type, const void* logits, int64_t row_stride, const uint8_t* mask,
+                    int32_t normalize, float scale, float balance, int32_t* topk_idx, float* topk_weights,
+                    int32_t* expert_count, float* expert_prob, float* loss, void* scratch, int64_t scratch_bytes,
+                    void* stream);
+moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logits, int64_t row_stride,
+                         const uint8_t* mask, int32_t normalize, float scale, float balance, const int32_t* topk_idx,
+                         const int32_t* expert_count, const float* dweights, const float* dloss, void* dlogits,
+                         int64_t dlogits_stride, void* stream);
+
+/*
+ * moe_rms_norm -- root-mean-square norm of x + residual, rows of H bf16 values:
+ *
+ *   h = x + residual (binary32),  rstd = 1 / sqrt(mean h^2 + eps)
+ *   sum = bf16_rne(h),  y = bf16_rne(v),  v = h * rstd * weight
+ *   q_scale = max|v| / 127,  q = rint(v / q_scale) as dispatch's int8 payload has it
+ *             (a row of zeros: 0; a row whose v holds an infinity or a NaN: q_scale
+ *             NaN, codes 0)
+ *
+ * Every result may be NULL, but not all of them.
+ *
+ *   rows, H      rows >= 0; H a multiple of 8 (of 16 with q), at most MOE_MAX_HIDDEN
+ *   x, residual  bf16 bits; residual may be NULL (0)
+ *   weight       bf16 bits [H]
+ *   eps          finite, at least 2^-126
+ *   q, q_scale   int8 rows and one float per row, both or none
+ *   strides      bytes from row to row: multiples of 16, at least a row's bytes;
+ *                q_scale_stride a multiple of 4 >= 4 (int8 slots of dispatch hold the
+ *                scale behind the row: any pair of strides will do)
+ * sum may be x or residual itself, y may be x, residual or neither (not also sum);
+ * no other overlap.
+ *
+ * moe_rms_norm_grad -- its gradient at h (the sum as it was kept), without int8:
+ *
+ *   dh      = bf16_rne(rstd * (weight dy - h rstd^2 mean(weight dy h)) + dsum)
+ *   dweight = sum over rows of dy h rstd            (binary32, fixed order)
+ *
+ * dh is the gradient of x and of the residual alike. dsum: the gradient of the
+ * sum that was passed on, or NULL. dweight: float [H] or NULL; with it scratch
+ * holds moe_rms_norm_grad_scratch_bytes(rows, H) bytes (256-byte aligned). dh may be
+ * dy or dsum itself; no other overlap.
+ */
+moe_status moe_rms_norm(int64_t rows, int32_t H, float eps, const uint16_t* x, int64_t x_stride,
+                        const uint16_t* residual, int64_t residual_stride, const uint16_t* weight, uint16_t* sum,
+                        int64_t sum_stride, uint16_t* y, int64_t y_stride, int8_t* q, int64_t q_stride, float* q_scale,
+                        int64_t q_scale_stride, void* stream);
+int64_t moe_rms_norm_grad_scratch_bytes(int64_t rows, int32_t H);
+moe_status moe_rms_norm_grad(int64_t rows, int32_t H, float eps, const uint16_t* dy, int64_t dy_stride,
+                             const uint16_t* h, int64_t h_stride, const uint16_t* weight, const uint16_t* dsum,
+                             int64_t dsum_stride, uint16_t* dh, int64_t dh_stride, float* dweight, void* scratch,
+                             int64_t scratch_bytes, void* stream);
+
+/*
+ * moe_int8_pack / moe_int8_unpack -- bf16 rows to int8 with a scale per row, bit
+ * for bit as dispatch's int8 payload (quant = 1) has them, and back to
+ * bf16_rne(q * scale). A row that holds an infinity or a NaN gets the scale NaN and
+ * codes 0. Weights are packed by output channel: a channel is a row.
+ *
+ *   groups, rows   groups >= 0 operands of rows >= 0 rows each, back to back
+ *   width          a multiple of 16, at most MOE_INT8_MAX_WIDTH
+ *   gated          0, or 1: x holds all gate rows, then all up rows of an operand
+ *                  (rows % 32 == 0), the operand 16 gate rows and their 16 up rows by turns
+ *   x              bf16 bits, rows x_row_stride bytes apart (a multiple of 16, >= 2 * width)
+ *   q              int8, rows q_row_stride bytes apart (a multiple of 16, >= width)
+ *   scale          float, scale_stride bytes apart (a multiple of 4, >= 4)
+ *   plan           NULL, or a plan of moe_expert_plan for E experts (plan_ints words):
+ *                  only the rows that it gives to experts are read and written
+ *                  (groups = 1, gated = 0)
+ */
+#define MOE_INT8_MAX_WIDTH 32768
+moe_status moe_int8_pack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const uint16_t* x,
+                         int64_t x_row_stride, int8_t* q, int64_t q_row_stride, float* scale, int64_t scale_stride,
+                         int32_t E, const int32_t* plan, int64_t plan_ints, void* stream);
+moe_status moe_int8_unpack(int32_t groups, int64_t rows, int32_t width, int32_t gated, const int8_t* q,
+                           int64_t q_row_stride, const float* scale, int64_t scale_stride, uint16_t* x,
+                           int64_t x_row_stride, int32_t E, const int32_t* plan, int64_t plan_ints, void* stream);
+
+/*
+ * moe_expert_product_int8 -- the linear layer on int8 rows and weights, a scale per
+ * row and per output channel. For every row r of expert e:
+ *
+ *   v[n] = (sum over k of wq_e[n][k] * xq[r][k]) * ws_e[n] * xs[r]
+ *          (products exact, binary32 sum: exact below 2^24)
+ *   gated = 0: y[r][n] = bf16_rne(v[n]),               n < N
+ *   gated = 1: y[r][i] = bf16_rne(silu(gate_i) * up_i), i < N / 2, gate_i and up_i the
+ *              i-th gate and up row's v (weights held by turns, as moe_int8_pack
+ *              makes them), silu(a) = a / (1 + e^-a)
+ *
+ *   E, N, K        experts, weight rows per expert (a multiple of 32, at most
+ *                  2 * MOE_INT8_MAX_WIDTH) and row width (a multiple of 16, at most
+ *                  MOE_INT8_MAX_WIDTH)
+ *   wq, ws         int8 [E,N,K], float [E,N]
+ *   xq             int8 rows, x_row_stride bytes apart (a multiple of 16, >= K)
+ *   xs             float, xs_stride bytes apart (a multiple of 4, >= 4). Of dispatch's
+ *                  int8 slots xq is the arena, xs the arena + Ceil(H, 32), and both
+ *                  strides moe_slot_stride(H, 1)
+ *   rows           rows of xq and y (with 0 nothing is enqueued, and err is not written)
+ *   plan           moe_expert_plan's for E experts, plan_ints words; or NULL with E = 1:
+ *                  all rows are the one expert's (a dense layer)
+ *   y              bf16 rows, y_row_stride bytes apart (a multiple of 16, at least 2
+ *                  bytes per value); rows that are no expert's are not written
+ *   err            int32 device word or NULL: MOE_ERR_CAPACITY for a tile outside the rows
+ *                  or of no expert (skipped), MOE_ERR_DEVICE_TIMEOUT
+ * A row whose scale is NaN gives NaN; no row affects another.
+ */
+moe_status moe_expert_product_int8(int32_t E, int32_t N, int32_t K, int32_t gated, const int8_t* wq, const float* ws,
+                                   const int8_t* xq, int64_t x_row_stride, const float* xs, int64_t xs_stride,
+                                   int64_t rows, const int32_t* plan, int64_t plan_ints, uint16_t* y,
+                                   int64_t y_row_stride, int32_t* err, void* stream);
+
+/*
  * moe_pad_partitions -- fixed-length receive partitions ("Ascend DeepEP MoE
  * Dispatch Optimization", section "输出长度有动态和固定两种模式": with a fixed
  * output length, num_worst_tokens, the host reads no count back and the rows
