@@ -66,7 +66,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     host = platform.machine()
     if not os.path.exists(stamp) or open(stamp).read().strip() != host:
         force = True
-    headers = [os.path.join(INCLUDE, "moe.h"), *(os.path.join(CSRC, h) for h in ("moe_device.cuh", "experts.cuh", "fp4.cuh", "int8.cuh"))]
+    headers = [os.path.join(INCLUDE, "moe.h"), *(os.path.join(CSRC, h) for h in ("moe_device.cuh", "experts.cuh", "fp4.cuh", "int8.cuh", "tensor.cuh"))]
     cc = nvcc()
     jobs = []
     objs = []

@@ -44,6 +44,7 @@ cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const
 // Test hook behind moe_test_product_wait (this host thread's next product).
 constexpr int kProductWarps = 12;  // warps of a product's CTA
 void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp);
+void take_product_wait_test(int64_t* wait_cycles, int32_t* quit_warp);  // leaves both where nothing is armed
 
 // Rows and plan of the expert layer from topk_idx alone (one partition, experts
 // at multiples of MOE_FP4_ROW_TILE rows).

@@ -30,12 +30,10 @@
 // tensor pipe's pace; 256 columns are the widest instruction. Where rows of codes are
 // no multiple of 128 bytes each load touches two lines of L2: 44800 rows 5984 -> 2048
 // 226 us, 7168 -> 2048 214.
-#include <cuda.h>
-#include <cuda_bf16.h>
-
 #include <atomic>
 
 #include "fp4.cuh"
+#include "tensor.cuh"
 
 namespace moe {
 namespace {
@@ -58,7 +56,6 @@ static_assert(2 * 32 * kPackStride <= kOutBytes, "staging");
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes;
 constexpr int kAcc1 = 224;                   // second place of the sums
-constexpr long long kWaitCycles = 1ll << 32;
 constexpr int kScaleCol = 480;               // scales of a stage: 8 columns of the weights', 16 of the rows'
 
 struct ProductArgs {
@@ -97,82 +94,6 @@ struct Unit {
 
 __device__ __forceinline__ uint32_t mma_n(int32_t rows) { return (rows + 31) & ~31; }
 
-// Arrival on a barrier of the leading CTA. What it hands over is tensor memory that
-// has been read (ordered by the tcgen05 fences), not data, so it releases at the
-// CTA's scope: at the cluster's it waited for the thread's global stores, about
-// a microsecond per tile (128 tokens, 1024 -> 14336: 456 us against 299).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// A wait has run out: the CTA's other roles are told, and the caller.
-__device__ __forceinline__ void give_up(Bars* b, const ProductArgs& a) {
-    *reinterpret_cast<volatile uint32_t*>(&b->abort) = 1u;
-    raise_error(a.err, MOE_ERR_DEVICE_TIMEOUT);
-}
-
-// Bounded wait of a whole warp, by polls and by time (about two seconds: a poll
-// may itself sleep); false if it ran out or another role of the CTA gave up.
-__device__ __forceinline__ bool wait_for(Bars* b, uint64_t* bar, uint32_t parity, const ProductArgs& a) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-    const long long began = clock64();
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&b->abort) != 0u)) return false;
-        if (__any_sync(0xffffffffu, clock64() - began > a.wait_cycles)) break;
-    }
-    give_up(b, a);
-    return false;
-}
-
-// Whether all 128 threads that meet at barrier `id` say so.
-__device__ __forceinline__ bool all_agree(int id, bool yes) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %2, 0;\n\t"
-        "bar.red.and.pred q, %1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(id), "r"(static_cast<uint32_t>(yes))
-        : "memory");
-    return all != 0;
-}
-
-// After a failed wait: what is in flight ends within microseconds, or (a peer
-// gave up first) never.
-__device__ __forceinline__ void drained(uint64_t* bar, uint32_t parity) {
-    const long long began = clock64();
-    while (!__any_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity)) &&
-           !__any_sync(0xffffffffu, clock64() - began > kWaitCycles / 64)) {
-    }
-}
-
-// One lane of a converged warp. The loading and the issuing warp run their
-// loops as whole warps on warp-uniform values and only the instructions
-// themselves are one lane's: in a branch of one lane the compiler cannot keep
-// descriptors in uniform registers, and each product then took about 100
-// cycles to issue and each scale copy 80 (of 128 cycles of work; measured).
-__device__ __forceinline__ bool elected() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-
-__device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 // TMA tile loads into this CTA's shared memory, counted on the barrier of the
 // pair's leading CTA.
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -189,11 +110,7 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// Shared-memory matrix descriptors: rows of 128 bytes, swizzled, 8 rows to
-// 1024 bytes; and scale chunks, 8 lanes of 16 bytes to 128 bytes.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Scale chunks, 8 lanes of 16 bytes to 128 bytes.
 __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
     return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (8ull << 32) | (1ull << 46);
 }
@@ -215,46 +132,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 
 __device__ __forceinline__ void scales_to_tmem(uint32_t col, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
-}
-
-// Arrives on `bar` of both CTAs once every product and copy issued so far is done.
-__device__ __forceinline__ void commit_to(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 16 lanes x 16 columns of tensor memory: v[4 i + j], column 8 i + 2 (lane % 4) + j % 2,
-// lane row lane / 4 + 8 (j / 2).
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(addr)
-                 : "memory");
-}
-
-// Four 8 x 8 blocks of 16-bit values, transposed: lane 8 q + j gives the address
-// of the 16 bytes that column j of block q goes to.
-__device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
-                 "r"(c), "r"(d)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// silu(g) * u. e^-|g| <= 1, so nothing overflows and the denominator is in [1, 2].
-__device__ __forceinline__ float gate_times_up(float g, float u) {
-    const float e = __expf(-fabsf(g));
-    return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
 }
 
 // A pair's units, first, first + step, .. of the launch's. They run through groups of
@@ -634,23 +511,6 @@ product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap wmap, co
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The CUDA driver's encoder, looked up once per process.
-EncodeTiled encoder() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // A map of codes (bytes, swizzled rows of 128) or scales (32-bit words, as they lie).
 bool encode(CUtensorMap* map, bool codes, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
@@ -719,16 +579,19 @@ void arm_product_wait_test(uint32_t wait_cycles, int32_t quit_warp) {
     t_test_quit_warp = quit_warp;
 }
 
+void take_product_wait_test(int64_t* wait_cycles, int32_t* quit_warp) {
+    if (t_test_wait_cycles == 0) return;
+    *wait_cycles = t_test_wait_cycles;
+    *quit_warp = t_test_quit_warp;
+    t_test_wait_cycles = 0;
+    t_test_quit_warp = -1;
+}
+
 cudaError_t launch_product(int32_t E, int32_t N, int32_t K, int32_t gated, const uint8_t* wq, const uint8_t* wsf,
                            const uint8_t* xq, const uint8_t* xsf, int64_t rows, const int32_t* plan, int64_t plan_ints,
                            uint16_t* y, int64_t y_stride, uint8_t* hq, uint8_t* hsf, int32_t* err, cudaStream_t stream) {
     ProductArgs a{E, N, K, plan_capacity(E, plan_ints), rows, plan, y, y_stride, hq, hsf, err, kWaitCycles, -1};
-    if (t_test_wait_cycles != 0) {  // one call armed by moe_test_product_wait
-        a.wait_cycles = t_test_wait_cycles;
-        a.quit_warp = t_test_quit_warp;
-        t_test_wait_cycles = 0;
-        t_test_quit_warp = -1;
-    }
+    take_product_wait_test(&a.wait_cycles, &a.quit_warp);
     if (a.tile_cap == 0) return cudaSuccess;
     // Rows that the plan has room for: it has one tile per expert and one per 256 rows.
     const bool four = four_tiles(static_cast<double>(a.tile_cap - E) * kPlanTileRows, N, K);

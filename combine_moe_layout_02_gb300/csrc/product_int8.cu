@@ -3,102 +3,646 @@
 //   v[r][n] = ws_e[n] * xs[r] * sum over k of w_e[n][k] * x[r][k]
 //   y[r] = bf16_rne(v[r]), or, gated, bf16_rne(silu(gate) * up) of the pairs.
 //
-// 64 weight rows x 64 rows per block, four products an instruction.
-#include <cuda_bf16.h>
+// sm_103a's tensor cores multiply no 8-bit integers, but every int8 is an f16 and
+// a product of two is exact in binary32, and so is a sum below 2^24 of them: the
+// codes become f16 on their way to tcgen05.mma kind::f16. (An int8 as two e4m3
+// parts would take four products at twice the rate.)
+//
+// A pair of CTAs (one per SM) computes 256 weight rows x up to 256 of an expert's
+// rows; the weights are the M side, so that few rows cost a thin instruction. Each
+// CTA has its 128 weight rows and half of the rows. Per 128 of K: warp 0 loads codes
+// (TMA, a ring of stages), warps 8-15 turn them into f16 -- the weights' straight
+// into tensor memory, from where the instruction takes its A side, the rows' into
+// shared memory, swizzled as its B side is --, warp 1 of the leading CTA issues
+// the products of K = 16, warps 4-7 of both CTAs take the sums out, times the
+// scales. Either group of four converting warps has a half of every 128 of K and a
+// place of its own for the result, so one converts while the other's is multiplied.
+// Weights through tensor memory save shared memory's rate: a stage's 64 of K are 16
+// KB of codes in, 16 out, 16 of f16 rows in and 16 out, 64 KB in the 512 cycles of
+// its products, at 128 bytes a cycle.
+//
+// Tensor memory: sums in two places, columns 0 and 192 on, which share 64 columns
+// (read first and given back early), and the f16 weights' two places of 32 columns.
+#include <atomic>
+
+#include <cuda_fp16.h>
 
 #include "fp4.cuh"
-#include "int8.cuh"
+#include "tensor.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 64, kPad = kStep + 4;
+constexpr int kMTile = 256;                 // weight rows of a CTA pair
+constexpr int kStageK = 128;                // codes of K per stage: one 128-byte swizzle row
+constexpr uint32_t kWBytes = 128 * 128;     // a CTA's weight rows of a stage
+constexpr uint32_t kXBox = 32 * 128;        // 32 rows of a stage
+constexpr uint32_t kOutStride = 80;         // bytes per staged row: 64 and a shift of 4 banks per row
+constexpr uint32_t kOutBytes = 4 * 16 * kOutStride;
+constexpr uint32_t kScaleBytes = 4 * kPlanTileRows * 4;  // the rows' scales, for each of four warps
+constexpr uint32_t kBarBytes = 512;
+constexpr int kAcc1 = 128;  // second place of the sums
+constexpr int kSharedChunks = (256 - kAcc1) / 16;
+constexpr int kMostSlots = 8, kMostStages = 6;
 
-__device__ __forceinline__ float gate_times_up(float g, float u) {
-    const float e = __expf(-fabsf(g));
-    return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
+// Up to 256 rows to a tile, or (THIN) up to 128: half the rows in shared memory make
+// room for more stages, half the sums in tensor memory for more places of f16 weights.
+template <bool THIN>
+struct Cut {
+    static constexpr int kRows = THIN ? 128 : 256;
+    static constexpr int kStages = THIN ? 6 : 4;
+    static constexpr int kGroups = THIN ? 4 : 2;                     // of four converting warps: two take turns at the halves of K
+    static constexpr int kThreads = 256 + 128 * kGroups;
+    static constexpr int kSlots = THIN ? 8 : 4;                      // places of f16 operands, 2 each group's
+    static constexpr int kACol = THIN ? 256 : 384;                   // the f16 weights, 32 columns a place
+    static constexpr uint32_t kStageBytes = kWBytes + kRows / 64 * kXBox;
+    static constexpr uint32_t kHalfBytes = kRows / 2 * 128;          // a CTA's rows of 64 f16
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kSlots * kHalfBytes + kOutBytes + kScaleBytes + kBarBytes;
+    static_assert(kACol + 32 * kSlots == 512 && kSlots <= kMostSlots && kStages <= kMostStages && kSmem <= 227 * 1024, "room");
+};
+
+struct Args {
+    ProductInt8Args p;
+    int32_t shift;        // a dense call's row tiles are 256 / 2^shift rows
+    int64_t wait_cycles;  // bound of a wait (kWaitCycles)
+    int32_t quit_warp;    // test hook: a warp of each CTA that acts as if its first wait had run out, or -1
+    int32_t* err;
+};
+
+// Barriers of a CTA, and its abort flag.
+struct Bars {
+    uint64_t full[kMostStages];   // each CTA: its loads of a stage have landed
+    uint64_t empty[kMostStages];  // each CTA: both groups have read a stage
+    uint64_t ready[kMostSlots];   // leading CTA: both CTAs' f16 operands of a place are there
+    uint64_t used[kMostSlots];    // each CTA: the products that read a place are done
+    uint64_t acc_full[2];     // each CTA: a tile's sums are complete
+    uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place of the sums
+    uint64_t shared_free;     // leading CTA: both CTAs have read the tile's part of the shared columns
+    uint64_t drain;           // leading CTA, after a failed wait: products in flight are done
+    uint32_t tmem;
+    uint32_t abort;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+
+// One tile of work.
+struct Unit {
+    int32_t e, row, n, m0;  // expert, first row, rows, first weight row of the pair
+};
+
+__device__ __forceinline__ uint32_t mma_n(int32_t rows) { return (rows + 31) & ~31; }
+
+// TMA tile loads into this CTA's shared memory, counted on its own barrier.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(256) product_int8_kernel(const ProductInt8Args a) {
-    pdl_wait_then_release();
-    __shared__ __align__(16) int8_t ws[kTile][kPad], xs[kTile][kPad];
-    __shared__ float v[kTile][kTile + 1];
-    const int ntiles = static_cast<int>(ceil_div(a.N, kTile));
-    const int64_t unit = blockIdx.x;
-    const int n0 = static_cast<int>(unit % ntiles) * kTile;
-    const int64_t part = unit / ntiles;  // a quarter of a row tile
-    int4 t;
-    if (a.plan) {
-        if (part / 4 >= __ldg(a.plan)) return;
-        t = __ldg(reinterpret_cast<const int4*>(a.plan + plan_tiles_at(a.E)) + part / 4);
-    } else {
-        const int64_t left = a.rows - part / 4 * kPlanTileRows;
-        t = make_int4(0, static_cast<int32_t>(part / 4 * kPlanTileRows), static_cast<int32_t>(left < kPlanTileRows ? left : kPlanTileRows), 0);
-    }
-    if (t.x < 0 || t.x >= a.E || t.y < 0 || t.z < 0 || t.z > kPlanTileRows || t.y + static_cast<int64_t>(t.z) > a.rows) {
-        raise_error(a.err, MOE_ERR_CAPACITY);
-        return;
-    }
-    const int r0 = static_cast<int>(part % 4) * kTile, rows = min(kTile, t.z - r0);
-    if (rows <= 0) return;
-    const int8_t* w = a.wq + (static_cast<int64_t>(t.x) * a.N) * a.K;
-    const int64_t row0 = t.y + r0;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int32_t acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kStep) {
-        const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
-        uint4 wv = make_uint4(0, 0, 0, 0), xv = wv;
-        if (n0 + r < a.N && k0 + c < a.K) wv = *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n0 + r) * a.K + k0 + c);
-        if (r < rows && k0 + c < a.K) xv = *reinterpret_cast<const uint4*>(a.xq + (row0 + r) * a.x_stride + k0 + c);
-        const uint32_t wa[4] = {wv.x, wv.y, wv.z, wv.w}, xa[4] = {xv.x, xv.y, xv.z, xv.w};
-        __syncthreads();
+// f16 x f16 to binary32, M = 256, N columns, A in tensor memory, B K-major.
+__device__ __forceinline__ uint32_t instr(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | (16u << 24); }
+
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// Four codes to four f16: code + 128 is the low byte of the f16 1024 + (code + 128).
+__device__ __forceinline__ void halves4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    const uint32_t b = codes ^ 0x80808080u;
+    const uint32_t u = __byte_perm(b, 0x64646464u, 0x4140), v = __byte_perm(b, 0x64646464u, 0x4342);
+    const uint32_t off = 0x64806480u;  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&off));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint4 read_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void write_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 64 codes of a swizzled row (its half `half`) to 64 f16, two to a word.
+__device__ __forceinline__ void row_halves(uint32_t row_addr, int row, int half, uint32_t (&h)[32]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint32_t*>(&ws[r][c + 4 * i]) = wa[i];
-            *reinterpret_cast<uint32_t*>(&xs[r][c + 4 * i]) = xa[i];
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v = read_shared(row_addr + (((4 * half + c) ^ (row & 7)) << 4));
+        halves4(v.x, h[8 * c], h[8 * c + 1]);
+        halves4(v.y, h[8 * c + 2], h[8 * c + 3]);
+        halves4(v.z, h[8 * c + 4], h[8 * c + 5]);
+        halves4(v.w, h[8 * c + 6], h[8 * c + 7]);
+    }
+}
+
+// A lane's 32 words to 32 columns of tensor memory.
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&h)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]), "r"(h[8]), "r"(h[9]),
+        "r"(h[10]), "r"(h[11]), "r"(h[12]), "r"(h[13]), "r"(h[14]), "r"(h[15]), "r"(h[16]), "r"(h[17]), "r"(h[18]),
+        "r"(h[19]), "r"(h[20]), "r"(h[21]), "r"(h[22]), "r"(h[23]), "r"(h[24]), "r"(h[25]), "r"(h[26]), "r"(h[27]),
+        "r"(h[28]), "r"(h[29]), "r"(h[30]), "r"(h[31])
+        : "memory");
+}
+
+// A pair's units, first, first + step, .. of the launch's; the weight rows are the
+// inner index. A role steps from unit to unit without a division and holds the next
+// one's plan words while it works on the current one. A plan's tile of more than
+// ROWS rows is one unit of several tiles.
+template <int ROWS>
+struct Units {
+    uint32_t per, part, in, step_part, step_in, left;
+    int4 tile;
+    Unit rest;  // what the current unit has left
+
+    __device__ __forceinline__ Units(const Args& a, uint32_t parts, uint32_t mtiles, uint32_t first, uint32_t step)
+        : per(mtiles), tile(make_int4(0, 0, 0, 0)), rest{0, 0, 0, 0} {
+        const uint32_t units = parts * mtiles;
+        left = first < units ? (units - first - 1) / step + 1 : 0;
+        part = first / per;
+        in = first - part * per;
+        step_part = step / per;
+        step_in = step - step_part * per;
+        fetch(a);
+    }
+    __device__ __forceinline__ void fetch(const Args& a) {
+        if (left == 0) return;
+        if (a.p.plan) {
+            tile = __ldg(reinterpret_cast<const int4*>(a.p.plan + plan_tiles_at(a.p.E)) + part);
+        } else {
+            const int32_t size = kPlanTileRows >> a.shift;
+            const int64_t first = static_cast<int64_t>(part) * size, rows = a.p.rows - first;
+            tile = make_int4(0, static_cast<int32_t>(first), static_cast<int32_t>(rows < size ? rows : size), 0);
         }
-        __syncthreads();
-        for (int k = 0; k < kStep; k += 4) {
-            int32_t p[4], q[4];
+    }
+    __device__ __forceinline__ bool more() const { return left > 0 || rest.n > 0; }
+    // The current tile, the same in every lane, or none (n = 0) where the plan's
+    // tile is no tile of these rows; then on to the next.
+    __device__ __forceinline__ Unit take(const Args& a) {
+        Unit o = rest;
+        if (rest.n == 0) {
+            o = Unit{uniform(tile.x), uniform(tile.y), uniform(tile.z), static_cast<int32_t>(in) * kMTile};
+            if (o.e < 0 || o.e >= a.p.E || o.row < 0 || o.n < 0 || o.n > kPlanTileRows ||
+                o.row + static_cast<int64_t>(o.n) > a.p.rows) {
+                raise_error(a.err, MOE_ERR_CAPACITY);
+                o.n = 0;
+            }
+            --left;
+            part += step_part;
+            in += step_in;
+            if (in >= per) {
+                in -= per;
+                ++part;
+            }
+            fetch(a);
+        }
+        if (ROWS < kPlanTileRows) {
+            const int32_t n = min(o.n, ROWS);
+            rest = Unit{o.e, o.row + n, o.n - n, o.m0};
+            o.n = n;
+        }
+        return o;
+    }
+};
+
+template <bool GATED, bool THIN>
+__global__ void __launch_bounds__(Cut<THIN>::kThreads, 1)
+product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+    constexpr int kStages = Cut<THIN>::kStages, kSlots = Cut<THIN>::kSlots, kACol = Cut<THIN>::kACol, kRows = Cut<THIN>::kRows;
+    constexpr uint32_t kStageBytes = Cut<THIN>::kStageBytes, kHalfBytes = Cut<THIN>::kHalfBytes, kTurns = Cut<THIN>::kGroups / 2;
+    extern __shared__ unsigned char smem_raw[];
+    // The same offset in both CTAs of the pair (their shared windows are alike).
+    unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    unsigned char* halves = smem + kStages * kStageBytes;
+    unsigned char* out_stage = halves + kSlots * kHalfBytes;
+    float* scales = reinterpret_cast<float*>(out_stage + kOutBytes);
+    Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes + kScaleBytes);
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t cta = cluster_ctarank();  // of the pair; 0 leads
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 8);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&bars->ready[i], 8);
+            mbar_init(&bars->used[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->acc_full[i], 1);
+            mbar_init(&bars->acc_empty[i], 8);
+        }
+        mbar_init(&bars->shared_free, 8);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == 3 && elected())
+        for (const CUtensorMap* map : {&wmap, &xmap}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    pdl_wait_then_release();
+
+    int32_t tiles = a.p.tile_cap;
+    if (a.p.plan) {
+        const int32_t planned = uniform(__ldg(a.p.plan));
+        tiles = planned < 0 ? 0 : (planned > tiles ? tiles : planned);
+    }
+    const uint32_t parts = static_cast<uint32_t>(tiles), mtiles = (a.p.N + kMTile - 1) / kMTile;
+    const uint32_t step = gridDim.x / 2, first = blockIdx.x / 2;
+    const int nstages = static_cast<int>(ceil_div(a.p.K, kStageK));
+    const bool short_end = a.p.K - (nstages - 1) * kStageK <= kStageK / 2;  // the last stage has one half
+    if (warp == a.quit_warp) give_up(bars, a);
+
+    if (warp == 0) {
+        uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
+        int64_t issued = 0;
+        bool ok = warp != a.quit_warp;
+        Units<kRows> list(a, parts, mtiles, first, step);
+        while (ok && list.more()) {
+            const Unit t = list.take(a);
+            if (t.n == 0) continue;
+            const uint32_t n = mma_n(t.n);
+            const int boxes = static_cast<int>((n / 2 + 31) / 32);
+            const uint32_t bytes = kWBytes + boxes * kXBox;
+            const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
+            const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
+            for (int k = 0; k < nstages; ++k) {
+                if (issued >= kStages && !wait_here(bars, &bars->empty[s], phase ^ 1, a)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = smem_addr(smem + s * kStageBytes), bar = smem_addr(&bars->full[s]);
+                if (elected()) {
+                    mbar_arrive_expect_tx(&bars->full[s], bytes);
+                    load_3d(base, &wmap, k * kStageK, m0, t.e, bar);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = *reinterpret_cast<const int32_t*>(&ws[tx + 16 * i][k]);
-                q[i] = *reinterpret_cast<const int32_t*>(&xs[ty + 16 * i][k]);
+                    for (int i = 0; i < kRows / 64; ++i)
+                        if (i < boxes) load_2d(base + kWBytes + i * kXBox, &xmap, k * kStageK, x0 + 32 * i, bar);
+                }
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) {  // bounded: what is in flight lands before the pair ends
+            for (int i = 0; i < kStages && i < issued; ++i) {
+                s = s == 0 ? kStages - 1 : s - 1;
+                if (s == kStages - 1) phase ^= 1;
+                drained(&bars->full[s], phase);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && cta == 0) {
+        uint32_t i = 0, last_n = 0;  // i: tiles so far
+        uint32_t turn = 0, uses[2 * kTurns] = {};
+        bool ok = warp != a.quit_warp;
+        Units<kRows> list(a, parts, mtiles, first, step);
+        while (ok && list.more()) {
+            const Unit t = list.take(a);
+            if (t.n == 0) continue;
+            const uint32_t n = mma_n(t.n), place = i & 1;
+            const uint32_t acc = tmem + (place ? kAcc1 : 0);
+            // The place's last sums have been read; and, where this tile and
+            // the one before it both reach the shared columns, that one's
+            // part of them too.
+            if (i >= 2) ok = wait_here(bars, &bars->acc_empty[place], ((i >> 1) - 1) & 1, a);
+            if (ok && i >= 1 && (place ? last_n : n) > static_cast<uint32_t>(kAcc1))
+                ok = wait_here(bars, &bars->shared_free, (i - 1) & 1, a);
+            tc_fence_after();
+            last_n = n;
+            for (int k = 0; ok && k < nstages; ++k) {
+                const bool end = k == nstages - 1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1 && end && short_end) break;
+                    uint32_t u = uses[half];
+                    if (kTurns > 1 && turn) u = uses[2 * kTurns - 2 + half];
+                    const uint32_t slot = 4 * turn + 2 * half + (u & 1);
+                    if (!wait_here(bars, &bars->ready[slot], u >> 1 & 1, a)) {
+                        ok = false;
+                        break;
+                    }
+                    if (kTurns > 1 && turn)
+                        ++uses[2 * kTurns - 2 + half];
+                    else
+                        ++uses[half];
+                    tc_fence_after();
+                    const uint64_t b = desc_rows(smem_addr(halves + slot * kHalfBytes));
+                    if (elected()) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma(acc, tmem + kACol + 32 * slot + 8 * j, b + 2 * j, instr(n), k > 0 || half > 0 || j > 0);
+                        commit_to(&bars->used[slot]);
+                        if (end && (half == 1 || short_end)) commit_to(&bars->acc_full[place]);
+                    }
+                    __syncwarp();
+                }
+                if (kTurns > 1) turn ^= 1;
+            }
+            ++i;
+        }
+        if (!ok) {  // bounded: products in flight end before tensor memory is given back
+            if (elected())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_addr(&bars->drain))
+                             : "memory");
+            drained(&bars->drain, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // Four warps a group: of every kTurns stages one, of its K one half.
+        const int group = (warp - 8) >> 2, half = group & 1, w = warp & 3;
+        const int row = w * 32 + lane;  // lane of tensor memory, and row of either operand
+        const uint32_t to = tmem + kACol + 64 * group + (static_cast<uint32_t>(w * 32) << 16);
+        const uint32_t mine = smem_addr(halves) + 2 * group * kHalfBytes + row * 128;
+        const uint32_t ready = cluster_map(bars->ready + 2 * group, 0);
+        uint32_t s = 0, phase = 0, uses = 0, turn = 0;
+        bool ok = warp != a.quit_warp;
+        Units<kRows> list(a, parts, mtiles, first, step);
+        while (ok && list.more()) {
+            const Unit t = list.take(a);
+            if (t.n == 0) continue;
+            const bool mine_too = row < static_cast<int>(mma_n(t.n) / 2);
+            for (int k = 0; k < nstages; ++k) {
+                const uint32_t at = s, parity = phase;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                if (kTurns > 1) {
+                    const uint32_t now = turn;
+                    turn ^= 1;
+                    if (now != static_cast<uint32_t>(group >> 1)) continue;
+                }
+                if (!wait_here(bars, &bars->full[at], parity, a)) {
+                    ok = false;
+                    break;
+                }
+                const bool skip = half == 1 && short_end && k == nstages - 1;
+                if (!skip) {
+                    const uint32_t slot = uses & 1;
+                    if (uses >= 2 && !wait_here(bars, &bars->used[2 * group + slot], (uses / 2 - 1) & 1, a)) {
+                        ok = false;
+                        break;
+                    }
+                    ++uses;
+                    const uint32_t base = smem_addr(smem + at * kStageBytes) + row * 128;
+                    uint32_t h[32];
+                    row_halves(base, row, half, h);
+                    tc_fence_after();
+                    tmem_store(to + 32 * slot, h);
+                    if (mine_too) {
+                        row_halves(base + kWBytes, row, half, h);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            write_shared(mine + slot * kHalfBytes + ((c ^ (row & 7)) << 4), h[4 * c], h[4 * c + 1],
+                                         h[4 * c + 2], h[4 * c + 3]);
+                    }
+                    // Seen by the tensor cores once the arrival is: every lane's f16 rows and tensor memory.
+                    fence_proxy_async_smem();
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready + 8 * slot);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->empty[at]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int w = warp & 3;  // lane quarter
+        unsigned char* stage_ptr = out_stage + w * 16 * kOutStride;
+        const uint32_t stage = smem_addr(stage_ptr);
+        float* xs = scales + w * kPlanTileRows;
+        // stmatrix: block q of 8 lanes; ungated blocks are the warp's four
+        // groups of 8 weight rows, gated two groups of each of two column blocks.
+        const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
+        const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
+        uint32_t i = 0;
+        Units<kRows> list(a, parts, mtiles, first, step);
+        while (list.more()) {
+            const Unit t = list.take(a);
+            if (t.n == 0) continue;
+            const uint32_t place = i & 1;
+            const int m = t.m0 + static_cast<int>(cta) * 128 + w * 32;  // the warp's weight rows
+            // Scales, while the sums are formed: four weight rows' per lane, all rows' per warp.
+            float ws[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = m + (lane >> 2) + 8 * j;
+                ws[j] = n < a.p.N ? __ldg(a.p.ws + static_cast<int64_t>(t.e) * a.p.N + n) : 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < kPlanTileRows / 32; ++j) {
+                const int r = lane + 32 * j;
+                if (r < t.n) xs[r] = __ldg(reinterpret_cast<const float*>(a.p.xs + (t.row + static_cast<int64_t>(r)) * a.p.xs_stride));
+            }
+            __syncwarp();
+            if (warp == a.quit_warp || !wait_here(bars, &bars->acc_full[place], (i >> 1) & 1, a)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
+            const int chunks = static_cast<int>(mma_n(t.n) / 16);
+            // Place 0 has the shared columns at its end, place 1 at its start:
+            // they are read first.
+            for (int q = 0; q < chunks; ++q) {
+                const int c = place ? q : chunks - 1 - q;
+                uint32_t v[2][8];
+                tmem_load(acc + 16 * c, v[0]);
+                tmem_load(acc + 16 * c + (16u << 16), v[1]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (q == min(kSharedChunks, chunks) - 1) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
+                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], 0));
+                }
+                const int c0 = 16 * c;  // first of the chunk's rows
+                if (m >= a.p.N || c0 >= t.n) continue;
+                float f[2][8];  // v times the scales
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(p[i], q[j], acc[i][j]);
+                for (int b = 0; b < 2; ++b) {
+                    const float2 x = *reinterpret_cast<const float2*>(xs + c0 + 8 * b + 2 * (lane & 3));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f[h][4 * b + j] = __uint_as_float(v[h][4 * b + j]) * ws[2 * h + (j >> 1)] * (j & 1 ? x.y : x.x);
+                }
+                uint8_t* y = reinterpret_cast<uint8_t*>(a.p.y) + (t.row + c0) * a.p.y_stride + (GATED ? m : 2 * m);
+                if constexpr (GATED) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            h[2 * b + j] = bf16_pair(gate_times_up(f[0][4 * b + 2 * j], f[1][4 * b + 2 * j]),
+                                                     gate_times_up(f[0][4 * b + 2 * j + 1], f[1][4 * b + 2 * j + 1]));
+                    store_turned(to_gated, h[0], h[1], h[2], h[3]);
+                    __syncwarp();
+                    const int r = lane >> 1;
+                    if (c0 + r < t.n)
+                        *reinterpret_cast<uint4*>(y + r * a.p.y_stride + (lane & 1) * 16) =
+                            *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 1) * 16);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) h[g] = bf16_pair(f[g >> 1][4 * b + 2 * (g & 1)], f[g >> 1][4 * b + 2 * (g & 1) + 1]);
+                        store_turned(to + 8 * b * kOutStride, h[0], h[1], h[2], h[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int r = 8 * p + (lane >> 2);
+                        if (c0 + r < t.n)
+                            *reinterpret_cast<uint4*>(y + r * a.p.y_stride + (lane & 3) * 16) =
+                                *reinterpret_cast<const uint4*>(stage_ptr + r * kOutStride + (lane & 3) * 16);
+                    }
+                }
+                __syncwarp();  // the staged rows have been read
+            }
+            ++i;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tx + 16 * i, r = ty + 16 * j;
-            if (n < a.N && r < rows)
-                v[r][tx + 16 * i] = static_cast<float>(acc[i][j]) * __ldg(a.ws + static_cast<int64_t>(t.x) * a.N + n) *
-                                    *reinterpret_cast<const float*>(a.xs + (row0 + r) * a.xs_stride);
-        }
+
+    // After a failed wait: loads that nobody waits for land before the cluster ends.
+    if (*reinterpret_cast<volatile uint32_t*>(&bars->abort) != 0u)
+        for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    // No CTA may leave while another's copies, products or arrivals can reach it.
+    tc_fence_before();
     __syncthreads();
-    const int width = a.gated ? kTile / 2 : kTile;
-    for (int i = threadIdx.x; i < rows * width; i += blockDim.x) {
-        const int r = i / width, c = i % width;
-        const int at = a.gated ? c / 16 * 32 + c % 16 : c;
-        if (n0 + at >= a.N) continue;
-        const float o = a.gated ? gate_times_up(v[r][at], v[r][at + 16]) : v[r][at];
-        uint16_t* y = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(a.y) + (row0 + r) * a.y_stride);
-        y[(a.gated ? n0 / 2 : n0) + c] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// A map of codes: swizzled rows of 128 bytes.
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs that can be resident at once on the current device (cached); allows the kernel its shared memory.
+template <bool GATED, bool THIN>
+int resident_pairs() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
+    if (prepare_kernel(reinterpret_cast<const void*>(product_int8_kernel<GATED, THIN>), Cut<THIN>::kSmem, Cut<THIN>::kThreads, nullptr) != cudaSuccess)
+        return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(Cut<THIN>::kThreads);
+    cfg.dynamicSmemBytes = Cut<THIN>::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, product_int8_kernel<GATED, THIN>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (slot) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Rows of a dense call's tiles, 256 / 2^shift, so that the pairs have work: of the sizes
+// the one whose rounds of units are over first, a unit taking 2 cycles per row and 64 of K
+// but no less than the weights' conversion does.
+int32_t tile_shift(const ProductInt8Args& p, int pairs) {
+    int32_t best = 0;
+    double least = 0;
+    for (int32_t shift = 0; shift <= 3; ++shift) {
+        const int32_t size = kPlanTileRows >> shift;
+        const int64_t units = ceil_div(p.rows, size) * ceil_div(p.N, kMTile);
+        const double time = static_cast<double>(ceil_div(units, pairs)) * (2 * size > 230 ? 2 * size : 230);
+        if (shift == 0 || time < least) {
+            best = shift;
+            least = time;
+        }
     }
+    return best;
+}
+
+template <bool GATED, bool THIN>
+cudaError_t launch_pairs(Args a, cudaStream_t stream) {
+    const ProductInt8Args& p = a.p;
+    const auto kernel = product_int8_kernel<GATED, THIN>;
+    const int pairs = resident_pairs<GATED, THIN>();
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    const int64_t most = static_cast<int64_t>(p.tile_cap) * ceil_div(p.N, kMTile);
+    if (most > INT32_MAX) return cudaErrorInvalidValue;  // units are counted in 32 bits
+    if (encoder() == nullptr) return cudaErrorNotSupported;
+    CUtensorMap wmap, xmap;
+    {
+        const cuuint64_t kb = static_cast<cuuint64_t>(p.K), n = static_cast<cuuint64_t>(p.N);
+        const cuuint64_t dims[3] = {kb, n, static_cast<cuuint64_t>(p.E)}, strides[2] = {kb, kb * n};
+        const cuuint32_t box[3] = {kStageK, 128, 1};
+        if (!encode(&wmap, p.wq, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.x_stride)};
+        const cuuint32_t box[2] = {kStageK, 32};
+        if (!encode(&xmap, p.xq, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    const unsigned grid = 2u * static_cast<unsigned>(most < pairs ? most : pairs);
+    return launch_pdl_cluster(kernel, grid, Cut<THIN>::kThreads, Cut<THIN>::kSmem, 2u, stream, a, wmap, xmap);
 }
 
 }  // namespace
 
-cudaError_t launch_product_int8(const ProductInt8Args& a, cudaStream_t stream) {
-    if (a.tile_cap == 0) return cudaSuccess;
-    const int64_t blocks = static_cast<int64_t>(a.tile_cap) * 4 * ceil_div(a.N, kTile);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(product_int8_kernel, static_cast<unsigned>(blocks), 256u, 0, stream, a);
+cudaError_t launch_product_int8(const ProductInt8Args& p, cudaStream_t stream) {
+    if (p.tile_cap == 0) return cudaSuccess;
+    Args a{p, 0, kWaitCycles, -1, p.err};
+    take_product_wait_test(&a.wait_cycles, &a.quit_warp);
+    bool thin;
+    if (p.plan) {
+        thin = p.tile_cap <= p.E + p.E / 2;  // few experts, if any, have more than one tile
+    } else {
+        const int pairs = resident_pairs<false, false>();
+        if (pairs < 1) return cudaErrorInvalidConfiguration;
+        a.shift = tile_shift(p, pairs);
+        a.p.tile_cap = static_cast<int32_t>(ceil_div(p.rows, kPlanTileRows >> a.shift));
+        thin = a.shift > 0;
+    }
+    return p.gated ? (thin ? launch_pairs<true, true>(a, stream) : launch_pairs<true, false>(a, stream))
+                   : (thin ? launch_pairs<false, true>(a, stream) : launch_pairs<false, false>(a, stream));
 }
 
 }  // namespace moe
