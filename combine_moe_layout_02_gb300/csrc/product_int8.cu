@@ -43,17 +43,18 @@ constexpr uint32_t kScaleBytes = 4 * kPlanTileRows * 4;  // the rows' scales, fo
 constexpr uint32_t kBarBytes = 512;
 constexpr int kAcc1 = 128;  // second place of the sums
 constexpr int kSharedChunks = (256 - kAcc1) / 16;
-constexpr int kMostSlots = 8, kMostStages = 6;
+constexpr int kMostSlots = 8, kMostStages = 9;
 
 // Up to 256 rows to a tile, or (THIN) up to 128: half the rows in shared memory make
 // room for more stages, half the sums in tensor memory for more places of f16 weights.
 template <bool THIN>
 struct Cut {
-    static constexpr int kRows = THIN ? 128 : 256;
-    static constexpr int kStages = THIN ? 6 : 4;
-    static constexpr int kGroups = THIN ? 4 : 2;                     // of four converting warps: two take turns at the halves of K
+    static constexpr int kRows = THIN ? 64 : 256;
+    static constexpr int kStages = THIN ? 9 : 4;
+    static constexpr int kGroups = 4;                     // of four converting warps: two take turns at the halves of K
     static constexpr int kThreads = 256 + 128 * kGroups;
-    static constexpr int kSlots = THIN ? 8 : 4;                      // places of f16 operands, 2 each group's
+    static constexpr int kSlots = THIN ? 8 : 4;                      // places of f16 operands, one or two each group's
+    static constexpr int kPer = kSlots / kGroups;
     static constexpr int kACol = THIN ? 256 : 384;                   // the f16 weights, 32 columns a place
     static constexpr uint32_t kStageBytes = kWBytes + kRows / 64 * kXBox;
     static constexpr uint32_t kHalfBytes = kRows / 2 * 128;          // a CTA's rows of 64 f16
@@ -138,16 +139,12 @@ __device__ __forceinline__ void write_shared(uint32_t addr, uint32_t a, uint32_t
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 64 codes of a swizzled row (its half `half`) to 64 f16, two to a word.
-__device__ __forceinline__ void row_halves(uint32_t row_addr, int row, int half, uint32_t (&h)[32]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint4 v = read_shared(row_addr + (((4 * half + c) ^ (row & 7)) << 4));
-        halves4(v.x, h[8 * c], h[8 * c + 1]);
-        halves4(v.y, h[8 * c + 2], h[8 * c + 3]);
-        halves4(v.z, h[8 * c + 4], h[8 * c + 5]);
-        halves4(v.w, h[8 * c + 6], h[8 * c + 7]);
-    }
+// 16 codes to 16 f16, two to a word.
+__device__ __forceinline__ void halves16(uint4 v, uint32_t* h) {
+    halves4(v.x, h[0], h[1]);
+    halves4(v.y, h[2], h[3]);
+    halves4(v.z, h[4], h[5]);
+    halves4(v.w, h[6], h[7]);
 }
 
 // A lane's 32 words to 32 columns of tensor memory.
@@ -226,7 +223,7 @@ template <bool GATED, bool THIN>
 __global__ void __launch_bounds__(Cut<THIN>::kThreads, 1)
 product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
     constexpr int kStages = Cut<THIN>::kStages, kSlots = Cut<THIN>::kSlots, kACol = Cut<THIN>::kACol, kRows = Cut<THIN>::kRows;
-    constexpr uint32_t kStageBytes = Cut<THIN>::kStageBytes, kHalfBytes = Cut<THIN>::kHalfBytes, kTurns = Cut<THIN>::kGroups / 2;
+    constexpr uint32_t kStageBytes = Cut<THIN>::kStageBytes, kHalfBytes = Cut<THIN>::kHalfBytes, kTurns = Cut<THIN>::kGroups / 2, kPer = Cut<THIN>::kPer;
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs of the pair (their shared windows are alike).
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -303,7 +300,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     mbar_arrive_expect_tx(&bars->full[s], bytes);
                     load_3d(base, &wmap, k * kStageK, m0, t.e, bar);
 #pragma unroll
-                    for (int i = 0; i < kRows / 64; ++i)
+                    for (int i = 0; i < (kRows + 63) / 64; ++i)
                         if (i < boxes) load_2d(base + kWBytes + i * kXBox, &xmap, k * kStageK, x0 + 32 * i, bar);
                 }
                 ++issued;
@@ -346,8 +343,8 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     if (half == 1 && end && short_end) break;
                     uint32_t u = uses[half];
                     if (kTurns > 1 && turn) u = uses[2 * kTurns - 2 + half];
-                    const uint32_t slot = 4 * turn + 2 * half + (u & 1);
-                    if (!wait_here(bars, &bars->ready[slot], u >> 1 & 1, a)) {
+                    const uint32_t slot = (2 * turn + half) * kPer + u % kPer;
+                    if (!wait_here(bars, &bars->ready[slot], u / kPer & 1, a)) {
                         ok = false;
                         break;
                     }
@@ -381,17 +378,19 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
     } else if (warp >= 8) {
         // Four warps a group: of every kTurns stages one, of its K one half.
         const int group = (warp - 8) >> 2, half = group & 1, w = warp & 3;
-        const int row = w * 32 + lane;  // lane of tensor memory, and row of either operand
-        const uint32_t to = tmem + kACol + 64 * group + (static_cast<uint32_t>(w * 32) << 16);
-        const uint32_t mine = smem_addr(halves) + 2 * group * kHalfBytes + row * 128;
-        const uint32_t ready = cluster_map(bars->ready + 2 * group, 0);
+        const int row = w * 32 + lane;           // lane of tensor memory and weight row
+        const int xrow = 8 * w + (lane & 7), xpart = lane >> 3;  // of the rows: which one, and which 16 of 64 codes
+        const uint32_t xfrom = ((4 * half + xpart) ^ (xrow & 7)) << 4, xto = ((2 * xpart) ^ (xrow & 7)) << 4;
+        const uint32_t to = tmem + kACol + 32 * kPer * group + (static_cast<uint32_t>(w * 32) << 16);
+        const uint32_t mine = smem_addr(halves) + kPer * group * kHalfBytes + xrow * 128;
+        const uint32_t ready = cluster_map(bars->ready + kPer * group, 0);
         uint32_t s = 0, phase = 0, uses = 0, turn = 0;
         bool ok = warp != a.quit_warp;
         Units<kRows> list(a, parts, mtiles, first, step);
         while (ok && list.more()) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
-            const bool mine_too = row < static_cast<int>(mma_n(t.n) / 2);
+            const int rows = static_cast<int>(mma_n(t.n) / 2);
             for (int k = 0; k < nstages; ++k) {
                 const uint32_t at = s, parity = phase;
                 if (++s == kStages) {
@@ -409,33 +408,46 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                 }
                 const bool skip = half == 1 && short_end && k == nstages - 1;
                 if (!skip) {
-                    const uint32_t slot = uses & 1;
-                    if (uses >= 2 && !wait_here(bars, &bars->used[2 * group + slot], (uses / 2 - 1) & 1, a)) {
+                    const uint32_t slot = uses % kPer;
+                    if (uses >= kPer && !wait_here(bars, &bars->used[kPer * group + slot], (uses / kPer - 1) & 1, a)) {
                         ok = false;
                         break;
                     }
                     ++uses;
-                    const uint32_t base = smem_addr(smem + at * kStageBytes) + row * 128;
+                    // All codes first: a lane's weight row, and of every 32 rows 16 codes of one (the
+                    // lanes of a warp are 8 rows x 4, so that neither side meets in a bank).
+                    const uint32_t base = smem_addr(smem + at * kStageBytes);
+                    uint4 wv[4], xv[kRows / 64];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) wv[c] = read_shared(base + row * 128 + (((4 * half + c) ^ (row & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < kRows / 64; ++j)
+                        if (32 * j + 8 * w < rows) xv[j] = read_shared(base + kWBytes + (xrow + 32 * j) * 128 + xfrom);
                     uint32_t h[32];
-                    row_halves(base, row, half, h);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) halves16(wv[c], h + 8 * c);
                     tc_fence_after();
                     tmem_store(to + 32 * slot, h);
-                    if (mine_too) {
-                        row_halves(base + kWBytes, row, half, h);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            write_shared(mine + slot * kHalfBytes + ((c ^ (row & 7)) << 4), h[4 * c], h[4 * c + 1],
-                                         h[4 * c + 2], h[4 * c + 3]);
+                    for (int j = 0; j < kRows / 64; ++j) {
+                        if (32 * j + 8 * w >= rows) continue;
+                        uint32_t x[8];
+                        halves16(xv[j], x);
+                        const uint32_t dst = mine + slot * kHalfBytes + j * 32 * 128;
+                        write_shared(dst + xto, x[0], x[1], x[2], x[3]);
+                        write_shared(dst + (xto ^ 16), x[4], x[5], x[6], x[7]);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->empty[at]);
                     // Seen by the tensor cores once the arrival is: every lane's f16 rows and tensor memory.
                     fence_proxy_async_smem();
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(ready + 8 * slot);
+                } else if (lane == 0) {
+                    mbar_arrive(&bars->empty[at]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->empty[at]);
             }
         }
     } else if (warp >= 4) {
