@@ -28,7 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cu", "layout.cu", "notify.cu", "dispatch.cu", "combine.cu", "layout_static.cu", "pad.cu", "expert.cu", "fused.cu", "run.cu", "exchange.cu",
-           "combine_grad.cu", "ffn.cu", "fp4.cu", "product.cu", "gate.cu", "norm.cu", "product_int8.cu"]
+           "combine_grad.cu", "ffn.cu", "fp4.cu", "product.cu", "gate.cu", "norm.cu", "product_int8.cu", "product_int8_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"match_hist": ["-DMOE_LAYOUT_MATCH_HIST"], "profile": ["-DMOE_PROFILE"]}
 

@@ -926,6 +926,7 @@ moe_status moe_expert_product_int8(int32_t E, int32_t N, int32_t K, int32_t gate
     a.xs = reinterpret_cast<const uint8_t*>(xs);
     a.xs_stride = xs_stride;
     a.plan = plan;
+    a.plan_rows = plan ? (static_cast<int64_t>(plan_capacity(E, plan_ints)) - E) * kPlanTileRows : 0;
     a.y = y;
     a.y_stride = y_row_stride;
     a.err = err;

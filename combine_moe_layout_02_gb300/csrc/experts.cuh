@@ -131,11 +131,15 @@ struct ProductInt8Args {
     const uint8_t* xs;
     int64_t xs_stride;
     const int32_t* plan;  // NULL: all rows are the one expert's
+    int64_t plan_rows;    // rows of the routings that the plan is made for, to a multiple of a tile's below
     uint16_t* y;
     int64_t y_stride;
     int32_t* err;
 };
 cudaError_t launch_product_int8(const ProductInt8Args& a, cudaStream_t stream);
+// Dense calls of few rows (product_int8_rows.cu): of 1..kInt8FewRows.
+constexpr int kInt8FewRows = 16;
+cudaError_t launch_product_int8_rows(const ProductInt8Args& a, cudaStream_t stream);
 
 // L2 cache of the current device, in bytes (cached).
 int device_l2_bytes();

@@ -4,6 +4,7 @@
 // and codes 0, so that what is computed from it is NaN.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "experts.cuh"
@@ -53,6 +54,17 @@ __device__ __forceinline__ uint2 int8_codes8(const float (&v)[8], const Int8Scal
         for (int i = 0; i < 4; ++i) w[h] |= (static_cast<uint32_t>(int8_code(v[4 * h + i], s)) & 0xffu) << (8 * i);
     }
     return make_uint2(w[0], w[1]);
+}
+
+// Four codes to four f16: code + 128 is the low byte of the f16 1024 + (code + 128).
+__device__ __forceinline__ void halves4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    const uint32_t b = codes ^ 0x80808080u;
+    const uint32_t u = __byte_perm(b, 0x64646464u, 0x4140), v = __byte_perm(b, 0x64646464u, 0x4342);
+    const uint32_t off = 0x64806480u;  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&off));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 }  // namespace moe

@@ -25,9 +25,8 @@
 // (read first and given back early), and the f16 weights' two places of 32 columns.
 #include <atomic>
 
-#include <cuda_fp16.h>
-
 #include "fp4.cuh"
+#include "int8.cuh"
 #include "tensor.cuh"
 
 namespace moe {
@@ -117,17 +116,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
-}
-
-// Four codes to four f16: code + 128 is the low byte of the f16 1024 + (code + 128).
-__device__ __forceinline__ void halves4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    const uint32_t b = codes ^ 0x80808080u;
-    const uint32_t u = __byte_perm(b, 0x64646464u, 0x4140), v = __byte_perm(b, 0x64646464u, 0x4342);
-    const uint32_t off = 0x64806480u;  // 1152
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&off));
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&off));
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 __device__ __forceinline__ uint4 read_shared(uint32_t addr) {
@@ -641,11 +629,16 @@ cudaError_t launch_pairs(Args a, cudaStream_t stream) {
 
 cudaError_t launch_product_int8(const ProductInt8Args& p, cudaStream_t stream) {
     if (p.tile_cap == 0) return cudaSuccess;
+    // Few rows, dense. Up to 8 cost product_int8_rows.cu one pass over the weights: always (1 to 8 rows, 8192 -> 16384: 28 us
+    // against 33). Up to 16 cost it more than that, which pays where the pairs would be short of units (7168 -> 4096: 13 us
+    // against 27; 8192 -> 16384 has 64 units for the 76 pairs).
+    if (p.plan == nullptr && (p.rows <= 8 || (p.rows <= kInt8FewRows && ceil_div(p.N, kMTile) * 4 <= device_sm_count())))
+        return launch_product_int8_rows(p, stream);
     Args a{p, 0, kWaitCycles, -1, p.err};
     take_product_wait_test(&a.wait_cycles, &a.quit_warp);
     bool thin;
     if (p.plan) {
-        thin = p.tile_cap <= p.E + p.E / 2;  // few experts, if any, have more than one tile
+        thin = p.plan_rows <= 8 * static_cast<int64_t>(p.E);
     } else {
         const int pairs = resident_pairs<false, false>();
         if (pairs < 1) return cudaErrorInvalidConfiguration;
