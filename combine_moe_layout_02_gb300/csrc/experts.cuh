@@ -77,7 +77,7 @@ cudaError_t launch_gate(const GateArgs& a, cudaStream_t stream);
 cudaError_t launch_gate_grad(const GateArgs& a, cudaStream_t stream);
 
 // Root-mean-square norm, int8 rows (norm.cu). Strides are in bytes.
-constexpr int kNormParts = 608;  // most blocks that leave sums in the gradient's scratch
+constexpr int kNormParts = 1216;  // most blocks that leave sums in the gradient's scratch
 struct NormArgs {
     int64_t rows;
     int32_t H;

@@ -34,26 +34,50 @@ __device__ __forceinline__ Int8Scale int8_scale(float most) {
     return s;
 }
 
-// rint(v / scale) with the division's own rounding decided exactly: |v / scale| <=
-// 127.13 (for scales down to the smallest denormal the rounding of most / 127 is
-// within half a unit, and then the quotient is at most 127 * 1.5), v * inv is within 2^-15 of it,
-// so only a product that near to a tie is divided.
-__device__ __forceinline__ int32_t int8_code(float v, const Int8Scale& s) {
-    const float t = v * s.inv;
-    float q = rintf(t);
-    if (!s.fast || fabsf(t - q) >= 0.5f - 0x1p-15f) q = s.inv == 0.f ? 0.f : rintf(__fdiv_rn(v, s.scale));
-    return static_cast<int32_t>(fminf(fmaxf(q, -127.f), 127.f));
+// The low bytes of 8 numbers 1.5 * 2^23 + code.
+__device__ __forceinline__ uint2 int8_bytes8(const float (&m)[8]) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(m[i]);
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+constexpr float kWholeBits = 12582912.f;  // 1.5 * 2^23: added to a number below 2^22, it leaves the whole number in the low bits
+
+// 8 values times inv to the nearest codes (|product| < 127.5).
+__device__ __forceinline__ uint2 int8_near8(const float (&v)[8], float inv) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaf(v[i], inv, kWholeBits);
+    return int8_bytes8(m);
 }
 
-__device__ __forceinline__ uint2 int8_codes8(const float (&v)[8], const Int8Scale& s) {
-    uint32_t w[2];
+// rint(v / scale), divided.
+static __device__ __noinline__ uint2 int8_divided8(float v0, float v1, float v2, float v3, float v4, float v5, float v6, float v7, float scale) {
+    const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[h] |= (static_cast<uint32_t>(int8_code(v[4 * h + i], s)) & 0xffu) << (8 * i);
+    for (int i = 0; i < 8; ++i) {
+        const float q = fminf(fmaxf(rintf(__fdiv_rn(v[i], scale)), -127.f), 127.f);
+        w[i >> 2] |= (static_cast<uint32_t>(static_cast<int32_t>(q)) & 0xffu) << (8 * (i & 3));
     }
     return make_uint2(w[0], w[1]);
+}
+
+// rint(v / scale) of 8 values, the quotient's rounding decided exactly. scale = most / 127
+// rounded, so |v / scale| < 127.13 where scale is a normal number, and v * inv, with inv
+// its rounded reciprocal, is within 2^-15 of it: only where a product is that near to
+// a tie (or inv is not good) are the quotients formed. Codes are 0 under a scale of 0 or NaN.
+__device__ __forceinline__ uint2 int8_codes8(const float (&v)[8], const Int8Scale& s) {
+    float m[8], off = 0.f;  // off: the largest distance of a product from its whole number
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = fmaf(v[i], s.inv, kWholeBits);
+        off = fmaxf(off, fabsf(fmaf(v[i], s.inv, kWholeBits - m[i])));
+    }
+    if (s.inv == 0.f) return make_uint2(0u, 0u);
+    if (s.fast && off < 0.5f - 0x1p-15f) return int8_bytes8(m);
+    return int8_divided8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], s.scale);
 }
 
 // Four codes to four f16: code + 128 is the low byte of the f16 1024 + (code + 128).
