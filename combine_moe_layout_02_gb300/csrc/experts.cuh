@@ -53,7 +53,7 @@ cudaError_t launch_expert_route(const moe_shape& s, const int32_t* topk_idx, int
                                 int32_t* plan, int64_t plan_ints, int32_t* err, void* scratch, cudaStream_t stream);
 
 // The router's gate and its gradient (gate.cu).
-constexpr int kGateParts = 608;  // most blocks that leave sums in the scratch
+constexpr int kGateParts = 1216;  // most blocks that leave sums in the scratch
 struct GateArgs {
     int32_t E, K, bf16, normalize;
     int64_t S;

@@ -11,9 +11,22 @@
 //   dz[e]  = p[e] * (c[e] + sum over k with i_k = e of a_k - T),
 //   T      = sum over e of p[e] c[e] + sum over k of p[i_k] a_k
 //
-// A token is a warp's; its row is in shared memory. Selection compares whole
-// numbers that order like the logits (NaN above all, -0 as 0), so ties are exact.
-// Sums over tokens are binary32 per warp, joined in a fixed order.
+// A token is a warp's, V of its logits a lane's, in registers; the next token's are
+// loaded meanwhile. The logits are read once and the sums of p stay in registers over
+// a warp's tokens. Bound by the selection's instructions (forward) and by memory
+// (backward).
+//
+// Selection: whole numbers in the order of the logits, the low bits replaced by the
+// expert's number counted down: one maximum over the warp then gives the next expert,
+// equal logits by ascending expert. A lane sorts its V once and offers its largest. Where
+// two of the K + 1 largest differ in the replaced bits only (a 16-bit logit has nothing
+// in them), or there is a NaN, the token is selected again with whole numbers of all
+// bits. (A maximum of all bits and then the lowest expert that has it, by two joins and a
+// search of the lane's V for each of the K, took twice as long.) The softmax is shifted by
+// the first of them, which is the largest logit but for those bits.
+//
+// Sums over tokens are binary32 per warp, joined in a fixed order. More than 1024
+// experts: rows in shared memory, selection by search (the _wide kernels).
 #include <cuda_bf16.h>
 
 #include "experts.cuh"
@@ -21,8 +34,11 @@
 namespace moe {
 namespace {
 
-constexpr int kGateWarps = 4;
+constexpr int kWideWarps = 4;
+constexpr int kGateWarps = 8;
+constexpr int kOneBlock = 32;  // tokens that one block takes, sums joined on the spot
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ float logit(const float* z, int e) { return __ldg(z + e); }
 __device__ __forceinline__ float logit(const __nv_bfloat16* z, int e) {
@@ -31,54 +47,524 @@ __device__ __forceinline__ float logit(const __nv_bfloat16* z, int e) {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Whole numbers in the order of the logits; 0 is below all of them.
+// Whole numbers in the order of the logits, -0 as 0, NaN above all; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float z) {
     if (z != z) return 0xffffffffu;
     const uint32_t u = __float_as_uint(z + 0.f);  // -0 becomes 0
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-constexpr uint32_t kNoLogit = 0x007fffffu;  // order_of(-infinity): an expert that may not be chosen
+__device__ __forceinline__ float logit_of(uint32_t order) {
+    return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
+}
+constexpr uint32_t kNoLogit = 0x007fffffu;  // order_of(-infinity): an expert that may not be chosen; numbers are above
+
+// e^x for x <= 0 by the hardware's 2^x (to 2^-22; below 2^-126: 0); x log2 e is rounded once.
+__device__ __forceinline__ float exp_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
+// 1 / x for 1 <= x < 2^126, to 2^-23.
+__device__ __forceinline__ float inverse_of(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
 
-template <typename T>
+// Sums over lanes 0 to 15, in each of them (and over 16 to 31 in those).
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Up to 1024 experts
+
+// 32-bit words of a lane in a warp's shared memory: V logits, V + 1 rows of lists.
+constexpr int lists_of(int V) { return 2 * V + 1; }
+
+// Expert of a lane's i-th logit: VEC neighbours to a load, ascending in i.
+template <int VEC>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+    return (i / VEC) * 32 * VEC + lane * VEC + i % VEC;
+}
+
+// A lane's raw logits of a row: VEC of them to a load of 16 bytes, or one by one.
+template <typename T, int V, int VEC>
+struct RowLoad {
+    static constexpr int kWords = VEC > 1 ? V * static_cast<int>(sizeof(T)) / 4 : V;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const GateArgs& a, int64_t g, int lane) {
+        const uint8_t* row = static_cast<const uint8_t*>(a.logits) + g * a.row_stride;
+        if constexpr (VEC > 1) {
+#pragma unroll
+            for (int n = 0; n < V / VEC; ++n) {
+                const int e = expert_of<VEC>(n * VEC, lane);
+                constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // past the experts: -infinity
+                uint4 v = make_uint4(kNone, kNone, kNone, kNone);
+                if (e < a.E) v = __ldg(reinterpret_cast<const uint4*>(row + e * sizeof(T)));
+                w[4 * n] = v.x;
+                w[4 * n + 1] = v.y;
+                w[4 * n + 2] = v.z;
+                w[4 * n + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = expert_of<1>(i, lane);
+                w[i] = __float_as_uint(e < a.E ? logit(reinterpret_cast<const T*>(row), e) : kNegInf);
+            }
+        }
+    }
+    __device__ __forceinline__ void values(float (&z)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (VEC > 1 && sizeof(T) == 2)
+                z[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+            else
+                z[i] = __uint_as_float(w[i]);
+        }
+    }
+};
+
+// The comparisons of odd-even merge sort (Batcher) for V numbers.
+template <int V>
+struct Network {
+    int n = 0;
+    short a[V * 8] = {}, b[V * 8] = {};
+
+    constexpr Network() {
+        for (int p = 1; p < V; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < V; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < V; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            a[n] = static_cast<short>(i + j);
+                            b[n++] = static_cast<short>(i + j + k);
+                        }
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void sort_descending(uint32_t (&k)[V]) {
+    constexpr Network<V> net;
+#pragma unroll
+    for (int i = 0; i < net.n; ++i) {
+        const uint32_t x = k[net.a[i]], y = k[net.b[i]];
+        k[net.a[i]] = max(x, y);
+        k[net.b[i]] = min(x, y);
+    }
+}
+
+// The K largest of the warp's logits: lane k's expert, or -1 in lanes past the last. *top: the
+// largest, but for the bits that an expert's number takes (0: none that may be chosen).
+// SHORT: the logits are 16-bit numbers. lists [V + 1][32]: the warp's, in shared memory, a
+// lane's column; the last row is 0.
+template <int V, int VEC, bool SHORT>
+__device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, uint32_t* lists, uint32_t* top) {
+    constexpr uint32_t kNumber = 32u * V - 1;  // the bits of an expert's number
+    uint32_t* own = lists + lane;
+    uint32_t head;
+    {
+        uint32_t k[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t u = __float_as_int(z[i] + 0.f);  // -0 becomes 0, any NaN the positive one of all ones
+            k[i] = ((static_cast<uint32_t>(u >> 31) | 0x80000000u) ^ static_cast<uint32_t>(u)) & ~kNumber;
+            k[i] |= kNumber - static_cast<uint32_t>(expert_of<VEC>(i, lane));
+        }
+        sort_descending(k);
+        head = k[0];
+#pragma unroll
+        for (int i = 0; i < V; ++i) own[32 * i] = k[i];
+    }
+    uint32_t mine = 0;
+    const int picks = SHORT ? K : K + 1;  // one more, to see whether it is apart from the last
+    for (int j = 0; j < picks; ++j) {
+        const uint32_t best = __reduce_max_sync(kAll, head);
+        if (lane == j) mine = best;
+        // One lane's: the numbers differ. Lanes that have no more stay at their 0, which is picked when all are there.
+        if (head == best && best != 0u) own += 32;
+        head = *own;
+    }
+    const uint32_t before = __shfl_up_sync(kAll, mine, 1);
+    *top = __shfl_sync(kAll, mine, 0);
+    *top = *top > kNoLogit ? *top & ~kNumber : 0u;
+    int32_t at = mine > kNoLogit && lane < K ? static_cast<int32_t>(kNumber - (mine & kNumber)) : -1;
+    if (SHORT || !__any_sync(kAll, lane >= 1 && mine > kNoLogit && (mine | kNumber) == (before | kNumber))) return at;
+    // All bits: the largest, then the lowest expert that has it.
+    at = -1;
+    uint32_t taken = 0;  // of the lane's V
+    for (int j = 0; j < K; ++j) {
+        uint32_t best = 0;
+        int i0 = 0;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i) {  // of equal ones the lowest
+            const uint32_t o = taken >> i & 1 ? 0u : order_of(z[i]);
+            if (o >= best) {
+                best = o;
+                i0 = i;
+            }
+        }
+        const uint32_t all = __reduce_max_sync(kAll, best);
+        if (all <= kNoLogit) break;
+        const int e = best == all ? expert_of<VEC>(i0, lane) : 1 << 20;
+        const int first = __reduce_min_sync(kAll, e);
+        if (lane == j) at = first;
+        if (e == first) taken |= 1u << i0;
+    }
+    return at;
+}
+
+// A row's largest logit, NaN above all, as order_of() gives it.
+template <int V>
+__device__ __forceinline__ uint32_t row_top(const float (&z)[V]) {
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(z[i]));
+    return __reduce_max_sync(kAll, order_of(m));
+}
+
+// The blocks' (parts') sums to counts, mean probabilities and the loss: expert e of this
+// CTA's share from `first` on; the shares' part of the loss is returned to thread 0. 32
+// experts at a time, a lane each, the warps' parts joined in ascending order.
+__device__ __forceinline__ float join_parts(const GateArgs& a, int parts, int first, int end, int32_t* n_out) {
+    __shared__ float sums[32][33];
+    __shared__ int32_t counts[32][33];
+    __shared__ int32_t routed[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    int32_t n = 0;
+    for (int b = threadIdx.x; b < parts; b += blockDim.x) n += a.part_count[static_cast<size_t>(b) * (a.E + 1) + a.E];
+    n = __reduce_add_sync(kAll, n);
+    if (lane == 0) routed[warp] = n;
+    __syncthreads();
+    n = __reduce_add_sync(kAll, lane < warps ? routed[lane] : 0);
+    *n_out = n;
+    const float inv = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+    float loss = 0.f;
+    for (int e0 = first; e0 < end; e0 += 32) {
+        const int e = e0 + lane;
+        float s = 0.f;
+        int32_t c = 0;
+        if (e < end)
+            for (int b = warp; b < parts; b += warps) {
+                s += a.part_prob[static_cast<size_t>(b) * a.E + e];
+                c += a.part_count[static_cast<size_t>(b) * (a.E + 1) + e];
+            }
+        sums[warp][lane] = s;
+        counts[warp][lane] = c;
+        __syncthreads();
+        if (warp == 0 && e < end) {
+            s = 0.f;
+            c = 0;
+            for (int w = 0; w < warps; ++w) {
+                s += sums[w][lane];
+                c += counts[w][lane];
+            }
+            s *= inv;
+            a.expert_count[e] = c;
+            if (a.expert_prob) a.expert_prob[e] = s;
+            loss += static_cast<float>(c) * s;
+        }
+        __syncthreads();
+    }
+    return warp == 0 ? warp_sum(loss) : 0.f;
+}
+
+__device__ __forceinline__ float loss_of(const GateArgs& a, float sum, int32_t n) {
+    return n > 0 ? a.balance * static_cast<float>(a.E) * (sum / (static_cast<float>(n) * a.K)) : 0.f;
+}
+
+template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a) {
     pdl_wait_then_release();
-    extern __shared__ float smem[];
+    // Of each warp: a token's logits (in the end the sums of p), and its lists; then [E + 1] counts.
+    extern __shared__ __align__(16) float smem[];
+    constexpr int kMine = 32 * lists_of(V);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* z = smem + static_cast<size_t>(warp) * 2 * a.E;  // the token's logits; the ones chosen are taken out
-    float* sums = z + a.E;                                  // the warp's sums of p
-    int32_t* count = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(kGateWarps) * 2 * a.E);  // [E + 1]
-    for (int e = lane; e < a.E; e += 32) sums[e] = 0.f;
+    int32_t* count = reinterpret_cast<int32_t*>(smem + kGateWarps * kMine);
+    float* logits = smem + warp * kMine;
+    uint32_t* lists = reinterpret_cast<uint32_t*>(logits + 32 * V);
+    lists[32 * V + lane] = 0u;
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp; g < a.S;
-         g += static_cast<int64_t>(gridDim.x) * kGateWarps) {
-        const T* row = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
-        uint32_t most = 0;
-        for (int e = lane; e < a.E; e += 32) {
-            z[e] = logit(row, e);
-            most = max(most, order_of(z[e]));
+    float acc[V] = {};
+    int32_t routed_tokens = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGateWarps;
+    int64_t g = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+    RowLoad<T, V, VEC> row;
+    uint8_t masked = 0;
+    const auto fetch = [&](int64_t t) {
+        if (t >= a.S) return;
+        row.load(a, t, lane);
+        masked = a.mask != nullptr && __ldg(a.mask + t) == 0;
+    };
+    fetch(g);
+    for (; g < a.S; g += step) {
+        float z[V];
+        row.values(z);
+        const bool out = masked != 0;
+        fetch(g + step);
+        if constexpr (VEC > 1) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(logits + expert_of<VEC>(i, lane)) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) logits[expert_of<1>(i, lane)] = z[i];
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        const bool routed = most > kNoLogit && (a.mask == nullptr || __ldg(a.mask + g) != 0);
-        if (!routed) {
+        __syncwarp();
+        uint32_t most = 0;
+        const int32_t at = out ? -1 : select<V, VEC, sizeof(T) == 2>(z, a.K, lane, lists, &most);
+        const float chosen = at >= 0 ? logits[at] : kNegInf;
+        __syncwarp();  // the lists and the logits have been read
+        if (most == 0) {
             if (lane < a.K) {
                 a.topk_idx[g * a.K + lane] = -1;
                 a.topk_weights[g * a.K + lane] = 0.f;
             }
             continue;
         }
-        const uint32_t u = most & 0x80000000u ? most ^ 0x80000000u : ~most;
-        const float top = __uint_as_float(u);  // NaN where most stands for one
+        const float top = logit_of(most);  // NaN or infinity where it is one
         float sum = 0.f;
-        for (int e = lane; e < a.E; e += 32) sum += __expf(z[e] - top);
-        const float inv = __frcp_rn(warp_sum(sum));
-        for (int e = lane; e < a.E; e += 32) sums[e] += __expf(z[e] - top) * inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = exp_of(z[i] - top);
+            sum += z[i];
+        }
+        const float p = at >= 0 ? exp_of(chosen - top) : 0.f;
+        const float inv = inverse_of(warp_sum(sum));
+        const float share = a.normalize ? __fdividef(a.scale, half_sum(p)) : a.scale * inv;  // of lanes below 16
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
+        if (lane < a.K) {
+            a.topk_idx[g * a.K + lane] = at;
+            // a NaN or an infinity in the row: all its weights, of slots that found an expert, are NaN
+            a.topk_weights[g * a.K + lane] = at < 0 ? 0.f : p * share + 0.f * inv;
+            if (at >= 0) atomicAdd(&count[at], 1);
+        }
+        ++routed_tokens;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i) logits[expert_of<VEC>(i, lane)] = acc[i];
+    if (lane == 0) atomicAdd(&count[a.E], routed_tokens);
+    __syncthreads();
+    float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
+    int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGateWarps; ++w) s += smem[w * kMine + e];
+        part[e] = s;
+        part_count[e] = count[e];
+    }
+    if (threadIdx.x == 0) part_count[a.E] = count[a.E];
+    if (gridDim.x > 1) return;
+    __syncthreads();  // the block's own words in global memory
+    int32_t n;
+    const float loss = join_parts(a, 1, 0, a.E, &n);
+    if (threadIdx.x == 0) {
+        a.expert_count[a.E] = n;
+        if (a.loss) *a.loss = loss_of(a, loss, n);
+    }
+}
+
+// One cluster: each CTA joins a share of the experts, the first one adds the shares' losses up.
+constexpr int kJoinCtas = 8;
+__global__ void __launch_bounds__(1024) gate_join_kernel(const GateArgs a, int parts) {
+    pdl_wait_then_release();
+    __shared__ float share;
+    const int per = static_cast<int>(round_up(ceil_div(a.E, kJoinCtas), 32)), first = min(a.E, static_cast<int>(blockIdx.x) * per);
+    int32_t n;
+    const float loss = join_parts(a, parts, first, min(a.E, first + per), &n);
+    if (threadIdx.x == 0) share = loss;
+    cluster_sync_all();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        float s = 0.f;
+        for (uint32_t r = 0; r < kJoinCtas; ++r) s += __int_as_float(ld_cluster_s32(cluster_map(&share, r)));
+        a.expert_count[a.E] = n;
+        if (a.loss) *a.loss = loss_of(a, s, n);
+    }
+    cluster_sync_all();
+}
+
+// The slots' part of the gradient, in lanes below K (K <= 16): expert (or -1), p, and a_k summed
+// over slots of the same expert in ascending order (in all of them); in all lanes t, the sum
+// over k of p[i_k] a_k: scale / D times sum_k dw_k p_k - sum_j dw_j p_j = 0 of normalized
+// weights, scale sum_k dw_k p_k of others. `e`: the slots' exponentials, 0 where there is none;
+// whose [E]: the warp's, in shared memory.
+struct Slots {
+    int32_t i;
+    float p, a, t;
+};
+static_assert(MOE_MAX_TOPK <= 16, "slots in half a warp");
+__device__ __forceinline__ Slots slots_of(const GateArgs& a, int lane, int32_t i, float dw, float e, float inv, volatile uint8_t* whose) {
+    Slots s{i, e * inv, 0.f, 0.f};
+    if (a.dweights == nullptr) return s;
+    const float back = half_sum(dw * e);
+    float own = a.scale * dw;
+    if (a.normalize) {
+        const float d = half_sum(e);
+        own = d > 0.f || d != d ? a.scale * (dw - back / d) / (d * inv) : 0.f;  // (0: no slot, or none that counts)
+    } else {
+        s.t = __shfl_sync(kAll, a.scale * back * inv, 0);
+    }
+    s.a = own;
+    // Two slots of one expert read back one's lane.
+    if (i >= 0) whose[i] = static_cast<uint8_t>(lane);
+    __syncwarp();
+    if (__any_sync(kAll, i >= 0 && whose[i] != lane)) {
+        s.a = 0.f;
+        for (int k = 0; k < a.K; ++k) {
+            const float o = __shfl_sync(kAll, own, k);
+            if (__shfl_sync(kAll, i, k) == i) s.a += o;
+        }
+    }
+    __syncwarp();
+    return s;
+}
+
+// dl * balance * E / (K n) / n.
+__device__ __forceinline__ float loss_unit(const GateArgs& a) {
+    const int32_t n = __ldg(a.expert_count + a.E);
+    if (a.dloss == nullptr || n <= 0) return 0.f;
+    return __ldg(a.dloss) * a.balance * a.E / (static_cast<float>(n) * static_cast<float>(n) * a.K);
+}
+
+template <typename T, int V, int VEC>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateArgs a) {
+    pdl_wait_then_release();
+    __shared__ float table[32 * V];  // c of each expert
+    __shared__ uint8_t whose[kGateWarps][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float unit = loss_unit(a);
+    for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
+        table[e] = e < a.E ? unit * static_cast<float>(__ldg(a.expert_count + e)) : 0.f;
+    __syncthreads();
+    float c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = table[expert_of<VEC>(i, lane)];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGateWarps;
+    int64_t g = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+    RowLoad<T, V, VEC> row;
+    uint8_t masked = 0;
+    float chosen = 0.f, dw = 0.f;
+    const auto ids = [&](int64_t t) {
+        const int32_t i = t < a.S && lane < a.K ? __ldg(a.topk_idx + t * a.K + lane) : -1;
+        return i < a.E ? i : -1;
+    };
+    // A token's logits, and its slots' by their ids, are loaded a token ahead, the ids two.
+    const auto fetch = [&](int64_t t, int32_t i) {
+        if (t >= a.S) return;
+        row.load(a, t, lane);
+        masked = a.mask != nullptr && __ldg(a.mask + t) == 0;
+        chosen = i >= 0 ? logit(reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + t * a.row_stride), i) : 0.f;
+        dw = i >= 0 && a.dweights ? __ldg(a.dweights + t * a.K + lane) : 0.f;
+    };
+    int32_t idx = ids(g), idx_next = ids(g + step);
+    fetch(g, idx);
+    for (; g < a.S; g += step) {
+        float z[V];
+        row.values(z);
+        const bool out = masked != 0;
+        const int32_t i_now = idx;
+        const float dw_now = dw, chosen_now = chosen;
+        idx = idx_next;
+        idx_next = ids(g + 2 * step);
+        fetch(g + step, idx);
+        T* to = reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride);
+        const uint32_t most = row_top(z);
+        const bool routed = !out && most > kNoLogit;
+        float t = 0.f, inv = 0.f;
+        Slots s{-1, 0.f, 0.f, 0.f};
+        if (routed) {
+            const float top = logit_of(most);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                z[i] = exp_of(z[i] - top);
+                sum += z[i];
+                t = fmaf(z[i], c[i], t);
+            }
+            inv = inverse_of(warp_sum(sum));
+            t = warp_sum(t) * inv;
+            s = slots_of(a, lane, i_now, dw_now, i_now >= 0 ? exp_of(chosen_now - top) : 0.f, inv, whose[warp]);
+            t += s.t;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = routed ? z[i] * inv * (c[i] - t) : 0.f;
+        if constexpr (VEC > 1) {
+#pragma unroll
+            for (int n = 0; n < V / VEC; ++n) {
+                const int e = expert_of<VEC>(n * VEC, lane);
+                if (e >= a.E) continue;
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 2) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(z[n * VEC + 2 * j], z[n * VEC + 2 * j + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+                    } else {
+                        w[j] = __float_as_uint(z[n * VEC + j]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (expert_of<1>(i, lane) < a.E) put(to + expert_of<1>(i, lane), z[i]);
+        }
+        __syncwarp();  // the chosen experts' over what was stored for them
+        if (s.i >= 0) put(to + s.i, s.p * (table[s.i] + s.a - t));
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// More than 1024 experts
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWideWarps) gate_wide_kernel(const GateArgs a) {
+    pdl_wait_then_release();
+    extern __shared__ float smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* z = smem + static_cast<size_t>(warp) * 2 * a.E;  // the token's logits; the ones chosen are taken out
+    float* sums = z + a.E;                                  // the warp's sums of p
+    int32_t* count = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(kWideWarps) * 2 * a.E);  // [E + 1]
+    for (int e = lane; e < a.E; e += 32) sums[e] = 0.f;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) count[e] = 0;
+    __syncthreads();
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kWideWarps + warp; g < a.S;
+         g += static_cast<int64_t>(gridDim.x) * kWideWarps) {
+        const T* row = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
+        uint32_t most = 0;
+        for (int e = lane; e < a.E; e += 32) {
+            z[e] = logit(row, e);
+            most = max(most, order_of(z[e]));
+        }
+        most = __reduce_max_sync(kAll, most);
+        if (most <= kNoLogit || (a.mask != nullptr && __ldg(a.mask + g) == 0)) {
+            if (lane < a.K) {
+                a.topk_idx[g * a.K + lane] = -1;
+                a.topk_weights[g * a.K + lane] = 0.f;
+            }
+            continue;
+        }
+        const float top = logit_of(most);  // NaN where most stands for one
+        float sum = 0.f;
+        for (int e = lane; e < a.E; e += 32) sum += exp_of(z[e] - top);
+        const float inv = inverse_of(warp_sum(sum));
+        for (int e = lane; e < a.E; e += 32) sums[e] += exp_of(z[e] - top) * inv;
         int32_t mine = -1;
         float p = 0.f;
         for (int k = 0; k < a.K; ++k) {
@@ -91,12 +577,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
                     at = e;
                 }
             }
-            const uint32_t all = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t all = __reduce_max_sync(kAll, best);
             if (all <= kNoLogit) break;
-            at = __reduce_min_sync(0xffffffffu, best == all ? at : a.E);
+            at = __reduce_min_sync(kAll, best == all ? at : a.E);
             if (lane == k) {
                 mine = at;
-                p = __expf(z[at] - top) * inv;
+                p = exp_of(z[at] - top) * inv;
             }
             __syncwarp();
             if (lane == 0) {
@@ -118,127 +604,137 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float s = 0.f;
-        for (int w = 0; w < kGateWarps; ++w) s += smem[(static_cast<size_t>(w) * 2 + 1) * a.E + e];
+        for (int w = 0; w < kWideWarps; ++w) s += smem[(static_cast<size_t>(w) * 2 + 1) * a.E + e];
         part[e] = s;
     }
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) part_count[e] = count[e];
 }
 
-// The blocks' sums to counts, mean probabilities and the loss.
-__global__ void __launch_bounds__(1024) gate_join_kernel(const GateArgs a, int parts) {
-    pdl_wait_then_release();
-    __shared__ float partial[32];
-    int32_t n = 0;
-    for (int b = 0; b < parts; ++b) n += a.part_count[static_cast<size_t>(b) * (a.E + 1) + a.E];
-    const float inv = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
-    float loss = 0.f;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        int32_t c = 0;
-        float s = 0.f;
-        for (int b = 0; b < parts; ++b) {
-            c += a.part_count[static_cast<size_t>(b) * (a.E + 1) + e];
-            s += a.part_prob[static_cast<size_t>(b) * a.E + e];
-        }
-        s *= inv;
-        a.expert_count[e] = c;
-        if (a.expert_prob) a.expert_prob[e] = s;
-        loss += static_cast<float>(c) * s;
-    }
-    if (threadIdx.x == 0) a.expert_count[a.E] = n;
-    loss = warp_sum(loss);
-    if ((threadIdx.x & 31) == 0) partial[threadIdx.x >> 5] = loss;
-    __syncthreads();
-    if (threadIdx.x == 0 && a.loss) {
-        float s = 0.f;
-        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += partial[w];
-        *a.loss = n > 0 ? a.balance * static_cast<float>(a.E) * (s / (static_cast<float>(n) * a.K)) : 0.f;
-    }
-}
-
 template <typename T>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateArgs a) {
+__global__ void __launch_bounds__(32 * kWideWarps) gate_wide_grad_kernel(const GateArgs a) {
     pdl_wait_then_release();
     extern __shared__ float smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* c = smem;                                                // [E]
-    float* add = smem + a.E + static_cast<size_t>(warp) * a.E;      // [E]: sum over k with i_k = e of a_k
-    const int32_t n = __ldg(a.expert_count + a.E);
-    const float unit = a.dloss && n > 0
-                           ? __ldg(a.dloss) * a.balance * a.E / (static_cast<float>(n) * static_cast<float>(n) * a.K) : 0.f;
+    float* c = smem;                                            // [E]
+    float* add = smem + a.E + static_cast<size_t>(warp) * a.E;  // [E]: sum over k with i_k = e of a_k
+    uint8_t* whose = reinterpret_cast<uint8_t*>(smem + static_cast<size_t>(kWideWarps + 1) * a.E) + warp * a.E;
+    const float unit = loss_unit(a);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) c[e] = unit * static_cast<float>(__ldg(a.expert_count + e));
     for (int e = lane; e < a.E; e += 32) add[e] = 0.f;
     __syncthreads();
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp; g < a.S;
-         g += static_cast<int64_t>(gridDim.x) * kGateWarps) {
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kWideWarps + warp; g < a.S;
+         g += static_cast<int64_t>(gridDim.x) * kWideWarps) {
         const T* row = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
         T* out = reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride);
         uint32_t most = 0;
         for (int e = lane; e < a.E; e += 32) most = max(most, order_of(logit(row, e)));
-        most = __reduce_max_sync(0xffffffffu, most);
+        most = __reduce_max_sync(kAll, most);
         if (most <= kNoLogit || (a.mask != nullptr && __ldg(a.mask + g) == 0)) {
             for (int e = lane; e < a.E; e += 32) put(out + e, 0.f);
             continue;
         }
-        const float top = __uint_as_float(most & 0x80000000u ? most ^ 0x80000000u : ~most);
+        const float top = logit_of(most);
         float sum = 0.f, t = 0.f;
         for (int e = lane; e < a.E; e += 32) {
-            const float v = __expf(logit(row, e) - top);
+            const float v = exp_of(logit(row, e) - top);
             sum += v;
             t += v * c[e];
         }
-        const float inv = __frcp_rn(warp_sum(sum));
+        const float inv = inverse_of(warp_sum(sum));
         t = warp_sum(t) * inv;
         int32_t i = -1;
-        float p = 0.f, dw = 0.f;
+        float dw = 0.f;
         if (lane < a.K) {
             i = __ldg(a.topk_idx + g * a.K + lane);
             if (i >= a.E) i = -1;
-            if (i >= 0 && a.dweights) {
-                dw = __ldg(a.dweights + g * a.K + lane);
-                p = __expf(logit(row, i) - top) * inv;
-            }
+            if (i >= 0 && a.dweights) dw = __ldg(a.dweights + g * a.K + lane);
         }
-        float d = 1.f, back = dw;
-        if (a.normalize && a.dweights) {
-            d = warp_sum(p);
-            back = dw - warp_sum(dw * p) / d;
-        }
-        const float ak = i >= 0 && a.dweights ? a.scale * back / d : 0.f;
-        t += warp_sum(p * ak);
-        if (i >= 0) atomicAdd(&add[i], ak);
+        const Slots s = slots_of(a, lane, i, dw, i >= 0 ? exp_of(logit(row, i) - top) : 0.f, inv, whose);
+        t += s.t;
+        if (s.i >= 0) add[s.i] = s.a;  // slots of the same expert have the same sum
         __syncwarp();
-        for (int e = lane; e < a.E; e += 32) put(out + e, __expf(logit(row, e) - top) * inv * (c[e] + add[e] - t));
+        for (int e = lane; e < a.E; e += 32) put(out + e, exp_of(logit(row, e) - top) * inv * (c[e] + add[e] - t));
         __syncwarp();
-        if (i >= 0) add[i] = 0.f;
+        if (s.i >= 0) add[s.i] = 0.f;
         __syncwarp();
     }
 }
 
-int gate_blocks(int64_t S) {
-    const int64_t n = ceil_div(S, kGateWarps);
-    return static_cast<int>(n < 1 ? 1 : n > kGateParts ? kGateParts : n);
+// ---------------------------------------------------------------------------
+
+using Kernel = void (*)(const GateArgs);
+
+// Loads of 16 bytes where rows are made of them.
+bool by_16(const GateArgs& a, int64_t stride) {
+    const int64_t elt = a.bf16 ? 2 : 4;
+    return a.E * elt % 16 == 0 && stride % 16 == 0;
+}
+
+template <bool GRAD, typename T, int V, int VEC>
+Kernel kernel_at() {
+    if constexpr (GRAD)
+        return gate_grad_kernel<T, V, VEC>;
+    else
+        return gate_kernel<T, V, VEC>;
+}
+int logits_of_a_lane(int E) { return E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+
+// by: rows are loaded 16 bytes at a time.
+template <bool GRAD, typename T>
+Kernel kernel_for(int E, bool by) {
+    constexpr int kVec = 16 / sizeof(T), kVec4 = kVec <= 4 ? kVec : 1;
+    switch (logits_of_a_lane(E)) {
+        case 2: return kernel_at<GRAD, T, 2, 1>();
+        case 4: return by ? kernel_at<GRAD, T, 4, kVec4>() : kernel_at<GRAD, T, 4, 1>();
+        case 8: return by ? kernel_at<GRAD, T, 8, kVec>() : kernel_at<GRAD, T, 8, 1>();
+        case 16: return by ? kernel_at<GRAD, T, 16, kVec>() : kernel_at<GRAD, T, 16, 1>();
+        default: return by ? kernel_at<GRAD, T, 32, kVec>() : kernel_at<GRAD, T, 32, 1>();
+    }
+}
+
+constexpr int kMostInRegisters = 1024;
+
+// Blocks of `warps` tokens at a time: what is resident, or needed, at most kGateParts.
+cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int64_t S, unsigned* blocks) {
+    int per_sm = 0;
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, 32 * warps, &per_sm);
+    int64_t n = static_cast<int64_t>(device_sm_count()) * (per_sm > 0 ? per_sm : 1);
+    if (n > kGateParts) n = kGateParts;
+    const int64_t need = ceil_div(S, warps);
+    *blocks = static_cast<unsigned>(need < 1 ? 1 : need < n ? need : n);
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_gate(const GateArgs& a, cudaStream_t stream) {
-    const size_t smem = (static_cast<size_t>(kGateWarps) * 2 * a.E + a.E + 1) * 4;
-    const int blocks = gate_blocks(a.S);
-    auto kernel = a.bf16 ? gate_kernel<__nv_bfloat16> : gate_kernel<float>;
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, 32 * kGateWarps, nullptr);
+    const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride);
+    const int warps = wide ? kWideWarps : kGateWarps;
+    const int entries = wide ? 2 * a.E : 32 * lists_of(logits_of_a_lane(a.E));
+    const size_t smem = (static_cast<size_t>(warps) * entries + a.E + 1) * 4;
+    const Kernel kernel = wide ? (a.bf16 ? gate_wide_kernel<__nv_bfloat16> : gate_wide_kernel<float>)
+                               : (a.bf16 ? kernel_for<false, __nv_bfloat16>(a.E, by) : kernel_for<false, float>(a.E, by));
+    unsigned blocks = 0;
+    cudaError_t e = blocks_for(kernel, smem, warps, a.S, &blocks);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, static_cast<unsigned>(blocks), 32 * kGateWarps, smem, stream, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(gate_join_kernel, 1u, 1024u, 0, stream, a, blocks);
+    const bool one = !wide && a.S <= kOneBlock;
+    if (one) blocks = 1;
+    e = launch_pdl(kernel, blocks, 32u * warps, smem, stream, a);
+    if (e != cudaSuccess || one || (!wide && blocks == 1)) return e;
+    return launch_pdl_cluster(gate_join_kernel, kJoinCtas, 1024u, 0, kJoinCtas, stream, a, static_cast<int>(blocks));
 }
 
 cudaError_t launch_gate_grad(const GateArgs& a, cudaStream_t stream) {
     if (a.S == 0) return cudaSuccess;
-    const size_t smem = static_cast<size_t>(kGateWarps + 1) * a.E * 4;
-    auto kernel = a.bf16 ? gate_grad_kernel<__nv_bfloat16> : gate_grad_kernel<float>;
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, 32 * kGateWarps, nullptr);
+    const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride) && by_16(a, a.dlogits_stride);
+    const int warps = wide ? kWideWarps : kGateWarps;
+    const size_t smem = wide ? static_cast<size_t>(warps + 1) * a.E * 4 + static_cast<size_t>(warps) * a.E : 0;
+    const Kernel kernel = wide ? (a.bf16 ? gate_wide_grad_kernel<__nv_bfloat16> : gate_wide_grad_kernel<float>)
+                               : (a.bf16 ? kernel_for<true, __nv_bfloat16>(a.E, by) : kernel_for<true, float>(a.E, by));
+    unsigned blocks = 0;
+    const cudaError_t e = blocks_for(kernel, smem, warps, a.S, &blocks);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, static_cast<unsigned>(gate_blocks(a.S)), 32 * kGateWarps, smem, stream, a);
+    return launch_pdl(kernel, blocks, 32u * warps, smem, stream, a);
 }
 
 }  // namespace moe
