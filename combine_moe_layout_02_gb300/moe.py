@@ -447,50 +447,83 @@ def moe_expert_ffn_fp4(shape, inner, x, topk_idx, topk_weights, w1q, w1sf, w2q, 
     _check(st, "moe_expert_ffn_fp4")
 
 
-def _cuda_tensor(t, dtypes, name):
-    """t's address; t is of one of the types and on the current device, where the call's stream is."""
-    import torch
+class _Types:
+    """torch's types that the calls compare with, and the current device's number (torch is imported with the first)."""
 
-    if t.dtype not in dtypes:
-        raise ValueError("expected %s in %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    def __init__(self):
+        import torch
+
+        self.bf16, self.f32, self.i8, self.u8, self.flag = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.bool
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+_types = None
+
+
+def _t():
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
+
+
+def _placed(t, name):
+    """t's address; t is on the current device, where the call's stream is."""
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    if t.get_device() != _t().device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, _t().device()))
     return t.data_ptr()
 
 
-def _flat(t, n, dtypes, name):
+def _typed(t, dtype, name):
+    if t.dtype is not dtype:
+        raise ValueError("expected %s in %s, got %s" % (name, dtype, t.dtype))
+
+
+def _flat(t, n, dtype, name):
     """Address of a contiguous tensor of n elements (None -> NULL)."""
     if t is None:
         return None
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("expected %s contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
-    return _cuda_tensor(t, dtypes, name)
+    if t.dtype is not dtype:
+        _typed(t, dtype, name)
+    return _placed(t, name)
 
 
-def _rows_of(t, rows, width, dtypes, name):
-    """(address, bytes from row to row) of a tensor [rows, width] whose rows may be apart (None -> NULL)."""
+def _rows_of(t, rows, width, dtype, size, name):
+    """(address, bytes from row to row) of a tensor [rows, width] of `size` bytes an element whose rows may be apart
+    (None -> NULL)."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != (rows, width) or (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < width):
-        raise ValueError("expected %s of shape %s with unit column stride, got %s with strides %s" % (
-            name, (rows, width), tuple(t.shape), t.stride()))
-    size = t.element_size()
-    # one row's stride says nothing
-    return _cuda_tensor(t, dtypes, name), size * (t.stride(0) if rows > 1 else -(-width * size // 16) * 16 // size)
+    if t.dtype is not dtype:
+        _typed(t, dtype, name)
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != width:
+        raise ValueError("expected %s of shape %s, got %s" % (name, (rows, width), tuple(t.shape)))
+    if rows <= 1:  # one row's stride says nothing
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError("expected %s with unit column stride, got strides %s" % (name, t.stride()))
+        return _placed(t, name), (width * size + 15) // 16 * 16
+    if t.is_contiguous():
+        return _placed(t, name), width * size
+    if (width > 1 and t.stride(1) != 1) or t.stride(0) < width:
+        raise ValueError("expected %s with unit column stride and rows that do not overlap, got strides %s" % (name, t.stride()))
+    return _placed(t, name), t.stride(0) * size
 
 
-_DTYPES = {}
-
-
-def _dtypes(*names):
-    got = _DTYPES.get(names)
-    if got is None:
-        import torch
-
-        got = _DTYPES[names] = tuple(getattr(torch, n) for n in names)
-    return got
+def _scales_of(t, rows, name):
+    """(address, bytes from one to the next) of rows float32 scales (None -> NULL)."""
+    if t is None:
+        return None, 0
+    _typed(t, _t().f32, name)
+    if t.dim() < 1 or t.size(0) != rows or t.numel() != rows:
+        raise ValueError("expected %s of %d scales, got %s" % (name, rows, tuple(t.shape)))
+    if rows <= 1:
+        return _placed(t, name), 4
+    if t.stride(0) < 1:
+        raise ValueError("expected %s with a place of its own for every row" % name)
+    return _placed(t, name), 4 * t.stride(0)
 
 
 class Gate:
@@ -515,42 +548,45 @@ class Gate:
         self.expert_prob = torch.empty((E,), dtype=torch.float32, device=device)
         self.loss = torch.empty((1,), dtype=torch.float32, device=device)
         self.scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        self._shape, self._nbytes = ctypes.byref(shape), nbytes
 
     def _logits(self, t, name):
-        ptr, stride = _rows_of(t, self.shape.S, self.shape.E, _dtypes("float32", "bfloat16"), name)
-        return int(t.element_size() == 2), ptr, stride
+        half = t.dtype is _t().bf16
+        if not half and t.dtype is not _t().f32:
+            raise ValueError("expected %s in torch.float32 or torch.bfloat16, got %s" % (name, t.dtype))
+        return (int(half), *_rows_of(t, self.shape.S, self.shape.E, t.dtype, 2 if half else 4, name))
 
     def _mask(self, mask):
-        return _flat(mask, self.shape.S, _dtypes("uint8", "bool"), "mask")
+        return None if mask is None else _flat(mask, self.shape.S, _t().flag if mask.dtype is _t().flag else _t().u8, "mask")
 
     def forward(self, logits, mask=None, stream=None):
         """Routes logits [S,E] (float32 or bfloat16, rows may be apart); mask [S] uint8 or bool: 0 for tokens left out."""
-        kind, ptr, stride = self._logits(logits, "logits")
-        st = lib().moe_gate(ctypes.byref(self.shape), kind, ptr, stride, self._mask(mask), self.normalize, self.scale,
+        st = lib().moe_gate(self._shape, *self._logits(logits, "logits"), self._mask(mask), self.normalize, self.scale,
                             self.balance, self.topk_idx.data_ptr(), self.topk_weights.data_ptr(),
                             self.expert_count.data_ptr(), self.expert_prob.data_ptr(), self.loss.data_ptr(),
-                            self.scratch.data_ptr(), self.scratch.numel(), _stream(stream))
-        _check(st, "moe_gate")
+                            self.scratch.data_ptr(), self._nbytes, _stream(stream))
+        if st:
+            raise MoeError(st, "moe_gate")
         return self.topk_idx, self.topk_weights
 
     def backward(self, logits, dweights=None, dloss=None, mask=None, dlogits=None, stream=None):
         """The logits' gradient from those of topk_weights [S,K] and of the loss [1] (float32; None: 0). logits and mask
         as in the forward call; dlogits: rows for the result, of logits' type (made where it is None)."""
-        import torch
-
-        s = self.shape
-        kind, ptr, stride = self._logits(logits, "logits")
+        s, f32 = self.shape, _t().f32
+        args = self._logits(logits, "logits")
         if dlogits is None:
+            import torch
+
             with _made_on(stream, logits.device):
                 dlogits = torch.empty((s.S, s.E), dtype=logits.dtype, device=logits.device)
-        elif dlogits.dtype != logits.dtype:
+        elif dlogits.dtype is not logits.dtype:
             raise ValueError("expected dlogits in %s, got %s" % (logits.dtype, dlogits.dtype))
-        _, out, out_stride = self._logits(dlogits, "dlogits")
-        st = lib().moe_gate_grad(ctypes.byref(s), kind, ptr, stride, self._mask(mask), self.normalize, self.scale,
-                                 self.balance, self.topk_idx.data_ptr(), self.expert_count.data_ptr(),
-                                 _flat(dweights, s.S * s.K, _dtypes("float32"), "dweights"),
-                                 _flat(dloss, 1, _dtypes("float32"), "dloss"), out, out_stride, _stream(stream))
-        _check(st, "moe_gate_grad")
+        st = lib().moe_gate_grad(self._shape, *args, self._mask(mask), self.normalize, self.scale, self.balance,
+                                 self.topk_idx.data_ptr(), self.expert_count.data_ptr(),
+                                 _flat(dweights, s.S * s.K, f32, "dweights"), _flat(dloss, 1, f32, "dloss"),
+                                 *self._logits(dlogits, "dlogits")[1:], _stream(stream))
+        if st:
+            raise MoeError(st, "moe_gate_grad")
         return dlogits
 
 
@@ -558,27 +594,13 @@ def moe_rms_norm(x, weight, eps, y=None, residual=None, sum_out=None, q=None, q_
     """Root-mean-square norm of x + residual [rows, H] in bf16 (include/moe.h): y and sum_out bf16 rows, q int8 rows with
     q_scale float32 [rows] (or [rows, 1], a column of any row-strided tensor). Rows may be apart."""
     rows, H = x.shape
-    bf16 = _dtypes("bfloat16")
-    args = []
-    for t, name in ((x, "x"), (residual, "residual")):
-        args += _rows_of(t, rows, H, bf16, name)
-    args.append(_flat(weight, H, bf16, "weight"))
-    for t, name in ((sum_out, "sum_out"), (y, "y")):
-        args += _rows_of(t, rows, H, bf16, name)
-    args += _rows_of(q, rows, H, _dtypes("int8"), "q")
-    args += _scales_of(q_scale, rows, "q_scale")
-    _check(lib().moe_rms_norm(rows, H, float(eps), *args, _stream(stream)), "moe_rms_norm")
-
-
-def _scales_of(t, rows, name):
-    """(address, bytes from one to the next) of rows float32 scales (None -> NULL)."""
-    if t is None:
-        return None, 0
-    if t.numel() != rows or t.dim() < 1 or t.shape[0] != rows:
-        raise ValueError("expected %s of %d scales, got %s" % (name, rows, tuple(t.shape)))
-    if rows > 1 and t.stride(0) < 1:
-        raise ValueError("expected %s with a stride of its own for every row" % name)
-    return _cuda_tensor(t, _dtypes("float32"), name), 4 * t.stride(0) if rows > 1 else 4
+    bf16 = _t().bf16
+    st = lib().moe_rms_norm(rows, H, eps, *_rows_of(x, rows, H, bf16, 2, "x"), *_rows_of(residual, rows, H, bf16, 2, "residual"),
+                            _flat(weight, H, bf16, "weight"), *_rows_of(sum_out, rows, H, bf16, 2, "sum_out"),
+                            *_rows_of(y, rows, H, bf16, 2, "y"), *_rows_of(q, rows, H, _t().i8, 1, "q"),
+                            *_scales_of(q_scale, rows, "q_scale"), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_rms_norm")
 
 
 def moe_rms_norm_grad_scratch_bytes(rows: int, H: int) -> int:
@@ -599,17 +621,16 @@ def moe_rms_norm_grad(dy, h, weight, eps, dh, dweight=None, dsum=None, scratch=N
     """Gradient of moe_rms_norm at h, the sum as it was kept: dh [rows, H] bf16 and dweight [H] float32 (needs scratch)
     from dy and dsum (bf16 rows, dsum the gradient of the sum passed on). Rows may be apart."""
     rows, H = h.shape
-    bf16 = _dtypes("bfloat16")
+    bf16 = _t().bf16
     if dweight is not None and scratch is None:
         raise ValueError("dweight needs scratch (rms_norm_grad_scratch)")
-    args = [*_rows_of(dy, rows, H, bf16, "dy"), *_rows_of(h, rows, H, bf16, "h"), _flat(weight, H, bf16, "weight"),
-            *_rows_of(dsum, rows, H, bf16, "dsum"), *_rows_of(dh, rows, H, bf16, "dh"),
-            _flat(dweight, H, _dtypes("float32"), "dweight")]
-    if scratch is not None:
-        args += [_flat(scratch, scratch.numel(), _dtypes("uint8"), "scratch"), scratch.numel()]
-    else:
-        args += [None, 0]
-    _check(lib().moe_rms_norm_grad(rows, H, float(eps), *args, _stream(stream)), "moe_rms_norm_grad")
+    n = 0 if scratch is None else scratch.numel()
+    st = lib().moe_rms_norm_grad(rows, H, eps, *_rows_of(dy, rows, H, bf16, 2, "dy"), *_rows_of(h, rows, H, bf16, 2, "h"),
+                                 _flat(weight, H, bf16, "weight"), *_rows_of(dsum, rows, H, bf16, 2, "dsum"),
+                                 *_rows_of(dh, rows, H, bf16, 2, "dh"), _flat(dweight, H, _t().f32, "dweight"),
+                                 _flat(scratch, n, _t().u8, "scratch"), n, _stream(stream))
+    if st:
+        raise MoeError(st, "moe_rms_norm_grad")
 
 
 class Int8Rows:
@@ -631,8 +652,8 @@ class Int8Rows:
 
     def _call(self, pack, x, E, plan, stream):
         n = self.groups * self.rows
-        b = _rows_of(x, n, self.width, _dtypes("bfloat16"), "x" if pack else "out")
-        q = _rows_of(self.q, n, self.width, _dtypes("int8"), "q")
+        b = _rows_of(x, n, self.width, _t().bf16, 2, "x" if pack else "out")
+        q = _rows_of(self.q, n, self.width, _t().i8, 1, "q")
         s = _scales_of(self.scale, n, "scale")
         name = "moe_int8_pack" if pack else "moe_int8_unpack"
         st = getattr(lib(), name)(self.groups, self.rows, self.width, self.gated, *((*b, *q, *s) if pack else (*q, *s, *b)),
@@ -1167,7 +1188,7 @@ class Buffers:
         if self._expert_arena is None or getattr(self, "plan", None) is None:
             raise ValueError("expected dispatch_expert and expert_plan before the product")
         N = weights.rows
-        out = _flat(y, self.expert_rows * (N // 2 if weights.gated else N), _dtypes("bfloat16"), "y")
+        out = _flat(y, self.expert_rows * (N // 2 if weights.gated else N), _t().bf16, "y")
         arena = self._expert_arena
         moe_expert_product_int8(s.E, N, s.H, weights.gated, weights.q, weights.scale, arena,
                                 arena.data_ptr() + (s.H + 31) // 32 * 32, self.expert_rows, self.plan, out, self.err,
