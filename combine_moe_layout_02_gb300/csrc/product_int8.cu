@@ -37,9 +37,10 @@ constexpr int kStageK = 128;                // codes of K per stage: one 128-byt
 constexpr uint32_t kWBytes = 128 * 128;     // a CTA's weight rows of a stage
 constexpr uint32_t kXBox = 32 * 128;        // 32 rows of a stage
 constexpr uint32_t kOutStride = 80;         // bytes per staged row: 64 and a shift of 4 banks per row
-constexpr uint32_t kOutBytes = 4 * 16 * kOutStride;
-constexpr uint32_t kScaleBytes = 4 * kPlanTileRows * 4;  // the rows' scales, for each of four warps
+constexpr uint32_t kOutBytes = 16 * kOutStride;             // of a warp that takes sums out
+constexpr uint32_t kScaleBytes = kPlanTileRows * 4;         // the rows' scales, for it
 constexpr uint32_t kBarBytes = 512;
+constexpr uint32_t kSentBytes = 128 * 64;  // a CTA's sums of 16 rows, binary32
 constexpr int kAcc1 = 128;  // second place of the sums
 constexpr int kSharedChunks = (256 - kAcc1) / 16;
 constexpr int kMostSlots = 8, kMostStages = 9;
@@ -50,20 +51,24 @@ template <bool THIN>
 struct Cut {
     static constexpr int kRows = THIN ? 64 : 256;
     static constexpr int kStages = THIN ? 9 : 4;
+    static constexpr int kEpiWarps = THIN ? 4 : 8;                   // that take sums out: one or two for each quarter of the lanes
     static constexpr int kGroups = 4;                     // of four converting warps: two take turns at the halves of K
-    static constexpr int kThreads = 256 + 128 * kGroups;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps + 128 * kGroups;
     static constexpr int kSlots = THIN ? 8 : 4;                      // places of f16 operands, one or two each group's
     static constexpr int kPer = kSlots / kGroups;
     static constexpr int kACol = THIN ? 256 : 384;                   // the f16 weights, 32 columns a place
     static constexpr uint32_t kStageBytes = kWBytes + kRows / 64 * kXBox;
     static constexpr uint32_t kHalfBytes = kRows / 2 * 128;          // a CTA's rows of 64 f16
-    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kSlots * kHalfBytes + kOutBytes + kScaleBytes + kBarBytes;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kSlots * kHalfBytes + kEpiWarps * (kOutBytes + kScaleBytes) + kBarBytes;
+    // parts of K: what the other pairs send of the chunks that a pair finishes, half of a tile's sums
+    static_assert(kRows / 16 * kSentBytes / 2 <= kStages * kStageBytes + kSlots * kHalfBytes, "room for sums");
     static_assert(kACol + 32 * kSlots == 512 && kSlots <= kMostSlots && kStages <= kMostStages && kSmem <= 227 * 1024, "room");
 };
 
 struct Args {
     ProductInt8Args p;
     int32_t shift;        // a dense call's row tiles are 256 / 2^shift rows
+    int32_t split;        // pairs that share the K of a tile: 1, or 2, one cluster (and one tile to it)
     int64_t wait_cycles;  // bound of a wait (kWaitCycles)
     int32_t quit_warp;    // test hook: a warp of each CTA that acts as if its first wait had run out, or -1
     int32_t* err;
@@ -77,6 +82,8 @@ struct Bars {
     uint64_t used[kMostSlots];    // each CTA: the products that read a place are done
     uint64_t acc_full[2];     // each CTA: a tile's sums are complete
     uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place of the sums
+    uint64_t may_send;        // each CTA, K in parts: the other pairs have room for its sums
+    uint64_t joined;          // each CTA, K in parts: the other pairs' sums are there
     uint64_t shared_free;     // leading CTA: both CTAs have read the tile's part of the shared columns
     uint64_t drain;           // leading CTA, after a failed wait: products in flight are done
     uint32_t tmem;
@@ -116,6 +123,23 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
+}
+
+// Arrives on `bar` of both CTAs of the pair led by `lead` once every product issued so far is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3u << lead))
+        : "memory");
+}
+
+// Arrival on a barrier of another CTA that hands over data written to it.
+__device__ __forceinline__ void arrive_with_data(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void write_cluster(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 __device__ __forceinline__ uint4 read_shared(uint32_t addr) {
@@ -212,15 +236,17 @@ __global__ void __launch_bounds__(Cut<THIN>::kThreads, 1)
 product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
     constexpr int kStages = Cut<THIN>::kStages, kSlots = Cut<THIN>::kSlots, kACol = Cut<THIN>::kACol, kRows = Cut<THIN>::kRows;
     constexpr uint32_t kStageBytes = Cut<THIN>::kStageBytes, kHalfBytes = Cut<THIN>::kHalfBytes, kTurns = Cut<THIN>::kGroups / 2, kPer = Cut<THIN>::kPer;
+    constexpr int kEpiWarps = Cut<THIN>::kEpiWarps, kParts = kEpiWarps / 4;
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs of the pair (their shared windows are alike).
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     unsigned char* halves = smem + kStages * kStageBytes;
     unsigned char* out_stage = halves + kSlots * kHalfBytes;
-    float* scales = reinterpret_cast<float*>(out_stage + kOutBytes);
-    Bars* bars = reinterpret_cast<Bars*>(out_stage + kOutBytes + kScaleBytes);
+    float* scales = reinterpret_cast<float*>(out_stage + kEpiWarps * kOutBytes);
+    Bars* bars = reinterpret_cast<Bars*>(out_stage + kEpiWarps * (kOutBytes + kScaleBytes));
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t cta = cluster_ctarank();  // of the pair; 0 leads
+    const uint32_t rank = cluster_ctarank(), cta = rank & 1, lead = rank & ~1u;  // of the pair, 0 leads; the leading CTA
+    const int kpart = static_cast<int>(rank >> 1);                               // the pair's part of K
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -233,9 +259,11 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->acc_full[i], 1);
-            mbar_init(&bars->acc_empty[i], 8);
+            mbar_init(&bars->acc_empty[i], 2 * kEpiWarps);
         }
-        mbar_init(&bars->shared_free, 8);
+        mbar_init(&bars->may_send, max(1, kEpiWarps * (a.split - 1)));
+        mbar_init(&bars->joined, max(1, kEpiWarps * (a.split - 1)));
+        mbar_init(&bars->shared_free, 2 * kEpiWarps);
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         mbar_init_fence();
@@ -260,8 +288,9 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         tiles = planned < 0 ? 0 : (planned > tiles ? tiles : planned);
     }
     const uint32_t parts = static_cast<uint32_t>(tiles), mtiles = (a.p.N + kMTile - 1) / kMTile;
-    const uint32_t step = gridDim.x / 2, first = blockIdx.x / 2;
+    const uint32_t step = gridDim.x / (2 * a.split), first = blockIdx.x / (2 * a.split);
     const int nstages = static_cast<int>(ceil_div(a.p.K, kStageK));
+    const int k_first = nstages * kpart / a.split, k_end = nstages * (kpart + 1) / a.split;  // the pair's stages
     const bool short_end = a.p.K - (nstages - 1) * kStageK <= kStageK / 2;  // the last stage has one half
     if (warp == a.quit_warp) give_up(bars, a);
 
@@ -278,7 +307,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             const uint32_t bytes = kWBytes + boxes * kXBox;
             const int32_t x0 = t.row + static_cast<int32_t>(cta * (n / 2));
             const int32_t m0 = t.m0 + static_cast<int32_t>(cta) * 128;
-            for (int k = 0; k < nstages; ++k) {
+            for (int k = k_first; k < k_end; ++k) {
                 if (issued >= kStages && !wait_here(bars, &bars->empty[s], phase ^ 1, a)) {
                     ok = false;
                     break;
@@ -324,11 +353,11 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                 ok = wait_here(bars, &bars->shared_free, (i - 1) & 1, a);
             tc_fence_after();
             last_n = n;
-            for (int k = 0; ok && k < nstages; ++k) {
-                const bool end = k == nstages - 1;
+            for (int k = k_first; ok && k < k_end; ++k) {
+                const bool end = k == k_end - 1, short_now = short_end && k == nstages - 1;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (half == 1 && end && short_end) break;
+                    if (half == 1 && short_now) break;
                     uint32_t u = uses[half];
                     if (kTurns > 1 && turn) u = uses[2 * kTurns - 2 + half];
                     const uint32_t slot = (2 * turn + half) * kPer + u % kPer;
@@ -345,9 +374,10 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     if (elected()) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma(acc, tmem + kACol + 32 * slot + 8 * j, b + 2 * j, instr(n), k > 0 || half > 0 || j > 0);
-                        commit_to(&bars->used[slot]);
-                        if (end && (half == 1 || short_end)) commit_to(&bars->acc_full[place]);
+                            mma(acc, tmem + kACol + 32 * slot + 8 * j, b + 2 * j, instr(n),
+                                k > k_first || half > 0 || j > 0);
+                        commit_pair(&bars->used[slot], lead);
+                        if (end && (half == 1 || short_now)) commit_pair(&bars->acc_full[place], lead);
                     }
                     __syncwarp();
                 }
@@ -363,15 +393,15 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             drained(&bars->drain, 0);
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    } else if (warp >= 4 + kEpiWarps) {
         // Four warps a group: of every kTurns stages one, of its K one half.
-        const int group = (warp - 8) >> 2, half = group & 1, w = warp & 3;
+        const int group = (warp - 4 - kEpiWarps) >> 2, half = group & 1, w = warp & 3;
         const int row = w * 32 + lane;           // lane of tensor memory and weight row
         const int xrow = 8 * w + (lane & 7), xpart = lane >> 3;  // of the rows: which one, and which 16 of 64 codes
         const uint32_t xfrom = ((4 * half + xpart) ^ (xrow & 7)) << 4, xto = ((2 * xpart) ^ (xrow & 7)) << 4;
         const uint32_t to = tmem + kACol + 32 * kPer * group + (static_cast<uint32_t>(w * 32) << 16);
         const uint32_t mine = smem_addr(halves) + kPer * group * kHalfBytes + xrow * 128;
-        const uint32_t ready = cluster_map(bars->ready + kPer * group, 0);
+        const uint32_t ready = cluster_map(bars->ready + kPer * group, lead);
         uint32_t s = 0, phase = 0, uses = 0, turn = 0;
         bool ok = warp != a.quit_warp;
         Units<kRows> list(a, parts, mtiles, first, step);
@@ -379,7 +409,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const int rows = static_cast<int>(mma_n(t.n) / 2);
-            for (int k = 0; k < nstages; ++k) {
+            for (int k = k_first; k < k_end; ++k) {
                 const uint32_t at = s, parity = phase;
                 if (++s == kStages) {
                     s = 0;
@@ -439,10 +469,10 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             }
         }
     } else if (warp >= 4) {
-        const int w = warp & 3;  // lane quarter
-        unsigned char* stage_ptr = out_stage + w * 16 * kOutStride;
+        const int w = warp & 3, part = (warp - 4) >> 2;  // lane quarter; which of every kParts chunks of 16 rows
+        unsigned char* stage_ptr = out_stage + (warp - 4) * 16 * kOutStride;
         const uint32_t stage = smem_addr(stage_ptr);
-        float* xs = scales + w * kPlanTileRows;
+        float* xs = scales + (warp - 4) * kPlanTileRows;
         // stmatrix: block q of 8 lanes; ungated blocks are the warp's four
         // groups of 8 weight rows, gated two groups of each of two column blocks.
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
@@ -471,10 +501,42 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             tc_fence_after();
             const uint32_t acc = tmem + (place ? kAcc1 : 0) + (static_cast<uint32_t>(w * 32) << 16);
             const int chunks = static_cast<int>(mma_n(t.n) / 16);
+            // K in parts: of every `split` chunks of 16 rows each pair finishes one and writes its sums of the
+            // others to the shared memory of the pair that finishes those, where loads and products are done
+            // by then, 16 a thread and chunk.
+            const uint32_t sent = smem_addr(smem) + (w * 32 + lane) * 16;
+            const int per = (chunks + a.split - 1) / a.split;  // chunks that a pair finishes
+            if (a.split > 1) {
+                if (lane == 0)
+                    for (int p = 0; p < a.split; ++p)
+                        if (p != kpart) arrive_with_data(cluster_map(&bars->may_send, 2 * p + cta));
+                if (!wait_for(bars, &bars->may_send, 0, a)) break;
+                for (int c = 0; c < chunks; ++c) {
+                    const int o = c % a.split;
+                    if (o == kpart || c / a.split % kParts != part) continue;
+                    const uint32_t there = cluster_map(smem, 2 * o + cta) - smem_addr(smem) + sent +
+                                           ((kpart < o ? kpart : kpart - 1) * per + c / a.split) * kSentBytes;
+                    uint32_t v[2][8];
+                    tmem_load(acc + 16 * c, v[0]);
+                    tmem_load(acc + 16 * c + (16u << 16), v[1]);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        write_cluster(there + i * 2048, v[i >> 1][4 * (i & 1)], v[i >> 1][4 * (i & 1) + 1], v[i >> 1][4 * (i & 1) + 2],
+                                      v[i >> 1][4 * (i & 1) + 3]);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    for (int p = 0; p < a.split; ++p)
+                        if (p != kpart) arrive_with_data(cluster_map(&bars->joined, 2 * p + cta));
+                if (!wait_for(bars, &bars->joined, 0, a)) break;
+            }
             // Place 0 has the shared columns at its end, place 1 at its start:
             // they are read first.
-            for (int q = 0; q < chunks; ++q) {
-                const int c = place ? q : chunks - 1 - q;
+            for (int q = 0; q < chunks / kParts; ++q) {
+                const int at = kParts * q + part;
+                const int c = a.split > 1 ? at * a.split + kpart : place ? at : chunks - 1 - at;
+                if (c >= chunks) break;  // of the pair's own there are fewer
                 uint32_t v[2][8];
                 tmem_load(acc + 16 * c, v[0]);
                 tmem_load(acc + 16 * c + (16u << 16), v[1]);
@@ -482,8 +544,24 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (q == min(kSharedChunks, chunks) - 1) mbar_arrive_cluster(cluster_map(&bars->shared_free, 0));
-                    if (q == chunks - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], 0));
+                    if (q == min(kSharedChunks, chunks) / kParts - 1) mbar_arrive_cluster(cluster_map(&bars->shared_free, lead));
+                    if (q == chunks / kParts - 1) mbar_arrive_cluster(cluster_map(&bars->acc_empty[place], lead));
+                }
+                if (a.split > 1) {  // the parts' sums in ascending order
+                    float s[2][8];
+                    for (int p = 0; p < a.split; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t* own = &v[i >> 1][4 * (i & 1)];
+                            uint4 o = make_uint4(own[0], own[1], own[2], own[3]);
+                            if (p != kpart) o = read_shared(sent + ((p < kpart ? p : p - 1) * per + c / a.split) * kSentBytes + i * 2048);
+                            float* to = &s[i >> 1][4 * (i & 1)];
+                            const float f[4] = {__uint_as_float(o.x), __uint_as_float(o.y), __uint_as_float(o.z), __uint_as_float(o.w)};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) to[j] = p == 0 ? f[j] : to[j] + f[j];
+                        }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __float_as_uint(s[i >> 3][i & 7]);
                 }
                 const int c0 = 16 * c;  // first of the chunk's rows
                 if (m >= a.p.N || c0 >= t.n) continue;
@@ -554,57 +632,77 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs that can be resident at once on the current device (cached); allows the kernel its shared memory.
+// Clusters of `split` pairs that can be resident at once on the current device (cached); allows the kernel its shared memory.
 template <bool GATED, bool THIN>
-int resident_pairs() {
-    static std::atomic<int> cache[64];
+int resident_clusters(int split) {
+    static std::atomic<int> cache[2][64];
+    const int at = split - 1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     const bool slot = dev >= 0 && dev < 64;
-    if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
+    if (slot && cache[at][dev].load(std::memory_order_relaxed) > 0) return cache[at][dev].load(std::memory_order_relaxed);
     if (prepare_kernel(reinterpret_cast<const void*>(product_int8_kernel<GATED, THIN>), Cut<THIN>::kSmem, Cut<THIN>::kThreads, nullptr) != cudaSuccess)
         return -1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(2 * split);
     cfg.blockDim = dim3(Cut<THIN>::kThreads);
     cfg.dynamicSmemBytes = Cut<THIN>::kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 2 * split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, product_int8_kernel<GATED, THIN>, &cfg) != cudaSuccess || n < 1) return -1;
-    if (slot) cache[dev].store(n, std::memory_order_relaxed);
+    if (slot) cache[at][dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
-// Rows of a dense call's tiles, 256 / 2^shift, so that the pairs have work: of the sizes
-// the one whose rounds of units are over first, a unit taking 2 cycles per row and 64 of K
-// but no less than the weights' conversion does.
-int32_t tile_shift(const ProductInt8Args& p, int pairs) {
-    int32_t best = 0;
+// How a call is cut: rows of a tile (256 >> shift; a plan's are 256), and pairs to a tile's K.
+struct Plan {
+    int shift, split;
+    bool thin;
+};
+
+// The cut whose rounds of units are over first, by what a unit of 256 / 128 / 64 or less rows takes: 0.27 / 0.21
+// / 0.20 us per 64 of K (the products, or the weights' conversion), 2.5 / 0.6 / 0 for its sums that nothing
+// overlaps; two pairs that share K take 4 more to join (256 rows 7168 -> 4096: 39 / 30 / 28 us, shared 29 / 23 /
+// -; 64 rows 28, shared 20; 256 rows 2048 -> 2048: 17 / 13 / 12, shared 17 / 14 / 13). They share it only where
+// every cluster has one tile. (Clusters of four pairs are resident too rarely.)
+template <bool GATED>
+bool cut(const ProductInt8Args& p, Plan* best) {
     double least = 0;
-    for (int32_t shift = 0; shift <= 3; ++shift) {
-        const int32_t size = kPlanTileRows >> shift;
-        const int64_t units = ceil_div(p.rows, size) * ceil_div(p.N, kMTile);
-        const double time = static_cast<double>(ceil_div(units, pairs)) * (2 * size > 230 ? 2 * size : 230);
-        if (shift == 0 || time < least) {
-            best = shift;
-            least = time;
+    const int stages = static_cast<int>(ceil_div(p.K, kStageK));
+    for (int shift = 0; shift <= (p.plan ? 0 : 3); ++shift) {
+        const int size = kPlanTileRows >> shift;
+        const bool thin = size <= Cut<true>::kRows;
+        const int64_t tiles = p.plan ? p.tile_cap : ceil_div(p.rows, size), units = tiles * ceil_div(p.N, kMTile);
+        const double of_k = shift == 0 ? 0.27 : shift == 1 ? 0.21 : 0.20, sums = shift == 0 ? 2.5 : shift == 1 ? 0.6 : 0.0;
+        for (int split = 1; split <= 2; ++split) {
+            const int clusters = thin ? resident_clusters<GATED, true>(split) : resident_clusters<GATED, false>(split);
+            if (clusters < 1) {
+                if (split == 1) return false;
+                continue;
+            }
+            if (split > 1 && (units > clusters || stages < 4)) continue;
+            const double time = static_cast<double>(ceil_div(units, clusters)) * (ceil_div(2 * stages, split) * of_k + sums) +
+                                (split > 1 ? 4.0 : 0.0);
+            if (shift + split == 1 || time < least) {
+                *best = Plan{shift, split, thin};
+                least = time;
+            }
         }
     }
-    return best;
+    return true;
 }
 
 template <bool GATED, bool THIN>
-cudaError_t launch_pairs(Args a, cudaStream_t stream) {
+cudaError_t launch_pairs(const Args& a, cudaStream_t stream) {
     const ProductInt8Args& p = a.p;
-    const auto kernel = product_int8_kernel<GATED, THIN>;
-    const int pairs = resident_pairs<GATED, THIN>();
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    const int clusters = resident_clusters<GATED, THIN>(a.split);
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
     const int64_t most = static_cast<int64_t>(p.tile_cap) * ceil_div(p.N, kMTile);
     if (most > INT32_MAX) return cudaErrorInvalidValue;  // units are counted in 32 bits
     if (encoder() == nullptr) return cudaErrorNotSupported;
@@ -621,8 +719,25 @@ cudaError_t launch_pairs(Args a, cudaStream_t stream) {
         const cuuint32_t box[2] = {kStageK, 32};
         if (!encode(&xmap, p.xq, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const unsigned grid = 2u * static_cast<unsigned>(most < pairs ? most : pairs);
-    return launch_pdl_cluster(kernel, grid, Cut<THIN>::kThreads, Cut<THIN>::kSmem, 2u, stream, a, wmap, xmap);
+    const unsigned ctas = 2u * static_cast<unsigned>(a.split), grid = ctas * static_cast<unsigned>(most < clusters ? most : clusters);
+    return launch_pdl_cluster(product_int8_kernel<GATED, THIN>, grid, Cut<THIN>::kThreads, Cut<THIN>::kSmem, ctas, stream, a, wmap, xmap);
+}
+
+template <bool GATED>
+cudaError_t launch_cut(Args a, cudaStream_t stream) {
+    Plan plan{0, 1, false};
+    if (!cut<GATED>(a.p, &plan)) return cudaErrorInvalidConfiguration;
+    if (a.p.plan) {
+        // Experts of few rows: half the shared memory for rows makes room for more stages. 256 experts 7168 -> 4096, 2 / 64 /
+        // 128 rows each: 1187 / 1196 / 2368 us (which takes their rows 64 at a time) against 1218 / 1300 / 1384, so only
+        // where hardly any has more than 64.
+        plan.thin = plan.split == 1 && a.p.plan_rows <= 8 * static_cast<int64_t>(a.p.E);
+    } else {
+        a.p.tile_cap = static_cast<int32_t>(ceil_div(a.p.rows, kPlanTileRows >> plan.shift));
+    }
+    a.shift = plan.shift;
+    a.split = plan.split;
+    return plan.thin ? launch_pairs<GATED, true>(a, stream) : launch_pairs<GATED, false>(a, stream);
 }
 
 }  // namespace
@@ -634,20 +749,9 @@ cudaError_t launch_product_int8(const ProductInt8Args& p, cudaStream_t stream) {
     // against 27; 8192 -> 16384 has 64 units for the 76 pairs).
     if (p.plan == nullptr && (p.rows <= 8 || (p.rows <= kInt8FewRows && ceil_div(p.N, kMTile) * 4 <= device_sm_count())))
         return launch_product_int8_rows(p, stream);
-    Args a{p, 0, kWaitCycles, -1, p.err};
+    Args a{p, 0, 1, kWaitCycles, -1, p.err};
     take_product_wait_test(&a.wait_cycles, &a.quit_warp);
-    bool thin;
-    if (p.plan) {
-        thin = p.plan_rows <= 8 * static_cast<int64_t>(p.E);
-    } else {
-        const int pairs = resident_pairs<false, false>();
-        if (pairs < 1) return cudaErrorInvalidConfiguration;
-        a.shift = tile_shift(p, pairs);
-        a.p.tile_cap = static_cast<int32_t>(ceil_div(p.rows, kPlanTileRows >> a.shift));
-        thin = a.shift > 0;
-    }
-    return p.gated ? (thin ? launch_pairs<true, true>(a, stream) : launch_pairs<true, false>(a, stream))
-                   : (thin ? launch_pairs<false, true>(a, stream) : launch_pairs<false, false>(a, stream));
+    return p.gated ? launch_cut<true>(a, stream) : launch_cut<false>(a, stream);
 }
 
 }  // namespace moe
