@@ -10,19 +10,29 @@
 //
 // A pair of CTAs (one per SM) computes 256 weight rows x up to 256 of an expert's
 // rows; the weights are the M side, so that few rows cost a thin instruction. Each
-// CTA has its 128 weight rows and half of the rows. Per 128 of K: warp 0 loads codes
-// (TMA, a ring of stages), warps 8-15 turn them into f16 -- the weights' straight
-// into tensor memory, from where the instruction takes its A side, the rows' into
-// shared memory, swizzled as its B side is --, warp 1 of the leading CTA issues
-// the products of K = 16, warps 4-7 of both CTAs take the sums out, times the
-// scales. Either group of four converting warps has a half of every 128 of K and a
-// place of its own for the result, so one converts while the other's is multiplied.
-// Weights through tensor memory save shared memory's rate: a stage's 64 of K are 16
-// KB of codes in, 16 out, 16 of f16 rows in and 16 out, 64 KB in the 512 cycles of
-// its products, at 128 bytes a cycle.
+// CTA has its 128 weight rows and half of the rows. Warp 0 loads codes (TMA, 128 of K
+// to a stage, a ring of stages); four groups of four warps turn them into f16 -- the
+// weights' straight into tensor memory, from where the instruction takes its A side,
+// the rows' into shared memory, swizzled as its B side is --, two groups by turns at
+// a stage, one at each half of its K; warp 1 of the leading CTA issues the products
+// of K = 16; the warps from 4 on take the sums out, times the scales. A group has places
+// of its own for what it makes, so they work while others' places are multiplied.
 //
-// Tensor memory: sums in two places, columns 0 and 192 on, which share 64 columns
-// (read first and given back early), and the f16 weights' two places of 32 columns.
+// What bounds it. Many rows: the tensor pipe and power (262144 rows 7168 -> 4096 gated:
+// 8.0-8.4 ms, 1.84-1.92 PFLOP/s; bursts of 8192 rows 2.0). Weights through tensor memory
+// save shared memory's rate: 64 of K are 16 KB of codes in, 16 out, 16 of f16 rows in and
+// 16 out, 64 KB in the 512 cycles of their products, at 128 bytes a cycle. Few rows:
+// the weights' bytes (64 tokens over 256 experts: 1.18 ms, 6.4 TB/s), with conversion
+// close behind (0.2 us per 64 of K and SM; without it the same call takes 1.09 ms).
+// Two groups instead of four: 1.65 ms. Arrivals and waits that release and acquire at the
+// cluster's scope instead of the CTA's cost both twice the time (3.6 and 14.4 ms): what
+// an arrival hands over are tensor memory, ordered by the tcgen05 fences, and f16 rows,
+// for which every writer has fenced the async proxy.
+//
+// Tensor memory: sums in two places, columns 0 and 128 on, which share 128 columns in
+// tiles of more than 128 rows (read first and given back early), and the f16 weights,
+// 32 columns to a place. Dense calls short of tiles cut them smaller, or let two pairs
+// share a tile's K and join through each other's shared memory (the rule is at cut()).
 #include <atomic>
 
 #include "fp4.cuh"
@@ -45,8 +55,8 @@ constexpr int kAcc1 = 128;  // second place of the sums
 constexpr int kSharedChunks = (256 - kAcc1) / 16;
 constexpr int kMostSlots = 8, kMostStages = 9;
 
-// Up to 256 rows to a tile, or (THIN) up to 128: half the rows in shared memory make
-// room for more stages, half the sums in tensor memory for more places of f16 weights.
+// Up to 256 rows to a tile, or (THIN) up to 64: fewer rows in shared memory make room
+// for more stages, fewer sums in tensor memory for more places of f16 weights.
 template <bool THIN>
 struct Cut {
     static constexpr int kRows = THIN ? 64 : 256;
