@@ -22,8 +22,7 @@
 // two of the K + 1 largest differ in the replaced bits only (a 16-bit logit has nothing
 // in them), or there is a NaN, the token is selected again with whole numbers of all
 // bits. (A maximum of all bits and then the lowest expert that has it, by two joins and a
-// search of the lane's V for each of the K, took twice as long.) The softmax is shifted by
-// the first of them, which is the largest logit but for those bits.
+// search of the lane's V for each of the K, took twice as long.)
 //
 // Sums over tokens are binary32 per warp, joined in a fixed order. More than 1024
 // experts: rows in shared memory, selection by search (the _wide kernels).
@@ -165,12 +164,11 @@ __device__ __forceinline__ void sort_descending(uint32_t (&k)[V]) {
     }
 }
 
-// The K largest of the warp's logits: lane k's expert, or -1 in lanes past the last. *top: the
-// largest, but for the bits that an expert's number takes (0: none that may be chosen).
-// SHORT: the logits are 16-bit numbers. lists [V + 1][32]: the warp's, in shared memory, a
-// lane's column; the last row is 0.
+// The K largest of the warp's logits: lane k's expert, or -1 in lanes past the last. SHORT: the
+// logits are 16-bit numbers. lists [V + 1][32]: the warp's, in shared memory, a lane's
+// column; the last row is 0.
 template <int V, int VEC, bool SHORT>
-__device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, uint32_t* lists, uint32_t* top) {
+__device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, uint32_t* lists) {
     constexpr uint32_t kNumber = 32u * V - 1;  // the bits of an expert's number
     uint32_t* own = lists + lane;
     uint32_t head;
@@ -197,8 +195,6 @@ __device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, 
         head = *own;
     }
     const uint32_t before = __shfl_up_sync(kAll, mine, 1);
-    *top = __shfl_sync(kAll, mine, 0);
-    *top = *top > kNoLogit ? *top & ~kNumber : 0u;
     int32_t at = mine > kNoLogit && lane < K ? static_cast<int32_t>(kNumber - (mine & kNumber)) : -1;
     if (SHORT || !__any_sync(kAll, lane >= 1 && mine > kNoLogit && (mine | kNumber) == (before | kNumber))) return at;
     // All bits: the largest, then the lowest expert that has it.
@@ -322,18 +318,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
             for (int i = 0; i < V; ++i) logits[expert_of<1>(i, lane)] = z[i];
         }
         __syncwarp();
-        uint32_t most = 0;
-        const int32_t at = out ? -1 : select<V, VEC, sizeof(T) == 2>(z, a.K, lane, lists, &most);
+        const int32_t at = out ? -1 : select<V, VEC, sizeof(T) == 2>(z, a.K, lane, lists);
         const float chosen = at >= 0 ? logits[at] : kNegInf;
+        const float top = __shfl_sync(kAll, chosen, 0);  // the largest logit, NaN where there is one
         __syncwarp();  // the lists and the logits have been read
-        if (most == 0) {
+        if (top == kNegInf) {  // no expert was found
             if (lane < a.K) {
                 a.topk_idx[g * a.K + lane] = -1;
                 a.topk_weights[g * a.K + lane] = 0.f;
             }
             continue;
         }
-        const float top = logit_of(most);  // NaN or infinity where it is one
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {

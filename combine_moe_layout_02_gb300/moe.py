@@ -454,6 +454,7 @@ class _Types:
         import torch
 
         self.bf16, self.f32, self.i8, self.u8, self.flag = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.bool
+        self.i16, self.u16 = torch.int16, torch.uint16  # bf16 bit patterns
         self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -671,16 +672,31 @@ class Int8Rows:
         return out
 
 
+def _held(t, rows, stride, row_bytes, dtypes, name):
+    """Address of a tensor that holds `rows` rows of row_bytes, `stride` bytes apart; an address is taken as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in dtypes or not t.is_contiguous() or (rows > 0 and t.nbytes < (rows - 1) * stride + row_bytes):
+        raise ValueError("expected %s contiguous in %s with %d rows of %d bytes, %d apart, got %s in %s" % (
+            name, " or ".join(str(d) for d in dtypes), rows, row_bytes, stride, tuple(t.shape), t.dtype))
+    return _placed(t, name)
+
+
 def moe_expert_product_int8(E, N, K, gated, wq, ws, xq, xs, rows, plan, y, err, x_row_stride=None, xs_stride=4,
                             y_row_stride=None, stream=None):
     """y's rows of every expert (plan None, E 1: of all rows) from int8 weights and rows (include/moe.h). Rows of xq are
-    packed, scales of xs one after another and y rows packed unless the strides (bytes) say otherwise."""
-    if y_row_stride is None:
-        y_row_stride = (N // 2 if gated else N) * 2
-    st = lib().moe_expert_product_int8(int(E), int(N), int(K), int(gated), _ptr(wq), _ptr(ws), _ptr(xq),
-                                       int(K if x_row_stride is None else x_row_stride), _ptr(xs), int(xs_stride), int(rows),
-                                       *_plan_args(E, plan)[1:], _ptr(y), int(y_row_stride), _ptr(err), _stream(stream))
-    _check(st, "moe_expert_product_int8")
+    packed, scales of xs one after another and y rows packed unless the strides (bytes) say otherwise. Tensors are held to
+    their sizes and types; addresses (of the scales in dispatch's slots, say) are taken as they are."""
+    T, width = _t(), (N // 2 if gated else N) * 2
+    x_row_stride = K if x_row_stride is None else x_row_stride
+    y_row_stride = width if y_row_stride is None else y_row_stride
+    st = lib().moe_expert_product_int8(
+        E, N, K, gated, _held(wq, E * N, K, K, (T.i8,), "wq"), _held(ws, E * N, 4, 4, (T.f32,), "ws"),
+        _held(xq, rows, x_row_stride, K, (T.i8, T.u8), "xq"), x_row_stride, _held(xs, rows, xs_stride, 4, (T.f32,), "xs"), xs_stride,
+        rows, *_plan_args(E, plan)[1:], _held(y, rows, y_row_stride, width, (T.bf16, T.i16, T.u16), "y"), y_row_stride, _ptr(err),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_expert_product_int8")
 
 
 # The types of a layer call's batch tensors; 16-bit whole numbers are bf16 bit patterns.
@@ -1179,7 +1195,7 @@ class Buffers:
     # ---- int8 experts (quant = 1, after layout, notify, notify_expert, expert_plan and dispatch_expert) ----
     def expert_product_int8(self, weights: Int8Rows, y, stream=None):
         """y's rows of every expert from the int8 slots that dispatch_expert filled: weights groups = E operands of N x H
-        (gated: y rows are silu(gate) * up), y bf16 [expert_rows, N or N / 2], rows contiguous."""
+        (gated: y rows are silu(gate) * up), y bf16 [expert_rows, N or N / 2] or more rows, contiguous."""
         s = self.shape
         if not s.quant:
             raise ValueError("expected the int8 payload (quant = 1)")
@@ -1188,10 +1204,9 @@ class Buffers:
         if self._expert_arena is None or getattr(self, "plan", None) is None:
             raise ValueError("expected dispatch_expert and expert_plan before the product")
         N = weights.rows
-        out = _flat(y, self.expert_rows * (N // 2 if weights.gated else N), _t().bf16, "y")
         arena = self._expert_arena
         moe_expert_product_int8(s.E, N, s.H, weights.gated, weights.q, weights.scale, arena,
-                                arena.data_ptr() + (s.H + 31) // 32 * 32, self.expert_rows, self.plan, out, self.err,
+                                arena.data_ptr() + (s.H + 31) // 32 * 32, self.expert_rows, self.plan, y, self.err,
                                 x_row_stride=self.stride, xs_stride=self.stride, stream=stream)
 
     def dispatch_fused(self, x, topk_idx, topk_weights, stream=None):

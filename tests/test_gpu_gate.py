@@ -166,6 +166,32 @@ def test_infinities_and_nan(E):
     assert dz[[2, 3, 6]].isnan().any(1).all() and not dz[1].any() and dz[[0, 4, 5, 7]].isfinite().all()
 
 
+@pytest.mark.parametrize("E", [50, 256, 1000, 1200])
+def test_large_logits(E):
+    """Logits whose neighbours in binary32 are as far apart as their exponentials: only differences count."""
+    import torch
+
+    g = torch.Generator().manual_seed(E)
+    z = torch.randint(0, 16, (40, E), generator=g).float()
+    z[:10] += 2.0 ** 23
+    z[10:20] -= 2.0 ** 23
+    z[20:30] = z[20:30] * 2.0 ** 100  # one or a few experts take all
+    z[30:] = torch.where(z[30:] > 7, torch.finfo(torch.float32).max, torch.finfo(torch.float32).min)
+    op = _gate(40, E, 6, balance=0.1)
+    op.forward(z.cuda())
+    z64 = z.double().numpy()
+    f = ref.gate(z64, 6, balance=0.1)
+    assert np.array_equal(op.topk_idx.cpu().numpy(), f["idx"])
+    rel = ref.gate_rel(np.minimum(z64[:20] - z64[:20].min(1, keepdims=True), 16))
+    w = f["weights"]
+    assert (np.abs(op.topk_weights.cpu().numpy() - w) <= w * (2 * rel + 12 * ref.ULP)).all()
+    dw = torch.randn((40, 6), generator=g)
+    dz = op.backward(z.cuda(), dw.cuda(), torch.ones(1, device="cuda"))
+    want, mag = ref.gate_grad(f, f["idx"], dw.double().numpy(), 1.0, True, 1.0, 0.1)
+    tol = mag * (4 * rel + (E / 32 + 30) * ref.ULP) + np.abs(want) * 2.0 ** -24 + 1e-37
+    assert (np.abs(dz.double().cpu().numpy() - want) <= tol).all()
+
+
 def test_no_token_is_routed():
     import torch
 

@@ -149,3 +149,39 @@ def test_helpers_refuse_on_the_host(lib):
         g.forward(torch.zeros((4, 15)))
     with pytest.raises(ValueError, match="unit column stride"):
         g.forward(torch.zeros((1, 16)).expand(4, 16))  # rows on top of one another
+
+
+def test_the_product_holds_tensors_to_their_sizes(lib):
+    E, N, K, rows = 2, 64, 32, 5
+    good = dict(wq=torch.zeros((E, N, K), dtype=torch.int8), ws=torch.zeros((E, N)), xq=torch.zeros((rows, K), dtype=torch.int8),
+                xs=torch.zeros(rows), y=torch.zeros((rows, N), dtype=torch.bfloat16))
+
+    def call(match, **k):
+        a = {**good, **k}
+        with pytest.raises(ValueError, match=match):
+            moe.moe_expert_product_int8(E, N, K, 0, a["wq"], a["ws"], a["xq"], a["xs"], rows, None, a["y"], None)
+
+    call("expected a CUDA tensor")
+    call("wq", wq=torch.zeros((E, N, K - 1), dtype=torch.int8))
+    call("wq", wq=torch.zeros((E, N, K)))
+    on = lambda **k: {**{n: A for n in good}, **k}
+    call("ws", **on(ws=torch.zeros((E, N - 1))))
+    call("ws", **on(ws=torch.zeros((E, N), dtype=torch.float64)))
+    call("xq", **on(xq=torch.zeros((rows - 1, K), dtype=torch.int8)))
+    call("xq", **on(xq=torch.zeros((rows, K)).t()))
+    call("xs", **on(xs=torch.zeros(rows - 1)))
+    call("y", **on(y=torch.zeros((rows, N - 1), dtype=torch.bfloat16)))
+    call("y", **on(y=torch.zeros((rows, N))))
+
+
+def test_buffers_refuse_a_product_before_its_rows(lib):
+    s = moe.make_shape(1, 4, 8, 2, 64, expert_alignment=128, quant=1)
+    buf = moe.Buffers(s, "cpu")
+    w = moe.Int8Rows(32, 64, "cpu", groups=4)
+    y = torch.zeros((1, 32), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="before the product"):
+        buf.expert_product_int8(w, y)
+    with pytest.raises(ValueError, match="weights of 4 experts"):
+        buf.expert_product_int8(moe.Int8Rows(32, 48, "cpu", groups=4), y)
+    with pytest.raises(ValueError, match="int8 payload"):
+        moe.Buffers(moe.make_shape(1, 4, 8, 2, 64, expert_alignment=128), "cpu").expert_product_int8(w, y)
