@@ -454,8 +454,10 @@ class _Types:
         import torch
 
         self.bf16, self.f32, self.i8, self.u8, self.flag = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.bool
-        self.i16, self.u16 = torch.int16, torch.uint16  # bf16 bit patterns
-        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        # int8 codes (dispatch's slots are bytes); scales; bf16 rows or their bit patterns
+        self.codes, self.scales, self.rows = (torch.int8, torch.uint8), (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
+        get = getattr(torch._C, "_cuda_getDevice", None)
+        self.device = get if get is not None and torch.cuda.is_available() else lambda: torch.cuda.current_device() if torch.cuda.is_available() else 0
 
 
 _types = None
@@ -493,32 +495,30 @@ def _flat(t, n, dtype, name):
     return _placed(t, name)
 
 
-def _rows_of(t, rows, width, dtype, size, name):
-    """(address, bytes from row to row) of a tensor [rows, width] of `size` bytes an element whose rows may be apart
-    (None -> NULL)."""
+def _rows_of(t, shape, dtype, size, name, device):
+    """(address, bytes from row to row) of a tensor of shape [rows, width] on the current device, `size` bytes an element,
+    whose rows may be apart (None -> NULL)."""
     if t is None:
         return None, 0
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr(), shape[1] * size  # the usual rows; all others and what is refused below
+    rows, width = shape
     if t.dtype is not dtype:
         _typed(t, dtype, name)
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != width:
+    if tuple(t.shape) != (rows, width):
         raise ValueError("expected %s of shape %s, got %s" % (name, (rows, width), tuple(t.shape)))
-    if rows <= 1:  # one row's stride says nothing
-        if width > 1 and t.stride(1) != 1:
-            raise ValueError("expected %s with unit column stride, got strides %s" % (name, t.stride()))
-        return _placed(t, name), (width * size + 15) // 16 * 16
-    if t.is_contiguous():
-        return _placed(t, name), width * size
-    if (width > 1 and t.stride(1) != 1) or t.stride(0) < width:
+    if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < width):
         raise ValueError("expected %s with unit column stride and rows that do not overlap, got strides %s" % (name, t.stride()))
-    return _placed(t, name), t.stride(0) * size
+    return _placed(t, name), (t.stride(0) if rows > 1 else width) * size
 
 
 def _scales_of(t, rows, name):
     """(address, bytes from one to the next) of rows float32 scales (None -> NULL)."""
     if t is None:
         return None, 0
-    _typed(t, _t().f32, name)
-    if t.dim() < 1 or t.size(0) != rows or t.numel() != rows:
+    if t.dtype is not _t().f32:
+        _typed(t, _t().f32, name)
+    if t.numel() != rows or t.dim() < 1 or t.size(0) != rows:
         raise ValueError("expected %s of %d scales, got %s" % (name, rows, tuple(t.shape)))
     if rows <= 1:
         return _placed(t, name), 4
@@ -549,13 +549,13 @@ class Gate:
         self.expert_prob = torch.empty((E,), dtype=torch.float32, device=device)
         self.loss = torch.empty((1,), dtype=torch.float32, device=device)
         self.scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-        self._shape, self._nbytes = ctypes.byref(shape), nbytes
+        self._shape, self._nbytes, self._rows = ctypes.byref(shape), nbytes, (S, E)
 
     def _logits(self, t, name):
         half = t.dtype is _t().bf16
         if not half and t.dtype is not _t().f32:
             raise ValueError("expected %s in torch.float32 or torch.bfloat16, got %s" % (name, t.dtype))
-        return (int(half), *_rows_of(t, self.shape.S, self.shape.E, t.dtype, 2 if half else 4, name))
+        return (int(half), *_rows_of(t, self._rows, t.dtype, 2 if half else 4, name, _t().device()))
 
     def _mask(self, mask):
         return None if mask is None else _flat(mask, self.shape.S, _t().flag if mask.dtype is _t().flag else _t().u8, "mask")
@@ -576,10 +576,11 @@ class Gate:
         s, f32 = self.shape, _t().f32
         args = self._logits(logits, "logits")
         if dlogits is None:
-            import torch
-
-            with _made_on(stream, logits.device):
-                dlogits = torch.empty((s.S, s.E), dtype=logits.dtype, device=logits.device)
+            if stream is None:
+                dlogits = logits.new_empty(self._rows)
+            else:
+                with _made_on(stream, logits.device):
+                    dlogits = logits.new_empty(self._rows)
         elif dlogits.dtype is not logits.dtype:
             raise ValueError("expected dlogits in %s, got %s" % (logits.dtype, dlogits.dtype))
         st = lib().moe_gate_grad(self._shape, *args, self._mask(mask), self.normalize, self.scale, self.balance,
@@ -594,12 +595,13 @@ class Gate:
 def moe_rms_norm(x, weight, eps, y=None, residual=None, sum_out=None, q=None, q_scale=None, stream=None):
     """Root-mean-square norm of x + residual [rows, H] in bf16 (include/moe.h): y and sum_out bf16 rows, q int8 rows with
     q_scale float32 [rows] (or [rows, 1], a column of any row-strided tensor). Rows may be apart."""
-    rows, H = x.shape
-    bf16 = _t().bf16
-    st = lib().moe_rms_norm(rows, H, eps, *_rows_of(x, rows, H, bf16, 2, "x"), *_rows_of(residual, rows, H, bf16, 2, "residual"),
-                            _flat(weight, H, bf16, "weight"), *_rows_of(sum_out, rows, H, bf16, 2, "sum_out"),
-                            *_rows_of(y, rows, H, bf16, 2, "y"), *_rows_of(q, rows, H, _t().i8, 1, "q"),
-                            *_scales_of(q_scale, rows, "q_scale"), _stream(stream))
+    shape = rows, H = x.shape
+    T = _t()
+    bf16, dev = T.bf16, T.device()
+    st = lib().moe_rms_norm(rows, H, eps, *_rows_of(x, shape, bf16, 2, "x", dev),
+                            *_rows_of(residual, shape, bf16, 2, "residual", dev), _flat(weight, H, bf16, "weight"),
+                            *_rows_of(sum_out, shape, bf16, 2, "sum_out", dev), *_rows_of(y, shape, bf16, 2, "y", dev),
+                            *_rows_of(q, shape, T.i8, 1, "q", dev), *_scales_of(q_scale, rows, "q_scale"), _stream(stream))
     if st:
         raise MoeError(st, "moe_rms_norm")
 
@@ -621,15 +623,16 @@ def rms_norm_grad_scratch(rows: int, H: int, device="cuda"):
 def moe_rms_norm_grad(dy, h, weight, eps, dh, dweight=None, dsum=None, scratch=None, stream=None):
     """Gradient of moe_rms_norm at h, the sum as it was kept: dh [rows, H] bf16 and dweight [H] float32 (needs scratch)
     from dy and dsum (bf16 rows, dsum the gradient of the sum passed on). Rows may be apart."""
-    rows, H = h.shape
-    bf16 = _t().bf16
+    shape = rows, H = h.shape
+    T = _t()
+    bf16, dev = T.bf16, T.device()
     if dweight is not None and scratch is None:
         raise ValueError("dweight needs scratch (rms_norm_grad_scratch)")
     n = 0 if scratch is None else scratch.numel()
-    st = lib().moe_rms_norm_grad(rows, H, eps, *_rows_of(dy, rows, H, bf16, 2, "dy"), *_rows_of(h, rows, H, bf16, 2, "h"),
-                                 _flat(weight, H, bf16, "weight"), *_rows_of(dsum, rows, H, bf16, 2, "dsum"),
-                                 *_rows_of(dh, rows, H, bf16, 2, "dh"), _flat(dweight, H, _t().f32, "dweight"),
-                                 _flat(scratch, n, _t().u8, "scratch"), n, _stream(stream))
+    st = lib().moe_rms_norm_grad(rows, H, eps, *_rows_of(dy, shape, bf16, 2, "dy", dev), *_rows_of(h, shape, bf16, 2, "h", dev),
+                                 _flat(weight, H, bf16, "weight"), *_rows_of(dsum, shape, bf16, 2, "dsum", dev),
+                                 *_rows_of(dh, shape, bf16, 2, "dh", dev), _flat(dweight, H, T.f32, "dweight"),
+                                 _flat(scratch, n, T.u8, "scratch"), n, _stream(stream))
     if st:
         raise MoeError(st, "moe_rms_norm_grad")
 
@@ -650,16 +653,20 @@ class Int8Rows:
         n = self.groups * self.rows
         self.q = torch.empty((n, self.width), dtype=torch.int8, device=device)
         self.scale = torch.empty((n,), dtype=torch.float32, device=device)
+        self._shape, self._sizes = (n, self.width), (self.groups, self.rows, self.width, int(self.gated))
 
     def _call(self, pack, x, E, plan, stream):
-        n = self.groups * self.rows
-        b = _rows_of(x, n, self.width, _t().bf16, 2, "x" if pack else "out")
-        q = _rows_of(self.q, n, self.width, _t().i8, 1, "q")
-        s = _scales_of(self.scale, n, "scale")
-        name = "moe_int8_pack" if pack else "moe_int8_unpack"
-        st = getattr(lib(), name)(self.groups, self.rows, self.width, self.gated, *((*b, *q, *s) if pack else (*q, *s, *b)),
-                                  *_plan_args(E, plan), _stream(stream))
-        _check(st, name)
+        shape, T = self._shape, _t()
+        dev = T.device()
+        b = _rows_of(x, shape, T.bf16, 2, "x" if pack else "out", dev)
+        q, s = _rows_of(self.q, shape, T.i8, 1, "q", dev), _scales_of(self.scale, shape[0], "scale")
+        plan = _NO_PLAN if plan is None else _plan_args(E, plan)
+        if pack:
+            st = lib().moe_int8_pack(*self._sizes, *b, *q, *s, *plan, _stream(stream))
+        else:
+            st = lib().moe_int8_unpack(*self._sizes, *q, *s, *b, *plan, _stream(stream))
+        if st:
+            raise MoeError(st, "moe_int8_pack" if pack else "moe_int8_unpack")
 
     def pack(self, x, E=0, plan=None, stream=None):
         """bf16 rows x [groups * rows, width] into these; with a plan, only the experts' rows."""
@@ -672,14 +679,14 @@ class Int8Rows:
         return out
 
 
-def _held(t, rows, stride, row_bytes, dtypes, name):
+def _held(t, rows, stride, row_bytes, dtypes, name, device):
     """Address of a tensor that holds `rows` rows of row_bytes, `stride` bytes apart; an address is taken as it is."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype not in dtypes or not t.is_contiguous() or (rows > 0 and t.nbytes < (rows - 1) * stride + row_bytes):
+    if t.dtype not in dtypes or not t.is_contiguous() or (t.nbytes < (rows - 1) * stride + row_bytes and rows > 0):
         raise ValueError("expected %s contiguous in %s with %d rows of %d bytes, %d apart, got %s in %s" % (
             name, " or ".join(str(d) for d in dtypes), rows, row_bytes, stride, tuple(t.shape), t.dtype))
-    return _placed(t, name)
+    return t.data_ptr() if t.get_device() == device else _placed(t, name)
 
 
 def moe_expert_product_int8(E, N, K, gated, wq, ws, xq, xs, rows, plan, y, err, x_row_stride=None, xs_stride=4,
@@ -688,13 +695,15 @@ def moe_expert_product_int8(E, N, K, gated, wq, ws, xq, xs, rows, plan, y, err, 
     packed, scales of xs one after another and y rows packed unless the strides (bytes) say otherwise. Tensors are held to
     their sizes and types; addresses (of the scales in dispatch's slots, say) are taken as they are."""
     T, width = _t(), (N // 2 if gated else N) * 2
+    dev = T.device()
     x_row_stride = K if x_row_stride is None else x_row_stride
     y_row_stride = width if y_row_stride is None else y_row_stride
     st = lib().moe_expert_product_int8(
-        E, N, K, gated, _held(wq, E * N, K, K, (T.i8,), "wq"), _held(ws, E * N, 4, 4, (T.f32,), "ws"),
-        _held(xq, rows, x_row_stride, K, (T.i8, T.u8), "xq"), x_row_stride, _held(xs, rows, xs_stride, 4, (T.f32,), "xs"), xs_stride,
-        rows, *_plan_args(E, plan)[1:], _held(y, rows, y_row_stride, width, (T.bf16, T.i16, T.u16), "y"), y_row_stride, _ptr(err),
-        _stream(stream))
+        E, N, K, gated, _held(wq, E * N, K, K, T.codes, "wq", dev), _held(ws, E * N, 4, 4, T.scales, "ws", dev),
+        _held(xq, rows, x_row_stride, K, T.codes, "xq", dev), x_row_stride,
+        _held(xs, rows, xs_stride, 4, T.scales, "xs", dev), xs_stride, rows,
+        *(_NO_PLAN if plan is None else _plan_args(E, plan))[1:], _held(y, rows, y_row_stride, width, T.rows, "y", dev),
+        y_row_stride, _ptr(err), _stream(stream))
     if st:
         raise MoeError(st, "moe_expert_product_int8")
 
