@@ -19,15 +19,15 @@
 // of its own for what it makes, so they work while others' places are multiplied.
 //
 // What bounds it. Many rows: the tensor pipe and power (262144 rows 7168 -> 4096 gated:
-// 8.0-8.4 ms, 1.84-1.92 PFLOP/s; bursts of 8192 rows 2.0). Weights through tensor memory
-// save shared memory's rate: 64 of K are 16 KB of codes in, 16 out, 16 of f16 rows in and
-// 16 out, 64 KB in the 512 cycles of their products, at 128 bytes a cycle. Few rows:
-// the weights' bytes (64 tokens over 256 experts: 1.18 ms, 6.4 TB/s), with conversion
-// close behind (0.2 us per 64 of K and SM; without it the same call takes 1.09 ms).
-// Two groups instead of four: 1.65 ms. Arrivals and waits that release and acquire at the
-// cluster's scope instead of the CTA's cost both twice the time (3.6 and 14.4 ms): what
-// an arrival hands over are tensor memory, ordered by the tcgen05 fences, and f16 rows,
-// for which every writer has fenced the async proxy.
+// 8.0-8.4 ms, 1.84-1.92 PFLOP/s; bursts of 8192 rows 2.0; back to back for seconds 9.6).
+// Weights through tensor memory save shared memory's rate: 64 of K are 16 KB of codes in,
+// 16 out, 16 of f16 rows in and 16 out, 64 KB in the 512 cycles of their products, at 128
+// bytes a cycle. Few rows: the weights' bytes (2 rows to each of 256 experts: 1.09 ms,
+// 6.9 TB/s). What it took there: four converting groups (two: 1.65 ms); one place to a
+// group (two, which let groups run ahead of the products: 1.18); four warps for the sums
+// (eight: 1.18); and arrivals and waits at the CTA's scope (at the cluster's 3.6, and many
+// rows 14.4): what an arrival hands over is tensor memory, ordered by the tcgen05 fences,
+// and f16 rows, for which every writer has fenced the async proxy.
 //
 // Tensor memory: sums in two places, columns 0 and 128 on, which share 128 columns in
 // tiles of more than 128 rows (read first and given back early), and the f16 weights,
@@ -53,26 +53,22 @@ constexpr uint32_t kBarBytes = 512;
 constexpr uint32_t kSentBytes = 128 * 64;  // a CTA's sums of 16 rows, binary32
 constexpr int kAcc1 = 128;  // second place of the sums
 constexpr int kSharedChunks = (256 - kAcc1) / 16;
-constexpr int kMostSlots = 8, kMostStages = 9;
+constexpr int kMostStages = 10;
+constexpr int kGroups = 4;     // of four converting warps: two by turns at a stage, one at each half of its K
+constexpr int kACol = 512 - 32 * kGroups;  // the f16 weights: a place of 32 columns for each group
 
-// Up to 256 rows to a tile, or (THIN) up to 64: fewer rows in shared memory make room
-// for more stages, fewer sums in tensor memory for more places of f16 weights.
-template <bool THIN>
+// Up to ROWS rows to a tile: fewer of them in shared memory make room for more stages.
+template <int ROWS>
 struct Cut {
-    static constexpr int kRows = THIN ? 64 : 256;
-    static constexpr int kStages = THIN ? 9 : 4;
-    static constexpr int kEpiWarps = THIN ? 4 : 8;                   // that take sums out: one or two for each quarter of the lanes
-    static constexpr int kGroups = 4;                     // of four converting warps: two take turns at the halves of K
+    static constexpr int kStages = ROWS <= 64 ? 10 : ROWS <= 128 ? 7 : 4;
+    static constexpr int kEpiWarps = ROWS <= 128 ? 4 : 8;            // that take sums out: one or two for each quarter of the lanes
     static constexpr int kThreads = 128 + 32 * kEpiWarps + 128 * kGroups;
-    static constexpr int kSlots = THIN ? 8 : 4;                      // places of f16 operands, one or two each group's
-    static constexpr int kPer = kSlots / kGroups;
-    static constexpr int kACol = THIN ? 256 : 384;                   // the f16 weights, 32 columns a place
-    static constexpr uint32_t kStageBytes = kWBytes + kRows / 64 * kXBox;
-    static constexpr uint32_t kHalfBytes = kRows / 2 * 128;          // a CTA's rows of 64 f16
-    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kSlots * kHalfBytes + kEpiWarps * (kOutBytes + kScaleBytes) + kBarBytes;
+    static constexpr uint32_t kStageBytes = kWBytes + ROWS / 64 * kXBox;
+    static constexpr uint32_t kHalfBytes = ROWS / 2 * 128;           // a CTA's rows of 64 f16
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kGroups * kHalfBytes + kEpiWarps * (kOutBytes + kScaleBytes) + kBarBytes;
     // parts of K: what the other pairs send of the chunks that a pair finishes, half of a tile's sums
-    static_assert(kRows / 16 * kSentBytes / 2 <= kStages * kStageBytes + kSlots * kHalfBytes, "room for sums");
-    static_assert(kACol + 32 * kSlots == 512 && kSlots <= kMostSlots && kStages <= kMostStages && kSmem <= 227 * 1024, "room");
+    static_assert(ROWS / 16 * kSentBytes / 2 <= kStages * kStageBytes + kGroups * kHalfBytes, "room for sums");
+    static_assert(kAcc1 + (ROWS < 256 ? ROWS : 256) <= kACol && kStages <= kMostStages && kSmem <= 227 * 1024, "room");
 };
 
 struct Args {
@@ -88,8 +84,8 @@ struct Args {
 struct Bars {
     uint64_t full[kMostStages];   // each CTA: its loads of a stage have landed
     uint64_t empty[kMostStages];  // each CTA: both groups have read a stage
-    uint64_t ready[kMostSlots];   // leading CTA: both CTAs' f16 operands of a place are there
-    uint64_t used[kMostSlots];    // each CTA: the products that read a place are done
+    uint64_t ready[kGroups];      // leading CTA: both CTAs' f16 operands of a group's place are there
+    uint64_t used[kGroups];       // each CTA: the products that read it are done
     uint64_t acc_full[2];     // each CTA: a tile's sums are complete
     uint64_t acc_empty[2];    // leading CTA: both CTAs have read a place of the sums
     uint64_t may_send;        // each CTA, K in parts: the other pairs have room for its sums
@@ -241,17 +237,16 @@ struct Units {
     }
 };
 
-template <bool GATED, bool THIN>
-__global__ void __launch_bounds__(Cut<THIN>::kThreads, 1)
+template <bool GATED, int ROWS>
+__global__ void __launch_bounds__(Cut<ROWS>::kThreads, 1)
 product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
-    constexpr int kStages = Cut<THIN>::kStages, kSlots = Cut<THIN>::kSlots, kACol = Cut<THIN>::kACol, kRows = Cut<THIN>::kRows;
-    constexpr uint32_t kStageBytes = Cut<THIN>::kStageBytes, kHalfBytes = Cut<THIN>::kHalfBytes, kTurns = Cut<THIN>::kGroups / 2, kPer = Cut<THIN>::kPer;
-    constexpr int kEpiWarps = Cut<THIN>::kEpiWarps, kParts = kEpiWarps / 4;
+    constexpr int kStages = Cut<ROWS>::kStages, kEpiWarps = Cut<ROWS>::kEpiWarps, kParts = kEpiWarps / 4;
+    constexpr uint32_t kStageBytes = Cut<ROWS>::kStageBytes, kHalfBytes = Cut<ROWS>::kHalfBytes;
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs of the pair (their shared windows are alike).
     unsigned char* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     unsigned char* halves = smem + kStages * kStageBytes;
-    unsigned char* out_stage = halves + kSlots * kHalfBytes;
+    unsigned char* out_stage = halves + kGroups * kHalfBytes;
     float* scales = reinterpret_cast<float*>(out_stage + kEpiWarps * kOutBytes);
     Bars* bars = reinterpret_cast<Bars*>(out_stage + kEpiWarps * (kOutBytes + kScaleBytes));
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -263,7 +258,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
             mbar_init(&bars->full[i], 1);
             mbar_init(&bars->empty[i], 8);
         }
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             mbar_init(&bars->ready[i], 8);
             mbar_init(&bars->used[i], 1);
         }
@@ -308,7 +303,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
         bool ok = warp != a.quit_warp;
-        Units<kRows> list(a, parts, mtiles, first, step);
+        Units<ROWS> list(a, parts, mtiles, first, step);
         while (ok && list.more()) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -327,7 +322,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     mbar_arrive_expect_tx(&bars->full[s], bytes);
                     load_3d(base, &wmap, k * kStageK, m0, t.e, bar);
 #pragma unroll
-                    for (int i = 0; i < (kRows + 63) / 64; ++i)
+                    for (int i = 0; i < ROWS / 64; ++i)
                         if (i < boxes) load_2d(base + kWBytes + i * kXBox, &xmap, k * kStageK, x0 + 32 * i, bar);
                 }
                 ++issued;
@@ -347,9 +342,9 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         __syncwarp();
     } else if (warp == 1 && cta == 0) {
         uint32_t i = 0, last_n = 0;  // i: tiles so far
-        uint32_t turn = 0, uses[2 * kTurns] = {};
+        uint32_t turn = 0, parity = 0;  // a bit a group: of its place's next use
         bool ok = warp != a.quit_warp;
-        Units<kRows> list(a, parts, mtiles, first, step);
+        Units<ROWS> list(a, parts, mtiles, first, step);
         while (ok && list.more()) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -368,17 +363,12 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (half == 1 && short_now) break;
-                    uint32_t u = uses[half];
-                    if (kTurns > 1 && turn) u = uses[2 * kTurns - 2 + half];
-                    const uint32_t slot = (2 * turn + half) * kPer + u % kPer;
-                    if (!wait_here(bars, &bars->ready[slot], u / kPer & 1, a)) {
+                    const uint32_t slot = 2 * turn + half;
+                    if (!wait_here(bars, &bars->ready[slot], parity >> slot & 1, a)) {
                         ok = false;
                         break;
                     }
-                    if (kTurns > 1 && turn)
-                        ++uses[2 * kTurns - 2 + half];
-                    else
-                        ++uses[half];
+                    parity ^= 1u << slot;
                     tc_fence_after();
                     const uint64_t b = desc_rows(smem_addr(halves + slot * kHalfBytes));
                     if (elected()) {
@@ -391,7 +381,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     }
                     __syncwarp();
                 }
-                if (kTurns > 1) turn ^= 1;
+                turn ^= 1;
             }
             ++i;
         }
@@ -404,17 +394,17 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         }
         __syncwarp();
     } else if (warp >= 4 + kEpiWarps) {
-        // Four warps a group: of every kTurns stages one, of its K one half.
+        // Four warps a group: of every two stages one, of its K one half.
         const int group = (warp - 4 - kEpiWarps) >> 2, half = group & 1, w = warp & 3;
         const int row = w * 32 + lane;           // lane of tensor memory and weight row
         const int xrow = 8 * w + (lane & 7), xpart = lane >> 3;  // of the rows: which one, and which 16 of 64 codes
         const uint32_t xfrom = ((4 * half + xpart) ^ (xrow & 7)) << 4, xto = ((2 * xpart) ^ (xrow & 7)) << 4;
-        const uint32_t to = tmem + kACol + 32 * kPer * group + (static_cast<uint32_t>(w * 32) << 16);
-        const uint32_t mine = smem_addr(halves) + kPer * group * kHalfBytes + xrow * 128;
-        const uint32_t ready = cluster_map(bars->ready + kPer * group, lead);
+        const uint32_t to = tmem + kACol + 32 * group + (static_cast<uint32_t>(w * 32) << 16);
+        const uint32_t mine = smem_addr(halves) + group * kHalfBytes + xrow * 128;
+        const uint32_t ready = cluster_map(bars->ready + group, lead);
         uint32_t s = 0, phase = 0, uses = 0, turn = 0;
         bool ok = warp != a.quit_warp;
-        Units<kRows> list(a, parts, mtiles, first, step);
+        Units<ROWS> list(a, parts, mtiles, first, step);
         while (ok && list.more()) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -425,19 +415,16 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     s = 0;
                     phase ^= 1;
                 }
-                if (kTurns > 1) {
-                    const uint32_t now = turn;
-                    turn ^= 1;
-                    if (now != static_cast<uint32_t>(group >> 1)) continue;
-                }
+                const uint32_t now = turn;
+                turn ^= 1;
+                if (now != static_cast<uint32_t>(group >> 1)) continue;
                 if (!wait_here(bars, &bars->full[at], parity, a)) {
                     ok = false;
                     break;
                 }
                 const bool skip = half == 1 && short_end && k == nstages - 1;
                 if (!skip) {
-                    const uint32_t slot = uses % kPer;
-                    if (uses >= kPer && !wait_here(bars, &bars->used[kPer * group + slot], (uses / kPer - 1) & 1, a)) {
+                    if (uses > 0 && !wait_here(bars, &bars->used[group], (uses - 1) & 1, a)) {
                         ok = false;
                         break;
                     }
@@ -445,23 +432,23 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     // All codes first: a lane's weight row, and of every 32 rows 16 codes of one (the
                     // lanes of a warp are 8 rows x 4, so that neither side meets in a bank).
                     const uint32_t base = smem_addr(smem + at * kStageBytes);
-                    uint4 wv[4], xv[kRows / 64];
+                    uint4 wv[4], xv[ROWS / 64];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) wv[c] = read_shared(base + row * 128 + (((4 * half + c) ^ (row & 7)) << 4));
 #pragma unroll
-                    for (int j = 0; j < kRows / 64; ++j)
+                    for (int j = 0; j < ROWS / 64; ++j)
                         if (32 * j + 8 * w < rows) xv[j] = read_shared(base + kWBytes + (xrow + 32 * j) * 128 + xfrom);
                     uint32_t h[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) halves16(wv[c], h + 8 * c);
                     tc_fence_after();
-                    tmem_store(to + 32 * slot, h);
+                    tmem_store(to, h);
 #pragma unroll
-                    for (int j = 0; j < kRows / 64; ++j) {
+                    for (int j = 0; j < ROWS / 64; ++j) {
                         if (32 * j + 8 * w >= rows) continue;
                         uint32_t x[8];
                         halves16(xv[j], x);
-                        const uint32_t dst = mine + slot * kHalfBytes + j * 32 * 128;
+                        const uint32_t dst = mine + j * 32 * 128;
                         write_shared(dst + xto, x[0], x[1], x[2], x[3]);
                         write_shared(dst + (xto ^ 16), x[4], x[5], x[6], x[7]);
                     }
@@ -472,7 +459,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(ready + 8 * slot);
+                    if (lane == 0) mbar_arrive_cluster(ready);
                 } else if (lane == 0) {
                     mbar_arrive(&bars->empty[at]);
                 }
@@ -488,7 +475,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
-        Units<kRows> list(a, parts, mtiles, first, step);
+        Units<ROWS> list(a, parts, mtiles, first, step);
         while (list.more()) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
@@ -643,7 +630,7 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 }
 
 // Clusters of `split` pairs that can be resident at once on the current device (cached); allows the kernel its shared memory.
-template <bool GATED, bool THIN>
+template <bool GATED, int ROWS>
 int resident_clusters(int split) {
     static std::atomic<int> cache[2][64];
     const int at = split - 1;
@@ -651,12 +638,12 @@ int resident_clusters(int split) {
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     const bool slot = dev >= 0 && dev < 64;
     if (slot && cache[at][dev].load(std::memory_order_relaxed) > 0) return cache[at][dev].load(std::memory_order_relaxed);
-    if (prepare_kernel(reinterpret_cast<const void*>(product_int8_kernel<GATED, THIN>), Cut<THIN>::kSmem, Cut<THIN>::kThreads, nullptr) != cudaSuccess)
+    if (prepare_kernel(reinterpret_cast<const void*>(product_int8_kernel<GATED, ROWS>), Cut<ROWS>::kSmem, Cut<ROWS>::kThreads, nullptr) != cudaSuccess)
         return -1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * split);
-    cfg.blockDim = dim3(Cut<THIN>::kThreads);
-    cfg.dynamicSmemBytes = Cut<THIN>::kSmem;
+    cfg.blockDim = dim3(Cut<ROWS>::kThreads);
+    cfg.dynamicSmemBytes = Cut<ROWS>::kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * split;
@@ -665,15 +652,20 @@ int resident_clusters(int split) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, product_int8_kernel<GATED, THIN>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_int8_kernel<GATED, ROWS>, &cfg) != cudaSuccess || n < 1) return -1;
     if (slot) cache[at][dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
-// How a call is cut: rows of a tile (256 >> shift; a plan's are 256), and pairs to a tile's K.
+template <bool GATED>
+int resident_clusters(int rows, int split) {
+    return rows <= 64 ? resident_clusters<GATED, 64>(split) : rows <= 128 ? resident_clusters<GATED, 128>(split) : resident_clusters<GATED, 256>(split);
+}
+
+// How a call is cut: rows of a tile (256 >> shift; a plan's are 256), pairs to a tile's K, and the
+// most rows that the kernel takes at a time.
 struct Plan {
-    int shift, split;
-    bool thin;
+    int shift, split, rows;
 };
 
 // The cut whose rounds of units are over first, by what a unit of 256 / 128 / 64 or less rows takes: 0.27 / 0.21
@@ -687,11 +679,10 @@ bool cut(const ProductInt8Args& p, Plan* best) {
     const int stages = static_cast<int>(ceil_div(p.K, kStageK));
     for (int shift = 0; shift <= (p.plan ? 0 : 3); ++shift) {
         const int size = kPlanTileRows >> shift;
-        const bool thin = size <= Cut<true>::kRows;
         const int64_t tiles = p.plan ? p.tile_cap : ceil_div(p.rows, size), units = tiles * ceil_div(p.N, kMTile);
         const double of_k = shift == 0 ? 0.27 : shift == 1 ? 0.21 : 0.20, sums = shift == 0 ? 2.5 : shift == 1 ? 0.6 : 0.0;
         for (int split = 1; split <= 2; ++split) {
-            const int clusters = thin ? resident_clusters<GATED, true>(split) : resident_clusters<GATED, false>(split);
+            const int clusters = resident_clusters<GATED>(size, split);
             if (clusters < 1) {
                 if (split == 1) return false;
                 continue;
@@ -700,7 +691,7 @@ bool cut(const ProductInt8Args& p, Plan* best) {
             const double time = static_cast<double>(ceil_div(units, clusters)) * (ceil_div(2 * stages, split) * of_k + sums) +
                                 (split > 1 ? 4.0 : 0.0);
             if (shift + split == 1 || time < least) {
-                *best = Plan{shift, split, thin};
+                *best = Plan{shift, split, size};
                 least = time;
             }
         }
@@ -708,10 +699,10 @@ bool cut(const ProductInt8Args& p, Plan* best) {
     return true;
 }
 
-template <bool GATED, bool THIN>
+template <bool GATED, int ROWS>
 cudaError_t launch_pairs(const Args& a, cudaStream_t stream) {
     const ProductInt8Args& p = a.p;
-    const int clusters = resident_clusters<GATED, THIN>(a.split);
+    const int clusters = resident_clusters<GATED, ROWS>(a.split);
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     const int64_t most = static_cast<int64_t>(p.tile_cap) * ceil_div(p.N, kMTile);
     if (most > INT32_MAX) return cudaErrorInvalidValue;  // units are counted in 32 bits
@@ -730,24 +721,25 @@ cudaError_t launch_pairs(const Args& a, cudaStream_t stream) {
         if (!encode(&xmap, p.xq, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
     const unsigned ctas = 2u * static_cast<unsigned>(a.split), grid = ctas * static_cast<unsigned>(most < clusters ? most : clusters);
-    return launch_pdl_cluster(product_int8_kernel<GATED, THIN>, grid, Cut<THIN>::kThreads, Cut<THIN>::kSmem, ctas, stream, a, wmap, xmap);
+    return launch_pdl_cluster(product_int8_kernel<GATED, ROWS>, grid, Cut<ROWS>::kThreads, Cut<ROWS>::kSmem, ctas, stream, a, wmap, xmap);
 }
 
 template <bool GATED>
 cudaError_t launch_cut(Args a, cudaStream_t stream) {
-    Plan plan{0, 1, false};
+    Plan plan{0, 1, 256};
     if (!cut<GATED>(a.p, &plan)) return cudaErrorInvalidConfiguration;
     if (a.p.plan) {
-        // Experts of few rows: half the shared memory for rows makes room for more stages. 256 experts 7168 -> 4096, 2 / 64 /
-        // 128 rows each: 1187 / 1196 / 2368 us (which takes their rows 64 at a time) against 1218 / 1300 / 1384, so only
-        // where hardly any has more than 64.
-        plan.thin = plan.split == 1 && a.p.plan_rows <= 8 * static_cast<int64_t>(a.p.E);
+        // By the rows that the routing gives an expert on average: more stages where they are few, against experts of more
+        // rows than the kernel takes at a time, whose weights are read again. 256 experts 7168 -> 4096 with 2 / 64 / 128
+        // rows each: 1085 / 1133 / 2239 us with 64 at a time, 1151 / 1186 / 1345 with 128, 1253 / 1323 / 1430 with 256.
+        const int64_t each = a.p.plan_rows / a.p.E;
+        if (plan.split == 1) plan.rows = each <= 24 ? 64 : each <= 64 ? 128 : 256;
     } else {
         a.p.tile_cap = static_cast<int32_t>(ceil_div(a.p.rows, kPlanTileRows >> plan.shift));
     }
     a.shift = plan.shift;
     a.split = plan.split;
-    return plan.thin ? launch_pairs<GATED, true>(a, stream) : launch_pairs<GATED, false>(a, stream);
+    return plan.rows <= 64 ? launch_pairs<GATED, 64>(a, stream) : plan.rows <= 128 ? launch_pairs<GATED, 128>(a, stream) : launch_pairs<GATED, 256>(a, stream);
 }
 
 }  // namespace
