@@ -87,8 +87,8 @@ __device__ __forceinline__ float half_sum(float v) {
 // ---------------------------------------------------------------------------
 // Up to 1024 experts
 
-// 32-bit words of a lane in a warp's shared memory: V logits, V + 1 rows of lists.
-constexpr int lists_of(int V) { return 2 * V + 1; }
+// 32-bit words of a lane in a warp's shared memory: V logits, V + 2 rows of lists.
+constexpr int lists_of(int V) { return 2 * V + 2; }
 
 // Expert of a lane's i-th logit: VEC neighbours to a load, ascending in i.
 template <int VEC>
@@ -165,8 +165,8 @@ __device__ __forceinline__ void sort_descending(uint32_t (&k)[V]) {
 }
 
 // The K largest of the warp's logits: lane k's expert, or -1 in lanes past the last. SHORT: the
-// logits are 16-bit numbers. lists [V + 1][32]: the warp's, in shared memory, a lane's
-// column; the last row is 0.
+// logits are 16-bit numbers. lists [V + 2][32]: the warp's, in shared memory, a lane's
+// column; row V is 0, row V + 1 takes what was picked.
 template <int V, int VEC, bool SHORT>
 __device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, uint32_t* lists) {
     constexpr uint32_t kNumber = 32u * V - 1;  // the bits of an expert's number
@@ -185,15 +185,23 @@ __device__ __forceinline__ int32_t select(const float (&z)[V], int K, int lane, 
 #pragma unroll
         for (int i = 0; i < V; ++i) own[32 * i] = k[i];
     }
-    uint32_t mine = 0;
+    uint32_t* picked = lists + 32 * (V + 1);
     const int picks = SHORT ? K : K + 1;  // one more, to see whether it is apart from the last
-    for (int j = 0; j < picks; ++j) {
-        const uint32_t best = __reduce_max_sync(kAll, head);
-        if (lane == j) mine = best;
-        // One lane's: the numbers differ. Lanes that have no more stay at their 0, which is picked when all are there.
-        if (head == best && best != 0u) own += 32;
-        head = *own;
+    constexpr int kAtOnce = SHORT ? 4 : 3;
+    static_assert(MOE_MAX_TOPK + kAtOnce <= 32 && 32 * V >= 32, "picks: a lane each, no more than there are numbers");
+    for (int j = 0; j < picks; j += kAtOnce) {
+#pragma unroll
+        for (int n = 0; n < kAtOnce; ++n) {
+            const uint32_t best = __reduce_max_sync(kAll, head);
+            if (head == best) {  // one lane's: the numbers differ; and none is 0, where a lane that has no more stays
+                picked[j + n] = best;
+                own += 32;
+            }
+            head = *own;
+        }
     }
+    __syncwarp();
+    const uint32_t mine = lane <= K ? picked[lane] : 0u;
     const uint32_t before = __shfl_up_sync(kAll, mine, 1);
     int32_t at = mine > kNoLogit && lane < K ? static_cast<int32_t>(kNumber - (mine & kNumber)) : -1;
     if (SHORT || !__any_sync(kAll, lane >= 1 && mine > kNoLogit && (mine | kNumber) == (before | kNumber))) return at;
