@@ -13,8 +13,9 @@
 //
 // A token is a warp's, V of its logits a lane's, in registers; the next token's are
 // loaded meanwhile. The logits are read once and the sums of p stay in registers over
-// a warp's tokens. Bound by the selection's instructions (forward) and by memory
-// (backward).
+// a warp's tokens. Bound by the selection's instructions (forward: 262144 tokens, 256
+// experts, 8 picks 130 us, 2.2 TB/s, 0.73 instructions a cycle) and by memory (backward:
+// 102 us, 5.4 TB/s). Up to 64 experts several tokens share a warp.
 //
 // Selection: whole numbers in the order of the logits, the low bits replaced by the
 // expert's number counted down: one maximum over the warp then gives the next expert,
@@ -90,14 +91,14 @@ __device__ __forceinline__ float half_sum(float v) {
 // 32-bit words of a lane in a warp's shared memory: V logits, V + 2 rows of lists.
 constexpr int lists_of(int V) { return 2 * V + 2; }
 
-// Expert of a lane's i-th logit: VEC neighbours to a load, ascending in i.
-template <int VEC>
+// Expert of a lane's i-th logit, L lanes to a row: VEC neighbours to a load, ascending in i.
+template <int VEC, int L = 32>
 __device__ __forceinline__ int expert_of(int i, int lane) {
-    return (i / VEC) * 32 * VEC + lane * VEC + i % VEC;
+    return (i / VEC) * L * VEC + lane * VEC + i % VEC;
 }
 
 // A lane's raw logits of a row: VEC of them to a load of 16 bytes, or one by one.
-template <typename T, int V, int VEC>
+template <typename T, int V, int VEC, int L = 32>
 struct RowLoad {
     static constexpr int kWords = VEC > 1 ? V * static_cast<int>(sizeof(T)) / 4 : V;
     uint32_t w[kWords];
@@ -107,7 +108,7 @@ struct RowLoad {
         if constexpr (VEC > 1) {
 #pragma unroll
             for (int n = 0; n < V / VEC; ++n) {
-                const int e = expert_of<VEC>(n * VEC, lane);
+                const int e = expert_of<VEC, L>(n * VEC, lane);
                 constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // past the experts: -infinity
                 uint4 v = make_uint4(kNone, kNone, kNone, kNone);
                 if (e < a.E) v = __ldg(reinterpret_cast<const uint4*>(row + e * sizeof(T)));
@@ -119,7 +120,7 @@ struct RowLoad {
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = expert_of<1>(i, lane);
+                const int e = expert_of<1, L>(i, lane);
                 w[i] = __float_as_uint(e < a.E ? logit(reinterpret_cast<const T*>(row), e) : kNegInf);
             }
         }
@@ -288,6 +289,26 @@ __device__ __forceinline__ float loss_of(const GateArgs& a, float sum, int32_t n
     return n > 0 ? a.balance * static_cast<float>(a.E) * (sum / (static_cast<float>(n) * a.K)) : 0.f;
 }
 
+// A block's sums, sum_of(e), and counts to its part; a block alone joins them at once.
+template <typename F>
+__device__ __forceinline__ void leave_parts(const GateArgs& a, const int32_t* count, F sum_of) {
+    float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
+    int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        part[e] = sum_of(e);
+        part_count[e] = count[e];
+    }
+    if (threadIdx.x == 0) part_count[a.E] = count[a.E];
+    if (gridDim.x > 1) return;
+    __syncthreads();  // the block's own words in global memory
+    int32_t n;
+    const float loss = join_parts(a, 1, 0, a.E, &n);
+    if (threadIdx.x == 0) {
+        a.expert_count[a.E] = n;
+        if (a.loss) *a.loss = loss_of(a, loss, n);
+    }
+}
+
 template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a) {
     pdl_wait_then_release();
@@ -361,24 +382,211 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     for (int i = 0; i < V; ++i) logits[expert_of<VEC>(i, lane)] = acc[i];
     if (lane == 0) atomicAdd(&count[a.E], routed_tokens);
     __syncthreads();
-    float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
-    int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    leave_parts(a, count, [&](int e) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kGateWarps; ++w) s += smem[w * kMine + e];
-        part[e] = s;
-        part_count[e] = count[e];
+        return s;
+    });
+}
+
+// ---------------------------------------------------------------------------
+// Up to 64 experts: L lanes to a token, 8 of its logits a lane's, 32 / L neighbouring tokens a
+// warp's. Joins by shuffles among L lanes cost a warp more than one maximum, and serve 32 / L
+// tokens. 262144 tokens, binary32, forward and backward: 8 experts, 2 picks 13 and 10 us (a warp
+// to a token: 73 and 77), 16 experts 17 and 10 (73, 77), 32 experts, 4 picks 28 and 19 (80, 78),
+// 64 experts, 6 picks 53 and 42 (87, 82); of 128 experts, 8 picks, two tokens to a warp would
+// take 116 and 88 (95, 88). Bound by the selection's instructions; small logits by the launch.
+
+constexpr int kTeamV = 8;
+constexpr int kMostInTeams = 64;
+
+template <int L>
+constexpr int kTeams = 32 / L;
+constexpr int kTeamPicks = MOE_MAX_TOPK + 5;  // of a token: K + 1, at a stride that spreads over the banks
+
+// Word of expert e in a warp's columns [8][32], of the first team.
+template <int VEC, int L>
+__device__ __forceinline__ int column_of(int e) {
+    return ((e / (VEC * L)) * VEC + e % VEC) * 32 + (e / VEC) % L;
+}
+
+template <int L>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t team_max(uint32_t v) {
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+}
+// NaN above all.
+template <int L>
+__device__ __forceinline__ float team_top(const float (&z)[kTeamV]) {
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < kTeamV; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(z[i]));
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__shfl_xor_sync(kAll, m, d)));
+    return m;
+}
+
+// As select(), for each team: picked[k] of the K largest, as team_pick() reads it. lists [9][32]:
+// the warp's, the last row 0. live: the team has a token.
+template <int L, int VEC, bool SHORT>
+__device__ __forceinline__ void select_of_team(const float (&z)[kTeamV], int K, int lane, bool live, uint32_t* lists, uint32_t* picked) {
+    constexpr int V = kTeamV;
+    constexpr uint32_t kNumber = V * L - 1;
+    const int l = lane % L;
+    uint32_t* own = lists + lane;
+    uint32_t head;
+    {
+        uint32_t k[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t u = __float_as_int(z[i] + 0.f);  // as in select()
+            k[i] = ((static_cast<uint32_t>(u >> 31) | 0x80000000u) ^ static_cast<uint32_t>(u)) & ~kNumber;
+            k[i] |= kNumber - static_cast<uint32_t>(expert_of<VEC, L>(i, l));
+        }
+        sort_descending(k);
+        head = k[0];
+#pragma unroll
+        for (int i = 0; i < V; ++i) own[32 * i] = k[i];
     }
-    if (threadIdx.x == 0) part_count[a.E] = count[a.E];
-    if (gridDim.x > 1) return;
-    __syncthreads();  // the block's own words in global memory
-    int32_t n;
-    const float loss = join_parts(a, 1, 0, a.E, &n);
-    if (threadIdx.x == 0) {
-        a.expert_count[a.E] = n;
-        if (a.loss) *a.loss = loss_of(a, loss, n);
+    const int picks = SHORT ? K : K + 1;
+    for (int j = 0; j < picks; ++j) {
+        const uint32_t best = team_max<L>(head);
+        if (head == best) {
+            picked[j] = best;
+            if (best != 0u) own += 32;  // (a team may have fewer numbers than picks)
+        }
+        head = *own;
     }
+    __syncwarp();
+    if constexpr (!SHORT) {
+        bool near = false;
+        for (int s = l; s < K; s += L) near |= picked[s + 1] > kNoLogit && (picked[s] | kNumber) == (picked[s + 1] | kNumber);
+        if (!__any_sync(kAll, live && near)) return;
+        __syncwarp();
+        uint32_t taken = 0;
+        for (int j = 0; j < K; ++j) {
+            uint32_t best = 0;
+            int i0 = 0;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i) {
+                const uint32_t o = taken >> i & 1 ? 0u : order_of(z[i]);
+                if (o >= best) {
+                    best = o;
+                    i0 = i;
+                }
+            }
+            const uint32_t all = team_max<L>(best);
+            const uint32_t mine = best == all && all > kNoLogit ? kNumber - static_cast<uint32_t>(expert_of<VEC, L>(i0, l)) + 1u : 0u;
+            const uint32_t first = team_max<L>(mine);  // the lowest expert's
+            if (mine == first) {                       // one lane's, or all write a 0
+                picked[j] = first ? ~kNumber | (first - 1u) : 0u;
+                if (first) taken |= 1u << i0;
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <int L>
+__device__ __forceinline__ int32_t team_pick(uint32_t picked) {
+    constexpr uint32_t kNumber = kTeamV * L - 1;
+    return picked > kNoLogit ? static_cast<int32_t>(kNumber - (picked & kNumber)) : -1;
+}
+
+// Words of a warp: a token's exponentials (in the end the sums of p), lists, picks.
+template <int L>
+constexpr int kTeamWords = 32 * kTeamV + 32 * (kTeamV + 1) + kTeams<L> * kTeamPicks;
+
+template <typename T, int L, int VEC>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_team_kernel(const GateArgs a) {
+    pdl_wait_then_release();
+    constexpr int V = kTeamV, P = kTeams<L>, kMine = kTeamWords<L>;
+    __shared__ float smem[kGateWarps * kMine];
+    __shared__ int32_t count[kMostInTeams + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, team = lane / L;
+    float* column = smem + warp * kMine;
+    uint32_t* lists = reinterpret_cast<uint32_t*>(column + 32 * V);
+    uint32_t* picked = lists + 32 * (V + 1) + team * kTeamPicks;
+    lists[32 * V + lane] = 0u;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) count[e] = 0;
+    __syncthreads();
+    float acc[V] = {};
+    int32_t routed_tokens = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kGateWarps * P);
+    int64_t first = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * P;  // the warp's first token
+    RowLoad<T, V, VEC, L> row = {};
+    uint8_t masked = 0;
+    const auto fetch = [&](int64_t t) {
+        if (t >= a.S) return;
+        row.load(a, t, l);
+        masked = a.mask != nullptr && __ldg(a.mask + t) == 0;
+    };
+    fetch(first + team);
+    for (; first < a.S; first += step) {
+        const int64_t g = first + team;
+        float z[V];
+        row.values(z);
+        bool live = g < a.S && masked == 0;
+        fetch(g + step);
+        const float top = team_top<L>(z);
+        live = live && top != kNegInf;
+        select_of_team<L, VEC, sizeof(T) == 2>(z, a.K, lane, live, lists, picked);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = exp_of(z[i] - top);
+            sum += z[i];
+            column[32 * i + lane] = z[i];
+        }
+        const float inv = inverse_of(team_sum<L>(sum));
+        __syncwarp();
+        const float* mine = column + team * L;
+        float d = 0.f;
+        if (a.normalize) {
+            for (int s = l; s < a.K; s += L) {
+                const int32_t at = team_pick<L>(picked[s]);
+                d += at >= 0 ? mine[column_of<VEC, L>(at)] : 0.f;
+            }
+            d = team_sum<L>(d);
+        }
+        const float share = a.normalize ? __fdividef(a.scale, d) : a.scale * inv;
+        if (g < a.S)
+            for (int s = l; s < a.K; s += L) {
+                const int32_t at = live ? team_pick<L>(picked[s]) : -1;
+                a.topk_idx[g * a.K + s] = at;
+                a.topk_weights[g * a.K + s] = at < 0 ? 0.f : mine[column_of<VEC, L>(at)] * share + 0.f * inv;
+                if (at >= 0) atomicAdd(&count[at], 1);
+            }
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
+            routed_tokens += l == 0;
+        }
+        __syncwarp();  // the columns and the picks have been read
+    }
+    routed_tokens = __reduce_add_sync(kAll, routed_tokens);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int d = 16; d >= L; d >>= 1) acc[i] += __shfl_xor_sync(kAll, acc[i], d);
+        column[32 * i + lane] = acc[i];
+    }
+    if (lane == 0) atomicAdd(&count[a.E], routed_tokens);
+    __syncthreads();
+    leave_parts(a, count, [&](int e) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGateWarps; ++w) s += smem[w * kMine + column_of<VEC, L>(e)];
+        return s;
+    });
 }
 
 // One cluster: each CTA joins a share of the experts, the first one adds the shares' losses up.
@@ -443,6 +651,33 @@ __device__ __forceinline__ float loss_unit(const GateArgs& a) {
     return __ldg(a.dloss) * a.balance * a.E / (static_cast<float>(n) * static_cast<float>(n) * a.K);
 }
 
+// A lane's V of a row.
+template <int V, int VEC, int L = 32, typename T>
+__device__ __forceinline__ void put_row(T* to, int E, int lane, const float (&z)[V]) {
+    if constexpr (VEC > 1) {
+#pragma unroll
+        for (int n = 0; n < V / VEC; ++n) {
+            const int e = expert_of<VEC, L>(n * VEC, lane);
+            if (e >= E) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 2) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(z[n * VEC + 2 * j], z[n * VEC + 2 * j + 1]);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+                } else {
+                    w[j] = __float_as_uint(z[n * VEC + j]);
+                }
+            }
+            *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (expert_of<1, L>(i, lane) < E) put(to + expert_of<1, L>(i, lane), z[i]);
+    }
+}
+
 template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateArgs a) {
     pdl_wait_then_release();
@@ -505,31 +740,117 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateAr
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = routed ? z[i] * inv * (c[i] - t) : 0.f;
-        if constexpr (VEC > 1) {
-#pragma unroll
-            for (int n = 0; n < V / VEC; ++n) {
-                const int e = expert_of<VEC>(n * VEC, lane);
-                if (e >= a.E) continue;
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 2) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(z[n * VEC + 2 * j], z[n * VEC + 2 * j + 1]);
-                        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-                    } else {
-                        w[j] = __float_as_uint(z[n * VEC + j]);
-                    }
-                }
-                *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (expert_of<1>(i, lane) < a.E) put(to + expert_of<1>(i, lane), z[i]);
-        }
+        put_row<V, VEC>(to, a.E, lane, z);
         __syncwarp();  // the chosen experts' over what was stored for them
         if (s.i >= 0) put(to + s.i, s.p * (table[s.i] + s.a - t));
         __syncwarp();
+    }
+}
+
+// As gate_team_kernel. A token's slots are the team's, in turn; the lane that has a slot's expert
+// adds a_k to its column, in ascending order of k.
+__device__ __forceinline__ void fetch_word(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from)
+                 : "memory");
+}
+
+template <typename T, int L, int VEC>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_team_grad_kernel(const GateArgs a) {
+    pdl_wait_then_release();
+    constexpr int V = kTeamV, P = kTeams<L>;
+    const int slots = P * a.K;  // of a warp's tokens
+    extern __shared__ __align__(16) float smem[];
+    __shared__ float table[V * L];  // c of each expert
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, team = lane / L;
+    float* column = smem + warp * (64 * V + 4 * slots);  // the exponentials
+    float* add = column + 32 * V;                         // sum over k with i_k = e of a_k
+    int32_t* ids = reinterpret_cast<int32_t*>(add + 32 * V);
+    float* dws = reinterpret_cast<float*>(ids + 2 * slots);
+    const float unit = loss_unit(a);
+    for (int e = threadIdx.x; e < V * L; e += blockDim.x)
+        table[e] = e < a.E ? unit * static_cast<float>(__ldg(a.expert_count + e)) : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) add[32 * i + lane] = 0.f;
+    __syncthreads();
+    float c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = table[expert_of<VEC, L>(i, l)];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kGateWarps * P);
+    int64_t first = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * P;
+    RowLoad<T, V, VEC, L> row = {};
+    uint8_t masked = 0;
+    // The next tokens' logits in registers, their slots in one of two places; a lane waits for what it has copied.
+    const auto fetch = [&](int64_t f, int place) {
+        if (a.dweights != nullptr && f < a.S) {
+            const int n = static_cast<int>((a.S - f < P ? a.S - f : P)) * a.K;
+            for (int s = lane; s < n; s += 32) {
+                fetch_word(ids + place * slots + s, a.topk_idx + f * a.K + s);
+                fetch_word(dws + place * slots + s, a.dweights + f * a.K + s);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (f + team < a.S) {
+            row.load(a, f + team, l);
+            masked = a.mask != nullptr && __ldg(a.mask + f + team) == 0;
+        }
+    };
+    fetch(first, 0);
+    for (int place = 0; first < a.S; first += step, place ^= 1) {
+        const int64_t g = first + team;
+        float z[V];
+        row.values(z);
+        bool live = g < a.S && masked == 0;
+        fetch(first + step, place ^ 1);
+        const float top = team_top<L>(z);
+        live = live && top != kNegInf;
+        float sum = 0.f, t = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = live ? exp_of(z[i] - top) : 0.f;
+            sum += z[i];
+            t = fmaf(z[i], c[i], t);
+            column[32 * i + lane] = z[i];
+        }
+        sum = team_sum<L>(sum);
+        const float inv = live ? inverse_of(sum) : 0.f;
+        t = team_sum<L>(t) * inv;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        if (a.dweights != nullptr) {
+            const int32_t* i_k = ids + place * slots + team * a.K;
+            const float* dw_k = dws + place * slots + team * a.K;
+            float back = 0.f, d = 0.f;
+            if (live)
+                for (int s = l; s < a.K; s += L) {
+                    const int32_t i = i_k[s];
+                    if (i < 0 || i >= a.E) continue;
+                    const float e = column[team * L + column_of<VEC, L>(i)];
+                    back = fmaf(dw_k[s], e, back);
+                    d += e;
+                }
+            back = team_sum<L>(back);
+            d = team_sum<L>(d);
+            float unit_a = a.scale, mean = 0.f;
+            if (a.normalize) {
+                mean = back / d;
+                unit_a = a.scale / (d * inv);
+            } else {
+                t += a.scale * back * inv;
+            }
+            if (live && (!a.normalize || d > 0.f || d != d))  // (0: no slot, or none that counts)
+                for (int s = 0; s < a.K; ++s) {
+                    const int32_t i = i_k[s];
+                    if (i < 0 || i >= a.E || (i / VEC) % L != l) continue;
+                    add[column_of<VEC, L>(i) - l + lane] += unit_a * (dw_k[s] - mean);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = live ? z[i] * inv * (c[i] + add[32 * i + lane] - t) : 0.f;
+            add[32 * i + lane] = 0.f;  // a lane's own
+        }
+        if (g < a.S) put_row<V, VEC, L>(reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride), a.E, l, z);
+        __syncwarp();  // the columns and the slots have been read
     }
 }
 
@@ -680,14 +1001,30 @@ Kernel kernel_at() {
     else
         return gate_kernel<T, V, VEC>;
 }
-int logits_of_a_lane(int E) { return E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+int logits_of_a_lane(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+int lanes_of_a_token(int E) { return E > kMostInTeams ? 32 : E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8; }
+
+template <bool GRAD, typename T, int L>
+Kernel team_at(bool by) {
+    constexpr int kVec = 16 / sizeof(T);
+    if constexpr (GRAD)
+        return by ? gate_team_grad_kernel<T, L, kVec> : gate_team_grad_kernel<T, L, 1>;
+    else
+        return by ? gate_team_kernel<T, L, kVec> : gate_team_kernel<T, L, 1>;
+}
 
 // by: rows are loaded 16 bytes at a time.
 template <bool GRAD, typename T>
 Kernel kernel_for(int E, bool by) {
+    switch (lanes_of_a_token(E)) {
+        case 1: return team_at<GRAD, T, 1>(by);
+        case 2: return team_at<GRAD, T, 2>(by);
+        case 4: return team_at<GRAD, T, 4>(by);
+        case 8: return team_at<GRAD, T, 8>(by);
+        default: break;
+    }
     constexpr int kVec = 16 / sizeof(T), kVec4 = kVec <= 4 ? kVec : 1;
     switch (logits_of_a_lane(E)) {
-        case 2: return kernel_at<GRAD, T, 2, 1>();
         case 4: return by ? kernel_at<GRAD, T, 4, kVec4>() : kernel_at<GRAD, T, 4, 1>();
         case 8: return by ? kernel_at<GRAD, T, 8, kVec>() : kernel_at<GRAD, T, 8, 1>();
         case 16: return by ? kernel_at<GRAD, T, 16, kVec>() : kernel_at<GRAD, T, 16, 1>();
@@ -697,13 +1034,13 @@ Kernel kernel_for(int E, bool by) {
 
 constexpr int kMostInRegisters = 1024;
 
-// Blocks of `warps` tokens at a time: what is resident, or needed, at most kGateParts.
-cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int64_t S, unsigned* blocks) {
+// Blocks of `tokens` at a time: what is resident, or needed, at most kGateParts.
+cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int tokens, int64_t S, unsigned* blocks) {
     int per_sm = 0;
     const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, 32 * warps, &per_sm);
     int64_t n = static_cast<int64_t>(device_sm_count()) * (per_sm > 0 ? per_sm : 1);
     if (n > kGateParts) n = kGateParts;
-    const int64_t need = ceil_div(S, warps);
+    const int64_t need = ceil_div(S, tokens);
     *blocks = static_cast<unsigned>(need < 1 ? 1 : need < n ? need : n);
     return e;
 }
@@ -713,12 +1050,12 @@ cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int64_t S, unsigne
 cudaError_t launch_gate(const GateArgs& a, cudaStream_t stream) {
     const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride);
     const int warps = wide ? kWideWarps : kGateWarps;
-    const int entries = wide ? 2 * a.E : 32 * lists_of(logits_of_a_lane(a.E));
-    const size_t smem = (static_cast<size_t>(warps) * entries + a.E + 1) * 4;
+    const int lanes = lanes_of_a_token(a.E), entries = wide ? 2 * a.E : 32 * lists_of(logits_of_a_lane(a.E));
+    const size_t smem = lanes < 32 ? 0 : (static_cast<size_t>(warps) * entries + a.E + 1) * 4;
     const Kernel kernel = wide ? (a.bf16 ? gate_wide_kernel<__nv_bfloat16> : gate_wide_kernel<float>)
                                : (a.bf16 ? kernel_for<false, __nv_bfloat16>(a.E, by) : kernel_for<false, float>(a.E, by));
     unsigned blocks = 0;
-    cudaError_t e = blocks_for(kernel, smem, warps, a.S, &blocks);
+    cudaError_t e = blocks_for(kernel, smem, warps, warps * 32 / lanes, a.S, &blocks);
     if (e != cudaSuccess) return e;
     const bool one = !wide && a.S <= kOneBlock;
     if (one) blocks = 1;
@@ -731,11 +1068,14 @@ cudaError_t launch_gate_grad(const GateArgs& a, cudaStream_t stream) {
     if (a.S == 0) return cudaSuccess;
     const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride) && by_16(a, a.dlogits_stride);
     const int warps = wide ? kWideWarps : kGateWarps;
-    const size_t smem = wide ? static_cast<size_t>(warps + 1) * a.E * 4 + static_cast<size_t>(warps) * a.E : 0;
+    const int lanes = lanes_of_a_token(a.E);
+    const size_t smem = wide         ? static_cast<size_t>(warps + 1) * a.E * 4 + static_cast<size_t>(warps) * a.E
+                        : lanes < 32 ? static_cast<size_t>(warps) * (64 * kTeamV + 4 * (32 / lanes) * a.K) * 4
+                                     : 0;
     const Kernel kernel = wide ? (a.bf16 ? gate_wide_grad_kernel<__nv_bfloat16> : gate_wide_grad_kernel<float>)
                                : (a.bf16 ? kernel_for<true, __nv_bfloat16>(a.E, by) : kernel_for<true, float>(a.E, by));
     unsigned blocks = 0;
-    const cudaError_t e = blocks_for(kernel, smem, warps, a.S, &blocks);
+    const cudaError_t e = blocks_for(kernel, smem, warps, warps * 32 / lanes, a.S, &blocks);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, blocks, 32u * warps, smem, stream, a);
 }

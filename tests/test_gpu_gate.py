@@ -297,3 +297,21 @@ def test_same_bits_again_in_a_graph_and_on_another_stream():
     out = op.backward(z[0], dw, dl, stream=side)
     side.synchronize()
     assert torch.equal(out, want[0][5]) and torch.equal(op.loss, want[0][4])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("S,E,K,normalize,banned,masked", [
+    (1, 8, 2, True, 0.0, 0.0),
+    (31, 8, 16, True, 0.0, 0.3),      # twice as many slots as experts
+    (2049, 8, 1, False, 0.2, 0.0),
+    (15, 16, 16, True, 0.0, 0.0),     # all experts of all tokens
+    (5000, 16, 2, True, 0.3, 0.1),
+    (999, 24, 5, False, 0.5, 0.2),
+    (8, 32, 4, True, 0.0, 1.0),       # no token is routed
+    (3001, 60, 4, True, 0.0, 0.0),
+    (70000, 64, 8, True, 0.1, 0.1),   # several turns of every warp
+    (257, 65, 6, True, 0.0, 0.0),     # a warp to a token from here on
+    (70000, 9, 3, False, 0.0, 0.5),
+])
+def test_tokens_that_share_a_warp(S, E, K, normalize, banned, masked, dtype):
+    test_gate_and_gradient(S, E, K, dtype, normalize, 1.5, 0.05, banned, masked)
