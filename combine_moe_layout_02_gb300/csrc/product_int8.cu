@@ -66,15 +66,17 @@ struct Cut {
     static constexpr uint32_t kStageBytes = kWBytes + ROWS / 64 * kXBox;
     static constexpr uint32_t kHalfBytes = ROWS / 2 * 128;           // a CTA's rows of 64 f16
     static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kGroups * kHalfBytes + kEpiWarps * (kOutBytes + kScaleBytes) + kBarBytes;
-    // parts of K: what the other pairs send of the chunks that a pair finishes, half of a tile's sums
-    static_assert(ROWS / 16 * kSentBytes / 2 <= kStages * kStageBytes + kGroups * kHalfBytes, "room for sums");
+    // parts of K: what the other pairs send of the chunks that a pair finishes, less than a tile's sums
+    static_assert(ROWS / 16 * kSentBytes <= kStages * kStageBytes + kGroups * kHalfBytes, "room for sums");
     static_assert(kAcc1 + (ROWS < 256 ? ROWS : 256) <= kACol && kStages <= kMostStages && kSmem <= 227 * 1024, "room");
 };
 
+constexpr int kMostShare = 4;  // 8 CTAs, the largest portable cluster
+
 struct Args {
     ProductInt8Args p;
-    int32_t shift;        // a dense call's row tiles are 256 / 2^shift rows
-    int32_t split;        // pairs that share the K of a tile: 1, or 2, one cluster (and one tile to it)
+    int32_t shift;        // tiles are 256 / 2^shift rows; a plan's are 256 and become 2^shift units, some of them empty
+    int32_t split;        // pairs that share the K of a tile: 1, or 2 to kMostShare, one cluster (and one tile to it)
     int64_t wait_cycles;  // bound of a wait (kWaitCycles)
     int32_t quit_warp;    // test hook: a warp of each CTA that acts as if its first wait had run out, or -1
     int32_t* err;
@@ -185,10 +187,11 @@ template <int ROWS>
 struct Units {
     uint32_t per, part, in, step_part, step_in, left;
     int4 tile;
-    Unit rest;  // what the current unit has left
+    int32_t skip;  // rows of the plan's tile that other units have
+    Unit rest;     // what the current unit has left
 
     __device__ __forceinline__ Units(const Args& a, uint32_t parts, uint32_t mtiles, uint32_t first, uint32_t step)
-        : per(mtiles), tile(make_int4(0, 0, 0, 0)), rest{0, 0, 0, 0} {
+        : per(mtiles), tile(make_int4(0, 0, 0, 0)), skip(0), rest{0, 0, 0, 0} {
         const uint32_t units = parts * mtiles;
         left = first < units ? (units - first - 1) / step + 1 : 0;
         part = first / per;
@@ -199,10 +202,11 @@ struct Units {
     }
     __device__ __forceinline__ void fetch(const Args& a) {
         if (left == 0) return;
+        const int32_t size = kPlanTileRows >> a.shift;
         if (a.p.plan) {
-            tile = __ldg(reinterpret_cast<const int4*>(a.p.plan + plan_tiles_at(a.p.E)) + part);
+            tile = __ldg(reinterpret_cast<const int4*>(a.p.plan + plan_tiles_at(a.p.E)) + (part >> a.shift));
+            skip = static_cast<int32_t>(part & ((1u << a.shift) - 1)) * size;
         } else {
-            const int32_t size = kPlanTileRows >> a.shift;
             const int64_t first = static_cast<int64_t>(part) * size, rows = a.p.rows - first;
             tile = make_int4(0, static_cast<int32_t>(first), static_cast<int32_t>(rows < size ? rows : size), 0);
         }
@@ -219,6 +223,9 @@ struct Units {
                 raise_error(a.err, MOE_ERR_CAPACITY);
                 o.n = 0;
             }
+            const int32_t over = uniform(skip);
+            o.row += over;
+            o.n = max(0, min(o.n - over, kPlanTileRows >> a.shift));
             --left;
             part += step_part;
             in += step_in;
@@ -292,7 +299,7 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         const int32_t planned = uniform(__ldg(a.p.plan));
         tiles = planned < 0 ? 0 : (planned > tiles ? tiles : planned);
     }
-    const uint32_t parts = static_cast<uint32_t>(tiles), mtiles = (a.p.N + kMTile - 1) / kMTile;
+    const uint32_t parts = static_cast<uint32_t>(tiles) << (a.p.plan ? a.shift : 0), mtiles = (a.p.N + kMTile - 1) / kMTile;
     const uint32_t step = gridDim.x / (2 * a.split), first = blockIdx.x / (2 * a.split);
     const int nstages = static_cast<int>(ceil_div(a.p.K, kStageK));
     const int k_first = nstages * kpart / a.split, k_end = nstages * (kpart + 1) / a.split;  // the pair's stages
@@ -632,7 +639,7 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 // Clusters of `split` pairs that can be resident at once on the current device (cached); allows the kernel its shared memory.
 template <bool GATED, int ROWS>
 int resident_clusters(int split) {
-    static std::atomic<int> cache[2][64];
+    static std::atomic<int> cache[kMostShare][64];
     const int at = split - 1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
@@ -668,28 +675,33 @@ struct Plan {
     int shift, split, rows;
 };
 
-// The cut whose rounds of units are over first, by what a unit of 256 / 128 / 64 or less rows takes: 0.27 / 0.21
-// / 0.20 us per 64 of K (the products, or the weights' conversion), 2.5 / 0.6 / 0 for its sums that nothing
-// overlaps; two pairs that share K take 4 more to join (256 rows 7168 -> 4096: 39 / 30 / 28 us, shared 29 / 23 /
-// -; 64 rows 28, shared 20; 256 rows 2048 -> 2048: 17 / 13 / 12, shared 17 / 14 / 13). They share it only where
-// every cluster has one tile. (Clusters of four pairs are resident too rarely.)
+// The cut whose rounds of units are over first, by what a unit of 256 / 128 / 64 / 32 rows takes: 0.27 / 0.19 / 0.175 /
+// 0.17 us per 64 of K (the products, or the weights' conversion), 2.2 / 1.5 / 0.5 / 0 for its sums that nothing
+// overlaps, and, where pairs share its K, 0.015 a row and 0.8 a pair to join them. They share it only where
+// every cluster has one tile, and only there a plan's tiles are cut (of 1 / 2 / 3 / 4 pairs 76 / 36 / 23 / 15 clusters are resident). Microseconds from 1 to
+// 4 pairs: 128 rows 7168 -> 512 in one tile 27.6, 20.4, 18.0, 16.1, in two 24.6, 17.1, 15.2, 13.2, in four
+// 23.8, 15.9, 13.6, 13.0; 64 rows 2048 -> 2048 in two 9.9, 9.0, 9.7; 139 rows 736 -> 320 gated in three 7.2, 8.3, 9.2.
 template <bool GATED>
 bool cut(const ProductInt8Args& p, Plan* best) {
+    constexpr double kOfK[] = {0.27, 0.19, 0.175, 0.17}, kSums[] = {2.2, 1.5, 0.5, 0.0};
     double least = 0;
     const int stages = static_cast<int>(ceil_div(p.K, kStageK));
-    for (int shift = 0; shift <= (p.plan ? 0 : 3); ++shift) {
+    const int64_t each = p.plan ? p.plan_rows / p.E : kPlanTileRows;  // an expert's rows on average
+    for (int shift = 0; shift <= 3; ++shift) {
         const int size = kPlanTileRows >> shift;
-        const int64_t tiles = p.plan ? p.tile_cap : ceil_div(p.rows, size), units = tiles * ceil_div(p.N, kMTile);
-        const double of_k = shift == 0 ? 0.27 : shift == 1 ? 0.21 : 0.20, sums = shift == 0 ? 2.5 : shift == 1 ? 0.6 : 0.0;
-        for (int split = 1; split <= 2; ++split) {
+        const int64_t tiles = p.plan ? static_cast<int64_t>(p.tile_cap) << shift : ceil_div(p.rows, size), units = tiles * ceil_div(p.N, kMTile);
+        int takes = shift;  // what a unit takes: as one of the rows that it has
+        while (takes < 3 && each <= kPlanTileRows >> (takes + 1)) ++takes;
+        for (int split = 1; split <= kMostShare; ++split) {
             const int clusters = resident_clusters<GATED>(size, split);
             if (clusters < 1) {
                 if (split == 1) return false;
                 continue;
             }
-            if (split > 1 && (units > clusters || stages < 4)) continue;
-            const double time = static_cast<double>(ceil_div(units, clusters)) * (ceil_div(2 * stages, split) * of_k + sums) +
-                                (split > 1 ? 4.0 : 0.0);
+            if (split > 1 && (units > clusters || stages < 2 * split)) continue;
+            if (p.plan && shift > 0 && units > clusters) continue;
+            const double time = static_cast<double>(ceil_div(units, clusters)) * (ceil_div(2 * stages, split) * kOfK[takes] + kSums[takes]) +
+                                (split > 1 ? 0.015 * (kPlanTileRows >> takes) + 0.8 * split : 0.0);
             if (shift + split == 1 || time < least) {
                 *best = Plan{shift, split, size};
                 least = time;
@@ -704,7 +716,7 @@ cudaError_t launch_pairs(const Args& a, cudaStream_t stream) {
     const ProductInt8Args& p = a.p;
     const int clusters = resident_clusters<GATED, ROWS>(a.split);
     if (clusters < 1) return cudaErrorInvalidConfiguration;
-    const int64_t most = static_cast<int64_t>(p.tile_cap) * ceil_div(p.N, kMTile);
+    const int64_t most = (static_cast<int64_t>(p.tile_cap) << (p.plan ? a.shift : 0)) * ceil_div(p.N, kMTile);
     if (most > INT32_MAX) return cudaErrorInvalidValue;  // units are counted in 32 bits
     if (encoder() == nullptr) return cudaErrorNotSupported;
     CUtensorMap wmap, xmap;
@@ -733,7 +745,7 @@ cudaError_t launch_cut(Args a, cudaStream_t stream) {
         // rows than the kernel takes at a time, whose weights are read again. 256 experts 7168 -> 4096 with 2 / 64 / 128
         // rows each: 1085 / 1133 / 2239 us with 64 at a time, 1151 / 1186 / 1345 with 128, 1253 / 1323 / 1430 with 256.
         const int64_t each = a.p.plan_rows / a.p.E;
-        if (plan.split == 1) plan.rows = each <= 24 ? 64 : each <= 64 ? 128 : 256;
+        if (plan.split == 1 && plan.shift == 0) plan.rows = each <= 24 ? 64 : each <= 64 ? 128 : 256;
     } else {
         a.p.tile_cap = static_cast<int32_t>(ceil_div(a.p.rows, kPlanTileRows >> plan.shift));
     }

@@ -180,3 +180,36 @@ def test_weights_past_32_bits_of_offset():
     moe.moe_expert_product_int8(1, 256, K, 0, one, scales[-1, -256:].contiguous(), rows, rows.data_ptr() + K, n, None, out, None,
                                 x_row_stride=stride, xs_stride=stride)
     assert torch.equal(out[-40:], y[:, -256:])
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("counts,N,K", [([167, 170], 640, 5408), ([254, 0, 300], 64, 4512), ([1], 512, 1040), ([257], 256, 528),
+                                        ([33, 31, 64, 65], 96, 272), ([0, 0, 5], 160, 2064), ([600, 2], 288, 1296), ([32, 256], 1056, 144)])
+def test_plans_of_few_experts(counts, N, K, gated):
+    """Plans whose every tile may have pairs of its own: tiles in parts, and K shared by two to four pairs."""
+    import torch
+
+    counts = np.array(counts)
+    E = len(counts)
+    plan, first = _plan(E, counts)
+    rows = int(first[-1])
+    wq, ws, xq, xs = _operands(E, N, K, rows, rows + N + K)
+    y = torch.full((rows + 1, N // 2 if gated else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = _err()
+    _call(E, N, K, gated, _up(wq, ws, xq, xs), rows, plan, y, err)
+    got = y.double().cpu().numpy()
+    lives = np.zeros(rows + 1, dtype=bool)
+    for e in range(E):
+        r = slice(int(first[e]), int(first[e]) + int(counts[e]))
+        lives[r] = True
+        if counts[e]:
+            want, off = ref.product(wq[e], ws[e], xq[r], xs[r], gated)
+            _check(got[r], want, off)
+    assert (got[~lives] == 7).all() and not err.any()
+
+
+@pytest.mark.parametrize("rows,N,K", [(17, 32, 32768), (32, 512, 7168), (40, 640, 656), (64, 1024, 3088), (120, 256, 1552),
+                                      (130, 352, 5472), (250, 416, 3872), (256, 768, 1040), (512, 512, 7168), (30, 32, 384)])
+def test_dense_calls_of_which_pairs_share_K(rows, N, K):
+    test_dense_calls_of_every_cut(rows, N, K, 0)
+    test_dense_calls_of_every_cut(rows, N, K, 1)
