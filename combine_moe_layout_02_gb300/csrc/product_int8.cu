@@ -182,7 +182,10 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&h)[32
 // A pair's units, first, first + step, .. of the launch's; the weight rows are the
 // inner index. A role steps from unit to unit without a division and holds the next
 // one's plan words while it works on the current one. A plan's tile of more than
-// ROWS rows is one unit of several tiles.
+// ROWS rows is one unit of several tiles. (Units of their own for each would spread hot
+// experts better, 8008 rows over 249 experts, one with 1001, 2048 -> 7168 701 -> 670 us, but looking
+// them up cost where rows are few, 2 rows each 7168 -> 4096 1098 -> 1135, and many, 1024 each 8.28 -> 8.38 ms. In
+// ranges of even length for each pair, 1098 -> 1280: pairs then read far apart.)
 template <int ROWS>
 struct Units {
     uint32_t per, part, in, step_part, step_in, left;
