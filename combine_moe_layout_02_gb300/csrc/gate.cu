@@ -26,7 +26,7 @@
 // search of the lane's V for each of the K, took twice as long.)
 //
 // Sums over tokens are binary32 per warp, joined in a fixed order. More than 1024
-// experts: rows in shared memory, selection by search (the _wide kernels).
+// experts: a block to a token (the _wide kernels).
 #include <cuda_bf16.h>
 
 #include "experts.cuh"
@@ -34,7 +34,6 @@
 namespace moe {
 namespace {
 
-constexpr int kWideWarps = 4;
 constexpr int kGateWarps = 8;
 constexpr int kOneBlock = 32;  // tokens that one block takes, sums joined on the spot
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -260,11 +259,23 @@ __device__ __forceinline__ float join_parts(const GateArgs& a, int parts, int fi
         const int e = e0 + lane;
         float s = 0.f;
         int32_t c = 0;
-        if (e < end)
-            for (int b = warp; b < parts; b += warps) {
-                s += a.part_prob[static_cast<size_t>(b) * a.E + e];
-                c += a.part_count[static_cast<size_t>(b) * (a.E + 1) + e];
+        constexpr int kAhead = 8;
+        for (int b0 = warp; b0 < parts; b0 += kAhead * warps) {  // eight parts' loads at a time
+            float ps[kAhead];
+            int32_t pc[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int b = b0 + j * warps;
+                const bool there = e < end && b < parts;
+                ps[j] = there ? __ldg(a.part_prob + static_cast<size_t>(b) * a.E + e) : 0.f;
+                pc[j] = there ? __ldg(a.part_count + static_cast<size_t>(b) * (a.E + 1) + e) : 0;
             }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                s += ps[j];
+                c += pc[j];
+            }
+        }
         sums[warp][lane] = s;
         counts[warp][lane] = c;
         __syncthreads();
@@ -292,21 +303,34 @@ __device__ __forceinline__ float loss_of(const GateArgs& a, float sum, int32_t n
 // A block's sums, sum_of(e), and counts to its part; a block alone joins them at once.
 template <typename F>
 __device__ __forceinline__ void leave_parts(const GateArgs& a, const int32_t* count, F sum_of) {
-    float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
-    int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
+    if (gridDim.x > 1) {
+        float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
+        int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+            part[e] = sum_of(e);
+            part_count[e] = count[e];
+        }
+        if (threadIdx.x == 0) part_count[a.E] = count[a.E];
+        return;
+    }
+    __shared__ float losses[32];
+    const int32_t n = count[a.E];
+    const float inv = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+    float loss = 0.f;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        part[e] = sum_of(e);
-        part_count[e] = count[e];
+        const float s = sum_of(e) * inv;
+        a.expert_count[e] = count[e];
+        if (a.expert_prob) a.expert_prob[e] = s;
+        loss += static_cast<float>(count[e]) * s;
     }
-    if (threadIdx.x == 0) part_count[a.E] = count[a.E];
-    if (gridDim.x > 1) return;
-    __syncthreads();  // the block's own words in global memory
-    int32_t n;
-    const float loss = join_parts(a, 1, 0, a.E, &n);
-    if (threadIdx.x == 0) {
-        a.expert_count[a.E] = n;
-        if (a.loss) *a.loss = loss_of(a, loss, n);
-    }
+    loss = warp_sum(loss);
+    if (threadIdx.x % 32 == 0) losses[threadIdx.x / 32] = loss;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    loss = 0.f;
+    for (unsigned w = 0; w < blockDim.x / 32; ++w) loss += losses[w];
+    a.expert_count[a.E] = n;
+    if (a.loss) *a.loss = loss_of(a, loss, n);
 }
 
 template <typename T, int V, int VEC>
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(1024) gate_join_kernel(const GateArgs a, int p
 // over slots of the same expert in ascending order (in all of them); in all lanes t, the sum
 // over k of p[i_k] a_k: scale / D times sum_k dw_k p_k - sum_j dw_j p_j = 0 of normalized
 // weights, scale sum_k dw_k p_k of others. `e`: the slots' exponentials, 0 where there is none;
-// whose [E]: the warp's, in shared memory.
+// whose [E]: the warp's, in shared memory, or none (then the slots are compared).
 struct Slots {
     int32_t i;
     float p, a, t;
@@ -630,10 +654,15 @@ __device__ __forceinline__ Slots slots_of(const GateArgs& a, int lane, int32_t i
         s.t = __shfl_sync(kAll, a.scale * back * inv, 0);
     }
     s.a = own;
-    // Two slots of one expert read back one's lane.
-    if (i >= 0) whose[i] = static_cast<uint8_t>(lane);
-    __syncwarp();
-    if (__any_sync(kAll, i >= 0 && whose[i] != lane)) {
+    bool twice;
+    if (whose != nullptr) {  // two slots of one expert read back one's lane
+        if (i >= 0) whose[i] = static_cast<uint8_t>(lane);
+        __syncwarp();
+        twice = i >= 0 && whose[i] != lane;
+    } else {
+        twice = __popc(__match_any_sync(kAll, i)) > 1 && i >= 0;
+    }
+    if (__any_sync(kAll, twice)) {
         s.a = 0.f;
         for (int k = 0; k < a.K; ++k) {
             const float o = __shfl_sync(kAll, own, k);
@@ -855,131 +884,212 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_team_grad_kernel(const G
 }
 
 // ---------------------------------------------------------------------------
-// More than 1024 experts
+// More than 1024 experts: a block to a token, 512 of its logits a warp's, which finds the K
+// largest of its own as above; the block's are among those. 16384 tokens, 4096 experts, 8 picks, binary32:
+// forward 232 us, backward 95 (5.7 TB/s); as a warp to a token, rows in shared memory and searched for each
+// pick, 1228 and 267. The forward pass is bound by its instructions.
 
+constexpr int kWideV = 16;
+constexpr int kWide = 32 * kWideV;  // experts of a warp
+constexpr int kWideWarps = MOE_MAX_EXPERTS / kWide;
+static_assert(MOE_MAX_EXPERTS % kWide == 0 && kWideWarps <= 8 && kWideWarps * MOE_MAX_TOPK <= 128, "a block's candidates, four a lane");
+
+// The arguments as a warp's share of the experts has them.
 template <typename T>
+__device__ __forceinline__ GateArgs share_of(const GateArgs& a, int warp) {
+    GateArgs mine = a;
+    mine.logits = static_cast<const uint8_t*>(a.logits) + static_cast<size_t>(warp) * kWide * sizeof(T);
+    mine.E = max(0, min(kWide, a.E - warp * kWide));
+    return mine;
+}
+
+template <typename T, int VEC>
 __global__ void __launch_bounds__(32 * kWideWarps) gate_wide_kernel(const GateArgs a) {
     pdl_wait_then_release();
-    extern __shared__ float smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* z = smem + static_cast<size_t>(warp) * 2 * a.E;  // the token's logits; the ones chosen are taken out
-    float* sums = z + a.E;                                  // the warp's sums of p
-    int32_t* count = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(kWideWarps) * 2 * a.E);  // [E + 1]
-    for (int e = lane; e < a.E; e += 32) sums[e] = 0.f;
+    // Of each warp as in gate_kernel; then [E + 1] counts.
+    extern __shared__ __align__(16) float smem[];
+    // By turns of two: a warp may be a token behind.
+    __shared__ float sums[2][kWideWarps], found[2][kWideWarps * MOE_MAX_TOPK];
+    __shared__ int32_t found_at[2][kWideWarps * MOE_MAX_TOPK];
+    constexpr int V = kWideV, kMine = 32 * lists_of(V);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    int32_t* count = reinterpret_cast<int32_t*>(smem + warps * kMine);
+    float* logits = smem + warp * kMine;
+    uint32_t* lists = reinterpret_cast<uint32_t*>(logits + 32 * V);
+    lists[32 * V + lane] = 0u;
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kWideWarps + warp; g < a.S;
-         g += static_cast<int64_t>(gridDim.x) * kWideWarps) {
-        const T* row = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
-        uint32_t most = 0;
-        for (int e = lane; e < a.E; e += 32) {
-            z[e] = logit(row, e);
-            most = max(most, order_of(z[e]));
-        }
-        most = __reduce_max_sync(kAll, most);
-        if (most <= kNoLogit || (a.mask != nullptr && __ldg(a.mask + g) == 0)) {
+    const GateArgs mine = share_of<T>(a, warp);
+    float acc[V] = {};
+    RowLoad<T, V, VEC> row = {};
+    uint8_t masked = 0;
+    const auto fetch = [&](int64_t t) {
+        if (t >= a.S) return;
+        row.load(mine, t, lane);
+        masked = a.mask != nullptr && __ldg(a.mask + t) == 0;
+    };
+    int64_t g = blockIdx.x;
+    fetch(g);
+    for (int turn = 0; g < a.S; g += gridDim.x, turn ^= 1) {
+        float z[V];
+        row.values(z);
+        const bool out = masked != 0;
+        fetch(g + gridDim.x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) logits[expert_of<VEC>(i, lane)] = z[i];
+        __syncwarp();
+        {
+            const int32_t at = out ? -1 : select<V, VEC, sizeof(T) == 2>(z, a.K, lane, lists);
             if (lane < a.K) {
+                found[turn][warp * a.K + lane] = at >= 0 ? logits[at] : kNegInf;
+                found_at[turn][warp * a.K + lane] = warp * kWide + at;
+            }
+        }
+        __syncthreads();
+        const uint32_t most = __reduce_max_sync(kAll, lane < warps ? order_of(found[turn][lane * a.K]) : 0u);
+        if (most <= kNoLogit) {  // no expert was found
+            if (warp == 0 && lane < a.K) {
                 a.topk_idx[g * a.K + lane] = -1;
                 a.topk_weights[g * a.K + lane] = 0.f;
             }
             continue;
         }
-        const float top = logit_of(most);  // NaN where most stands for one
+        const float top = logit_of(most);
         float sum = 0.f;
-        for (int e = lane; e < a.E; e += 32) sum += exp_of(z[e] - top);
-        const float inv = inverse_of(warp_sum(sum));
-        for (int e = lane; e < a.E; e += 32) sums[e] += exp_of(z[e] - top) * inv;
-        int32_t mine = -1;
-        float p = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = exp_of(z[i] - top);
+            sum += z[i];
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) sums[turn][warp] = sum;
+        __syncthreads();
+        const float inv = inverse_of(warp_sum(lane < warps ? sums[turn][lane] : 0.f));
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
+        if (warp != 0) continue;
+        // The K largest of what the warps found, four a lane, of equal ones the lowest expert.
+        uint32_t key[4];
+        int32_t at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = lane + 32 * j;
+            key[j] = c < warps * a.K ? order_of(found[turn][c]) : 0u;
+            at[j] = c < warps * a.K ? found_at[turn][c] : 0;
+        }
+        int32_t pick = -1;
+        float e = 0.f;
         for (int k = 0; k < a.K; ++k) {
-            uint32_t best = 0;
-            int at = a.E;
-            for (int e = lane; e < a.E; e += 32) {
-                const uint32_t o = order_of(z[e]);
-                if (o > best) {
-                    best = o;
-                    at = e;
+            uint32_t best = key[0];
+            int32_t best_at = at[0];
+#pragma unroll
+            for (int j = 1; j < 4; ++j)
+                if (key[j] > best || (key[j] == best && at[j] < best_at)) {
+                    best = key[j];
+                    best_at = at[j];
                 }
-            }
             const uint32_t all = __reduce_max_sync(kAll, best);
             if (all <= kNoLogit) break;
-            at = __reduce_min_sync(kAll, best == all ? at : a.E);
+            const int32_t next = static_cast<int32_t>(__reduce_min_sync(kAll, best == all ? static_cast<uint32_t>(best_at) : 0x7fffffffu));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (key[j] == all && at[j] == next) key[j] = 0u;
             if (lane == k) {
-                mine = at;
-                p = exp_of(z[at] - top) * inv;
+                pick = next;
+                e = exp_of(logit_of(all) - top);
             }
-            __syncwarp();
-            if (lane == 0) {
-                z[at] = kNegInf;
-                atomicAdd(&count[at], 1);
-            }
-            __syncwarp();
         }
-        const float d = a.normalize ? warp_sum(p) : 1.f;
+        const float share = a.normalize ? __fdividef(a.scale, half_sum(e)) : a.scale * inv;  // of lanes below 16
         if (lane < a.K) {
-            a.topk_idx[g * a.K + lane] = mine;
-            a.topk_weights[g * a.K + lane] = mine < 0 ? 0.f : a.scale * __fdividef(p, d);
+            a.topk_idx[g * a.K + lane] = pick;
+            a.topk_weights[g * a.K + lane] = pick < 0 ? 0.f : e * share + 0.f * inv;  // as in gate_kernel
+            if (pick >= 0) atomicAdd(&count[pick], 1);
         }
         if (lane == 0) atomicAdd(&count[a.E], 1);
-        __syncwarp();
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i) logits[expert_of<VEC>(i, lane)] = acc[i];
     __syncthreads();
-    float* part = a.part_prob + static_cast<size_t>(blockIdx.x) * a.E;
-    int32_t* part_count = a.part_count + static_cast<size_t>(blockIdx.x) * (a.E + 1);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        float s = 0.f;
-        for (int w = 0; w < kWideWarps; ++w) s += smem[(static_cast<size_t>(w) * 2 + 1) * a.E + e];
-        part[e] = s;
-    }
-    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) part_count[e] = count[e];
+    leave_parts(a, count, [&](int e) { return smem[e / kWide * kMine + e % kWide]; });
 }
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(32 * kWideWarps) gate_wide_grad_kernel(const GateArgs a) {
     pdl_wait_then_release();
-    extern __shared__ float smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* c = smem;                                            // [E]
-    float* add = smem + a.E + static_cast<size_t>(warp) * a.E;  // [E]: sum over k with i_k = e of a_k
-    uint8_t* whose = reinterpret_cast<uint8_t*>(smem + static_cast<size_t>(kWideWarps + 1) * a.E) + warp * a.E;
+    __shared__ uint32_t tops[2][kWideWarps];  // by turns of two
+    __shared__ float sums[2][2][kWideWarps];
+    constexpr int V = kWideV;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const float unit = loss_unit(a);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) c[e] = unit * static_cast<float>(__ldg(a.expert_count + e));
-    for (int e = lane; e < a.E; e += 32) add[e] = 0.f;
-    __syncthreads();
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * kWideWarps + warp; g < a.S;
-         g += static_cast<int64_t>(gridDim.x) * kWideWarps) {
-        const T* row = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
-        T* out = reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride);
-        uint32_t most = 0;
-        for (int e = lane; e < a.E; e += 32) most = max(most, order_of(logit(row, e)));
-        most = __reduce_max_sync(kAll, most);
-        if (most <= kNoLogit || (a.mask != nullptr && __ldg(a.mask + g) == 0)) {
-            for (int e = lane; e < a.E; e += 32) put(out + e, 0.f);
-            continue;
+    const GateArgs mine = share_of<T>(a, warp);
+    float c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = expert_of<VEC>(i, lane);
+        c[i] = e < mine.E ? unit * static_cast<float>(__ldg(a.expert_count + warp * kWide + e)) : 0.f;
+    }
+    RowLoad<T, V, VEC> row = {};
+    uint8_t masked = 0;
+    float chosen = 0.f, dw = 0.f;
+    const auto ids = [&](int64_t t) {
+        const int32_t i = t < a.S && lane < a.K ? __ldg(a.topk_idx + t * a.K + lane) : -1;
+        return i < a.E ? i : -1;
+    };
+    const auto fetch = [&](int64_t t, int32_t i) {
+        if (t >= a.S) return;
+        row.load(mine, t, lane);
+        masked = a.mask != nullptr && __ldg(a.mask + t) == 0;
+        chosen = i >= 0 ? logit(reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + t * a.row_stride), i) : 0.f;
+        dw = i >= 0 && a.dweights ? __ldg(a.dweights + t * a.K + lane) : 0.f;
+    };
+    int64_t g = blockIdx.x;
+    int32_t idx = ids(g), idx_next = ids(g + gridDim.x);
+    fetch(g, idx);
+    for (int turn = 0; g < a.S; g += gridDim.x, turn ^= 1) {
+        float z[V];
+        row.values(z);
+        const bool out = masked != 0;
+        const int32_t i_now = idx;
+        const float dw_now = dw, chosen_now = chosen;
+        idx = idx_next;
+        idx_next = ids(g + 2 * static_cast<int64_t>(gridDim.x));
+        fetch(g + gridDim.x, idx);
+        T* to = reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride) + warp * kWide;
+        uint32_t most = row_top(z);
+        if (lane == 0) tops[turn][warp] = most;
+        __syncthreads();
+        most = __reduce_max_sync(kAll, lane < warps ? tops[turn][lane] : 0u);
+        const bool routed = !out && most > kNoLogit;
+        float t = 0.f, inv = 0.f;
+        Slots s{-1, 0.f, 0.f, 0.f};
+        if (routed) {
+            const float top = logit_of(most);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                z[i] = exp_of(z[i] - top);
+                sum += z[i];
+                t = fmaf(z[i], c[i], t);
+            }
+            sum = warp_sum(sum);
+            t = warp_sum(t);
+            if (lane == 0) {
+                sums[turn][0][warp] = sum;
+                sums[turn][1][warp] = t;
+            }
+            __syncthreads();
+            inv = inverse_of(warp_sum(lane < warps ? sums[turn][0][lane] : 0.f));
+            t = warp_sum(lane < warps ? sums[turn][1][lane] : 0.f) * inv;
+            s = slots_of(a, lane, i_now, dw_now, i_now >= 0 ? exp_of(chosen_now - top) : 0.f, inv, nullptr);
+            t += s.t;
         }
-        const float top = logit_of(most);
-        float sum = 0.f, t = 0.f;
-        for (int e = lane; e < a.E; e += 32) {
-            const float v = exp_of(logit(row, e) - top);
-            sum += v;
-            t += v * c[e];
-        }
-        const float inv = inverse_of(warp_sum(sum));
-        t = warp_sum(t) * inv;
-        int32_t i = -1;
-        float dw = 0.f;
-        if (lane < a.K) {
-            i = __ldg(a.topk_idx + g * a.K + lane);
-            if (i >= a.E) i = -1;
-            if (i >= 0 && a.dweights) dw = __ldg(a.dweights + g * a.K + lane);
-        }
-        const Slots s = slots_of(a, lane, i, dw, i >= 0 ? exp_of(logit(row, i) - top) : 0.f, inv, whose);
-        t += s.t;
-        if (s.i >= 0) add[s.i] = s.a;  // slots of the same expert have the same sum
-        __syncwarp();
-        for (int e = lane; e < a.E; e += 32) put(out + e, exp_of(logit(row, e) - top) * inv * (c[e] + add[e] - t));
-        __syncwarp();
-        if (s.i >= 0) add[s.i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = routed ? z[i] * inv * (c[i] - t) : 0.f;
+        put_row<V, VEC>(to, mine.E, lane, z);
+        __syncwarp();  // the warp's chosen experts' over what was stored for them
+        const int at = s.i - warp * kWide;
+        if (s.i >= 0 && at >= 0 && at < kWide) put(to + at, s.p * (unit * static_cast<float>(__ldg(a.expert_count + s.i)) + s.a - t));
         __syncwarp();
     }
 }
@@ -1001,6 +1111,7 @@ Kernel kernel_at() {
     else
         return gate_kernel<T, V, VEC>;
 }
+constexpr int kMostInRegisters = 1024;  // of a warp
 int logits_of_a_lane(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 int lanes_of_a_token(int E) { return E > kMostInTeams ? 32 : E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8; }
 
@@ -1016,6 +1127,13 @@ Kernel team_at(bool by) {
 // by: rows are loaded 16 bytes at a time.
 template <bool GRAD, typename T>
 Kernel kernel_for(int E, bool by) {
+    if (E > kMostInRegisters) {
+        constexpr int kVec = 16 / sizeof(T);
+        if constexpr (GRAD)
+            return by ? gate_wide_grad_kernel<T, kVec> : gate_wide_grad_kernel<T, 1>;
+        else
+            return by ? gate_wide_kernel<T, kVec> : gate_wide_kernel<T, 1>;
+    }
     switch (lanes_of_a_token(E)) {
         case 1: return team_at<GRAD, T, 1>(by);
         case 2: return team_at<GRAD, T, 2>(by);
@@ -1032,10 +1150,18 @@ Kernel kernel_for(int E, bool by) {
     }
 }
 
-constexpr int kMostInRegisters = 1024;
+// A token's lanes, and a block's warps.
+struct Geometry {
+    int lanes, warps;
+};
+Geometry geometry(int E) {
+    if (E > kMostInRegisters) return {kWide, static_cast<int>(ceil_div(E, kWide))};
+    return {lanes_of_a_token(E), kGateWarps};
+}
 
-// Blocks of `tokens` at a time: what is resident, or needed, at most kGateParts.
-cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int tokens, int64_t S, unsigned* blocks) {
+// Blocks: what is resident, or needed, at most kGateParts.
+cudaError_t blocks_for(Kernel kernel, size_t smem, const Geometry& geo, int64_t S, unsigned* blocks) {
+    const int warps = geo.warps, tokens = geo.lanes > 32 ? 1 : warps * 32 / geo.lanes;
     int per_sm = 0;
     const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, 32 * warps, &per_sm);
     int64_t n = static_cast<int64_t>(device_sm_count()) * (per_sm > 0 ? per_sm : 1);
@@ -1048,36 +1174,29 @@ cudaError_t blocks_for(Kernel kernel, size_t smem, int warps, int tokens, int64_
 }  // namespace
 
 cudaError_t launch_gate(const GateArgs& a, cudaStream_t stream) {
-    const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride);
-    const int warps = wide ? kWideWarps : kGateWarps;
-    const int lanes = lanes_of_a_token(a.E), entries = wide ? 2 * a.E : 32 * lists_of(logits_of_a_lane(a.E));
-    const size_t smem = lanes < 32 ? 0 : (static_cast<size_t>(warps) * entries + a.E + 1) * 4;
-    const Kernel kernel = wide ? (a.bf16 ? gate_wide_kernel<__nv_bfloat16> : gate_wide_kernel<float>)
-                               : (a.bf16 ? kernel_for<false, __nv_bfloat16>(a.E, by) : kernel_for<false, float>(a.E, by));
+    const Geometry geo = geometry(a.E);
+    const bool by = by_16(a, a.row_stride);
+    const size_t smem = geo.lanes < 32 ? 0 : (static_cast<size_t>(geo.warps) * 32 * lists_of(geo.lanes > 32 ? kWideV : logits_of_a_lane(a.E)) + a.E + 1) * 4;
+    const Kernel kernel = a.bf16 ? kernel_for<false, __nv_bfloat16>(a.E, by) : kernel_for<false, float>(a.E, by);
     unsigned blocks = 0;
-    cudaError_t e = blocks_for(kernel, smem, warps, warps * 32 / lanes, a.S, &blocks);
+    cudaError_t e = blocks_for(kernel, smem, geo, a.S, &blocks);
     if (e != cudaSuccess) return e;
-    const bool one = !wide && a.S <= kOneBlock;
-    if (one) blocks = 1;
-    e = launch_pdl(kernel, blocks, 32u * warps, smem, stream, a);
-    if (e != cudaSuccess || one || (!wide && blocks == 1)) return e;
+    if (geo.lanes <= 32 && a.S <= kOneBlock) blocks = 1;
+    e = launch_pdl(kernel, blocks, 32u * geo.warps, smem, stream, a);
+    if (e != cudaSuccess || blocks == 1) return e;
     return launch_pdl_cluster(gate_join_kernel, kJoinCtas, 1024u, 0, kJoinCtas, stream, a, static_cast<int>(blocks));
 }
 
 cudaError_t launch_gate_grad(const GateArgs& a, cudaStream_t stream) {
     if (a.S == 0) return cudaSuccess;
-    const bool wide = a.E > kMostInRegisters, by = by_16(a, a.row_stride) && by_16(a, a.dlogits_stride);
-    const int warps = wide ? kWideWarps : kGateWarps;
-    const int lanes = lanes_of_a_token(a.E);
-    const size_t smem = wide         ? static_cast<size_t>(warps + 1) * a.E * 4 + static_cast<size_t>(warps) * a.E
-                        : lanes < 32 ? static_cast<size_t>(warps) * (64 * kTeamV + 4 * (32 / lanes) * a.K) * 4
-                                     : 0;
-    const Kernel kernel = wide ? (a.bf16 ? gate_wide_grad_kernel<__nv_bfloat16> : gate_wide_grad_kernel<float>)
-                               : (a.bf16 ? kernel_for<true, __nv_bfloat16>(a.E, by) : kernel_for<true, float>(a.E, by));
+    const Geometry geo = geometry(a.E);
+    const bool by = by_16(a, a.row_stride) && by_16(a, a.dlogits_stride);
+    const size_t smem = geo.lanes < 32 ? static_cast<size_t>(geo.warps) * (64 * kTeamV + 4 * (32 / geo.lanes) * a.K) * 4 : 0;
+    const Kernel kernel = a.bf16 ? kernel_for<true, __nv_bfloat16>(a.E, by) : kernel_for<true, float>(a.E, by);
     unsigned blocks = 0;
-    const cudaError_t e = blocks_for(kernel, smem, warps, warps * 32 / lanes, a.S, &blocks);
+    const cudaError_t e = blocks_for(kernel, smem, geo, a.S, &blocks);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, blocks, 32u * warps, smem, stream, a);
+    return launch_pdl(kernel, blocks, 32u * geo.warps, smem, stream, a);
 }
 
 }  // namespace moe
