@@ -308,3 +308,23 @@ def test_past_32_bits_of_offset(H):
     moe.moe_rms_norm_grad(x, x, w, EPS, dh)
     moe.moe_rms_norm_grad(tail, tail, w, EPS, g)
     assert torch.equal(dh[-128:], g)
+
+
+@pytest.mark.parametrize("power", [-100, -84, -83, -82, -40, 0, 60, 120])
+def test_int8_rows_of_every_bf16_quotient(power):
+    """Each largest value of a power of two with each value down to 2^-9 of it: quotients at and beside ties."""
+    import torch
+
+    mantissas = np.arange(128, 256, dtype=np.float32)
+    below = np.concatenate([mantissas * np.float32(2.0) ** -k for k in range(10)])
+    rows = []
+    for m in mantissas:
+        v = np.where(below <= m, below, np.float32(0))
+        rows.append(np.concatenate([[m], v, -v, np.zeros(15)]).astype(np.float32))
+    x = (np.stack(rows) * np.float32(2.0) ** (power - 7)).astype(np.float32)
+    xd = torch.from_numpy(x).to(torch.bfloat16)
+    assert (xd.float().numpy() == x).all()
+    scale = np.abs(x).max(1) / np.float32(127)
+    want = np.rint(x / scale[:, None])
+    op = moe.Int8Rows(*x.shape).pack(xd.cuda())
+    assert np.array_equal(op.q.cpu().numpy(), want.astype(np.int8)) and np.array_equal(op.scale.cpu().numpy(), scale)
