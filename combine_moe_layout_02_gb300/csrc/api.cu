@@ -741,7 +741,7 @@ moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logit
     if (st != MOE_OK) return st;
     const int64_t slots = a.S * a.K, elt = a.bf16 ? 2 : 4;
     if (!ok_ptr(topk_idx, slots, 16) || !ok_ptr(expert_count, 1, 16) || !ok_opt(dweights, 16) || !ok_opt(dloss, 4) ||
-        !ok_ptr(dlogits, a.S, 16) || !ok_stride(dlogits_stride, a.E * elt, elt))
+        !ok_ptr(dlogits, a.S, 16) || !ok_stride(dlogits_stride, a.E * elt, elt) || (a.S > 0 && dlogits == logits))
         return MOE_ERR_INVALID_ARG;
     a.scale = scale;
     a.balance = balance;

@@ -64,9 +64,9 @@ static __device__ __noinline__ uint2 int8_divided8(float v0, float v1, float v2,
     return make_uint2(w[0], w[1]);
 }
 
-// rint(v / scale) of 8 values, the quotient rounded as a division rounds it: v * inv is within an ulp
-// of it, what it leaves of v is exact, and adding that times inv rounds right where inv is the rounded reciprocal
-// (P. Markstein, IBM Journal of Research and Development 34, 1990). What is left of v that matters, near a tie
+// rint(v / scale) of 8 values, the quotient rounded as a division rounds it: v * inv is within two ulps
+// of it, and adding what that leaves of v times inv rounds right where inv is the rounded reciprocal
+// (P. Markstein, IBM Journal of Research and Development 34, 1990; every quotient of bf16 values is tested). What is left of v that matters, near a tie
 // and so |v| >= scale / 4, is above 2^-26 scale: a scale from 2^-90 on keeps it a normal number. bf16 rows
 // reach a tie often (127 v / max is a quotient of small whole numbers): 32768 x 7168 packed in 170 us when
 // only products near one were divided, in 123 so. Codes are 0 under a scale of 0 or NaN.

@@ -550,12 +550,17 @@ class Gate:
         self.loss = torch.empty((1,), dtype=torch.float32, device=device)
         self.scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
         self._shape, self._nbytes, self._rows = ctypes.byref(shape), nbytes, (S, E)
+        self._device = self.scratch.get_device() if self.scratch.is_cuda else -1
 
     def _logits(self, t, name):
         half = t.dtype is _t().bf16
         if not half and t.dtype is not _t().f32:
             raise ValueError("expected %s in torch.float32 or torch.bfloat16, got %s" % (name, t.dtype))
-        return (int(half), *_rows_of(t, self._rows, t.dtype, 2 if half else 4, name, _t().device()))
+        dev = _t().device()
+        rows = _rows_of(t, self._rows, t.dtype, 2 if half else 4, name, dev)
+        if self._device != dev:
+            raise ValueError("the gate's buffers are on %s, the current device is cuda:%d" % (self.scratch.device, dev))
+        return int(half), *rows
 
     def _mask(self, mask):
         return None if mask is None else _flat(mask, self.shape.S, _t().flag if mask.dtype is _t().flag else _t().u8, "mask")

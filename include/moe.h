@@ -533,7 +533,8 @@ moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint1
  *   logits, mask, normalize, scale, balance   as in the forward call
  *   topk_idx, expert_count                    its results
  *   dweights     float [S,K] or NULL (0); dloss float [1] or NULL (0)
- *   dlogits      rows of `type`, dlogits_stride bytes apart; may not overlap logits
+ *   dlogits      rows of `type`, dlogits_stride bytes apart; may not overlap logits (the
+ *                same address is refused)
  */
 #define MOE_F32 0
 #define MOE_BF16 1

@@ -315,3 +315,20 @@ def test_same_bits_again_in_a_graph_and_on_another_stream():
 ])
 def test_tokens_that_share_a_warp(S, E, K, normalize, banned, masked, dtype):
     test_gate_and_gradient(S, E, K, dtype, normalize, 1.5, 0.05, banned, masked)
+
+
+def test_buffers_elsewhere_are_refused():
+    import torch
+
+    op = moe.Gate(moe.make_shape(1, 8, 4, 2, 64), "cpu")
+    z = torch.zeros((4, 8), device="cuda")
+    with pytest.raises(ValueError, match="the gate's buffers are on cpu"):
+        op.forward(z)
+    with pytest.raises(ValueError, match="the gate's buffers are on cpu"):
+        op.backward(z)
+    op = _gate(4, 8, 2)
+    with pytest.raises(ValueError):
+        op.forward(torch.zeros((4, 8)))
+    op.forward(z)
+    with pytest.raises(moe.MoeError):
+        op.backward(z, dlogits=z)

@@ -37,7 +37,7 @@ def test_gate_refusals(lib):
 def test_gate_gradient_refusals(lib):
     s = moe.make_shape(1, 16, 64, 2, 64)
 
-    def call(shape=s, kind=0, z=A, stride=64, normalize=1, idx=A, c=A, dw=A, dl=A, dz=A, dstride=64):
+    def call(shape=s, kind=0, z=A, stride=64, normalize=1, idx=A, c=A, dw=A, dl=A, dz=A + 4096, dstride=64):
         return lib.moe_gate_grad(shape, kind, z, stride, None, normalize, 1.0, 0.0, idx, c, dw, dl, dz, dstride, None)
 
     for name in ("z", "idx", "c", "dz"):
@@ -45,6 +45,7 @@ def test_gate_gradient_refusals(lib):
     assert call(dw=A + 4) == BAD and call(dl=A + 1) == BAD
     assert call(kind=3) == BAD and call(normalize=-1) == BAD and call(stride=60) == BAD and call(dstride=60) == BAD
     assert call(dstride=65) == BAD
+    assert call(dz=A) == BAD  # over the logits
     empty = moe.make_shape(1, 16, 0, 2, 64)
     assert call(shape=empty, z=None, idx=None, dz=None) == moe.MOE_OK
 
