@@ -182,10 +182,8 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&h)[32
 // A pair's units, first, first + step, .. of the launch's; the weight rows are the
 // inner index. A role steps from unit to unit without a division and holds the next
 // one's plan words while it works on the current one. A plan's tile of more than
-// ROWS rows is one unit of several tiles. (Units of their own for each would spread hot
-// experts better, 8008 rows over 249 experts, one with 1001, 2048 -> 7168 701 -> 670 us, but looking
-// them up cost where rows are few, 2 rows each 7168 -> 4096 1098 -> 1135, and many, 1024 each 8.28 -> 8.38 ms. In
-// ranges of even length for each pair, 1098 -> 1280: pairs then read far apart.)
+// ROWS rows is one unit of several tiles. (In ranges of even length for each pair, 2 rows each 7168 -> 4096 1098 -> 1280 us:
+// pairs then read far apart.)
 template <int ROWS>
 struct Units {
     uint32_t per, part, in, step_part, step_in, left;
@@ -193,9 +191,9 @@ struct Units {
     int32_t skip;  // rows of the plan's tile that other units have
     Unit rest;     // what the current unit has left
 
-    __device__ __forceinline__ Units(const Args& a, uint32_t parts, uint32_t mtiles, uint32_t first, uint32_t step)
+    __device__ __forceinline__ Units(const Args& a, uint32_t tiles, uint32_t mtiles, uint32_t first, uint32_t step)
         : per(mtiles), tile(make_int4(0, 0, 0, 0)), skip(0), rest{0, 0, 0, 0} {
-        const uint32_t units = parts * mtiles;
+        const uint32_t units = (tiles << (a.p.plan ? a.shift : 0)) * mtiles;
         left = first < units ? (units - first - 1) / step + 1 : 0;
         part = first / per;
         in = first - part * per;
@@ -214,7 +212,7 @@ struct Units {
             tile = make_int4(0, static_cast<int32_t>(first), static_cast<int32_t>(rows < size ? rows : size), 0);
         }
     }
-    __device__ __forceinline__ bool more() const { return left > 0 || rest.n > 0; }
+    __device__ __forceinline__ bool more(const Args&) const { return left > 0 || rest.n > 0; }
     // The current tile, the same in every lane, or none (n = 0) where the plan's
     // tile is no tile of these rows; then on to the next.
     __device__ __forceinline__ Unit take(const Args& a) {
@@ -245,6 +243,90 @@ struct Units {
         }
         return o;
     }
+};
+
+// The same of tiles of up to 128 rows, which a plan's average asks for where some experts may have far more: both halves of a
+// plan's tile are units, neighbours in the order, so that the pairs, which get units by turns, get as much to do. A warp holds
+// 32 of the plan's tiles, a lane each. 8008 rows over 249 experts, one with 1001, 2048 -> 7168 701 -> 670 us, 31 rows
+// each 643 -> 621. (Looking units up costs more than it gives where rows are few, 2 rows each 7168 -> 4096 in tiles of
+// 64 1098 -> 1135, and where a tile is a unit anyway, 1024 rows each 8.28 -> 8.38 ms.)
+struct HalfUnits {
+    static constexpr int kSize = kPlanTileRows / 2;
+    uint32_t per, part, in, step_part, step_in;
+    uint32_t tiles;         // the plan's, or the rows'
+    uint32_t base, before;  // first tile that is held, halves before it
+    uint32_t upto, held;    // halves of the tiles that are held up to the lane's, and of all
+    int4 tile;              // the lane's
+
+    __device__ __forceinline__ HalfUnits(const Args& a, uint32_t all_tiles, uint32_t mtiles, uint32_t first, uint32_t step)
+        : per(mtiles), tiles(all_tiles), base(0), before(0), upto(0), held(0), tile(make_int4(0, 0, 0, 0)) {
+        part = first / per;
+        in = first - part * per;
+        step_part = step / per;
+        step_in = step - step_part * per;
+        if (a.p.plan) hold(a);
+    }
+    // (what is no count of rows is one, and skipped)
+    __device__ __forceinline__ static uint32_t halves_of(int32_t n) { return n > kSize && n <= kPlanTileRows ? 2 : 1; }
+    __device__ __forceinline__ void hold(const Args& a) {
+        const uint32_t lane = threadIdx.x & 31, i = base + lane;
+        if (i < tiles) tile = __ldg(reinterpret_cast<const int4*>(a.p.plan + plan_tiles_at(a.p.E)) + i);
+        upto = i < tiles ? halves_of(tile.z) : 0;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d *= 2) {
+            const uint32_t other = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += other;
+        }
+        held = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    __device__ __forceinline__ bool more(const Args& a) {
+        if (!a.p.plan) return part < tiles;
+        while (part - before >= held) {
+            if (base >= tiles) return false;
+            base += 32;
+            before += held;
+            hold(a);
+        }
+        return true;
+    }
+    __device__ __forceinline__ Unit take(const Args& a) {
+        const int32_t m0 = static_cast<int32_t>(in) * kMTile;
+        Unit o;
+        if (a.p.plan) {
+            const int at = __ffs(__ballot_sync(0xffffffffu, part - before < upto)) - 1;
+            o = Unit{uniform(__shfl_sync(0xffffffffu, tile.x, at)), uniform(__shfl_sync(0xffffffffu, tile.y, at)),
+                     uniform(__shfl_sync(0xffffffffu, tile.z, at)), m0};
+            const uint32_t end = uniform(__shfl_sync(0xffffffffu, upto, at));
+            if (o.e < 0 || o.e >= a.p.E || o.row < 0 || o.n < 0 || o.n > kPlanTileRows ||
+                o.row + static_cast<int64_t>(o.n) > a.p.rows) {
+                raise_error(a.err, MOE_ERR_CAPACITY);
+                o.n = 0;
+            } else {
+                const int32_t skip = kSize * static_cast<int32_t>(halves_of(o.n) - (end - (part - before)));
+                o.row += skip;
+                o.n = min(o.n - skip, kSize);
+            }
+        } else {
+            const int64_t first = static_cast<int64_t>(part) * kSize, rows = a.p.rows - first;
+            o = Unit{0, static_cast<int32_t>(first), static_cast<int32_t>(rows < kSize ? rows : kSize), m0};
+        }
+        part += step_part;
+        in += step_in;
+        if (in >= per) {
+            in -= per;
+            ++part;
+        }
+        return o;
+    }
+};
+
+template <int ROWS>
+struct ListOf {
+    using Type = Units<ROWS>;
+};
+template <>
+struct ListOf<128> {
+    using Type = HalfUnits;
 };
 
 template <bool GATED, int ROWS>
@@ -297,12 +379,10 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
     const uint32_t tmem = bars->tmem;
     pdl_wait_then_release();
 
-    int32_t tiles = a.p.tile_cap;
-    if (a.p.plan) {
-        const int32_t planned = uniform(__ldg(a.p.plan));
-        tiles = planned < 0 ? 0 : (planned > tiles ? tiles : planned);
-    }
-    const uint32_t parts = static_cast<uint32_t>(tiles) << (a.p.plan ? a.shift : 0), mtiles = (a.p.N + kMTile - 1) / kMTile;
+    using List = typename ListOf<ROWS>::Type;
+    uint32_t tiles = a.p.tile_cap;
+    if (a.p.plan) tiles = max(0, min(uniform(__ldg(a.p.plan)), a.p.tile_cap));
+    const uint32_t mtiles = (a.p.N + kMTile - 1) / kMTile;
     const uint32_t step = gridDim.x / (2 * a.split), first = blockIdx.x / (2 * a.split);
     const int nstages = static_cast<int>(ceil_div(a.p.K, kStageK));
     const int k_first = nstages * kpart / a.split, k_end = nstages * (kpart + 1) / a.split;  // the pair's stages
@@ -313,8 +393,8 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         uint32_t s = 0, phase = 0;  // stage, and the parity its last use completed with
         int64_t issued = 0;
         bool ok = warp != a.quit_warp;
-        Units<ROWS> list(a, parts, mtiles, first, step);
-        while (ok && list.more()) {
+        List list(a, tiles, mtiles, first, step);
+        while (ok && list.more(a)) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n);
@@ -354,8 +434,8 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         uint32_t i = 0, last_n = 0;  // i: tiles so far
         uint32_t turn = 0, parity = 0;  // a bit a group: of its place's next use
         bool ok = warp != a.quit_warp;
-        Units<ROWS> list(a, parts, mtiles, first, step);
-        while (ok && list.more()) {
+        List list(a, tiles, mtiles, first, step);
+        while (ok && list.more(a)) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t n = mma_n(t.n), place = i & 1;
@@ -414,8 +494,8 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         const uint32_t ready = cluster_map(bars->ready + group, lead);
         uint32_t s = 0, phase = 0, uses = 0, turn = 0;
         bool ok = warp != a.quit_warp;
-        Units<ROWS> list(a, parts, mtiles, first, step);
-        while (ok && list.more()) {
+        List list(a, tiles, mtiles, first, step);
+        while (ok && list.more(a)) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const int rows = static_cast<int>(mma_n(t.n) / 2);
@@ -485,8 +565,8 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
         const uint32_t to = stage + (lane & 7) * kOutStride + (lane >> 3) * 16;
         const uint32_t to_gated = stage + ((lane & 7) + 8 * (lane >> 4)) * kOutStride + ((lane >> 3) & 1) * 16;
         uint32_t i = 0;
-        Units<ROWS> list(a, parts, mtiles, first, step);
-        while (list.more()) {
+        List list(a, tiles, mtiles, first, step);
+        while (list.more(a)) {
             const Unit t = list.take(a);
             if (t.n == 0) continue;
             const uint32_t place = i & 1;
