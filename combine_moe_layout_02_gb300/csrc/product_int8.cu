@@ -825,10 +825,12 @@ cudaError_t launch_cut(Args a, cudaStream_t stream) {
     if (!cut<GATED>(a.p, &plan)) return cudaErrorInvalidConfiguration;
     if (a.p.plan) {
         // By the rows that the routing gives an expert on average: more stages where they are few, against experts of more
-        // rows than the kernel takes at a time, whose weights are read again. 256 experts 7168 -> 4096 with 2 / 64 / 128
-        // rows each: 1085 / 1133 / 2239 us with 64 at a time, 1151 / 1186 / 1345 with 128, 1253 / 1323 / 1430 with 256.
+        // rows than the kernel takes at a time, whose weights are read again. 256 experts 7168 -> 4096 with 2 / 31 / 64 / 96 /
+        // 140 rows each: 1098 / 1115 / 1133 / 2230 / - us with 64 at a time, 1151 / 1174 / 1215 / 1295 / 2463 with 128,
+        // 1253 / - / 1323 / 1384 / 1575 with 256; 8008 rows, one expert with 1001: 1395 with 64, 1265 with 128; 24576
+        // rows, one with 1209: 1568 with 128, 1534 with 256.
         const int64_t each = a.p.plan_rows / a.p.E;
-        if (plan.split == 1 && plan.shift == 0) plan.rows = each <= 24 ? 64 : each <= 64 ? 128 : 256;
+        if (plan.split == 1 && plan.shift == 0) plan.rows = each <= 24 ? 64 : each <= 96 ? 128 : 256;
     } else {
         a.p.tile_cap = static_cast<int32_t>(ceil_div(a.p.rows, kPlanTileRows >> plan.shift));
     }
