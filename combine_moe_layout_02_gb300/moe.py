@@ -454,6 +454,7 @@ class _Types:
         import torch
 
         self.bf16, self.f32, self.i8, self.u8, self.flag = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.bool
+        self.empty_like = torch.empty_like  # 1.3 us of host time, new_empty 3
         # int8 codes (dispatch's slots are bytes); scales; bf16 rows or their bit patterns
         self.codes, self.scales, self.rows = (torch.int8, torch.uint8), (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
         get = getattr(torch._C, "_cuda_getDevice", None)
@@ -582,7 +583,7 @@ class Gate:
         args = self._logits(logits, "logits")
         if dlogits is None:
             if stream is None:
-                dlogits = logits.new_empty(self._rows)
+                dlogits = _t().empty_like(logits) if logits.is_contiguous() else logits.new_empty(self._rows)
             else:
                 with _made_on(stream, logits.device):
                     dlogits = logits.new_empty(self._rows)
