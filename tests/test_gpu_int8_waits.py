@@ -213,3 +213,51 @@ def test_plans_of_few_experts(counts, N, K, gated):
 def test_dense_calls_of_which_pairs_share_K(rows, N, K):
     test_dense_calls_of_every_cut(rows, N, K, 0)
     test_dense_calls_of_every_cut(rows, N, K, 1)
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("counts", [[31] * 60 + [130, 256, 257, 700, 0, 1, 128, 129], [700, 513] + [28] * 31 + [128] * 3, [90] * 40,
+                                    [0] * 33 + [1500] + [20] * 14])
+def test_some_experts_have_far_more_rows_than_the_average(counts, gated):
+    """Plans whose average asks for tiles of 128 rows: longer ones are two units each, and a warp looks up 32 at a time."""
+    import torch
+
+    counts = np.array(counts)
+    E, N, K = len(counts), 288, 400
+    plan, first = _plan(E, counts)
+    rows = int(first[-1])
+    wq, ws, xq, xs = _operands(E, N, K, rows, E)
+    y = torch.full((rows, N // 2 if gated else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = _err()
+    _call(E, N, K, gated, _up(wq, ws, xq, xs), rows, plan, y, err)
+    got = y.double().cpu().numpy()
+    for e in range(E):
+        at = slice(first[e], first[e] + counts[e])
+        if counts[e]:
+            _check(got[at], *ref.product(wq[e], ws[e], xq[at], xs[at], gated), where=e)
+        assert (got[first[e] + counts[e]:first[e + 1]] == 7).all()
+    assert not err.any()
+
+
+@pytest.mark.parametrize("quit_warp", [0, 1, 4, 7, 9, 11])
+def test_every_role_ends_in_tiles_of_128_rows(quit_warp):
+    import torch
+
+    counts = np.array([31] * 60 + [130, 256, 257, 700, 0, 1, 128, 129])
+    E, N, K = len(counts), 1056, 1040
+    plan, first = _plan(E, counts)
+    rows = int(first[-1])
+    operands = _up(*_operands(E, N, K, rows, 1))
+    err = _err()
+    y = [torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    _call(E, N, K, 0, operands, rows, plan, y[0], err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    moe.moe_test_product_wait(SHORT, quit_warp)
+    _call(E, N, K, 0, operands, rows, plan, y[1], err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == moe.MOE_ERR_DEVICE_TIMEOUT
+    err.zero_()
+    _call(E, N, K, 0, operands, rows, plan, y[1], err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0 and torch.equal(y[0], y[1])
