@@ -15,7 +15,7 @@
 // weights' straight into tensor memory, from where the instruction takes its A side,
 // the rows' into shared memory, swizzled as its B side is --, two groups by turns at
 // a stage, one at each half of its K; warp 1 of the leading CTA issues the products
-// of K = 16; the warps from 4 on take the sums out, times the scales. A group has places
+// of K = 16; the warps from 4 on take the sums out, times the scales. A group has a place
 // of its own for what it makes, so they work while others' places are multiplied.
 //
 // What bounds it. Many rows: the tensor pipe and power (262144 rows 7168 -> 4096 gated:
@@ -32,8 +32,8 @@
 //
 // Tensor memory: sums in two places, columns 0 and 128 on, which share 128 columns in
 // tiles of more than 128 rows (read first and given back early), and the f16 weights,
-// 32 columns to a place. Dense calls short of tiles cut them smaller, or let two pairs
-// share a tile's K and join through each other's shared memory (the rule is at cut()).
+// 32 columns to a place. Dense calls short of tiles cut them smaller, or let up to four
+// pairs share a tile's K and join through each other's shared memory (the rule is at cut()).
 #include <atomic>
 
 #include "fp4.cuh"
