@@ -515,9 +515,13 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                 }
                 const bool skip = half == 1 && short_end && k == nstages - 1;
                 if (!skip) {
-                    // All codes first, and the stage goes back before the group's place is waited for: a lane's
-                    // weight row, and of every 32 rows 16 codes of one (the lanes of a warp are 8 rows x 4, so
-                    // that neither side meets in a bank).
+                    if (uses > 0 && !wait_here(bars, &bars->used[group], (uses - 1) & 1, a)) {
+                        ok = false;
+                        break;
+                    }
+                    ++uses;
+                    // All codes first: a lane's weight row, and of every 32 rows 16 codes of one (the
+                    // lanes of a warp are 8 rows x 4, so that neither side meets in a bank).
                     const uint32_t base = smem_addr(smem + at * kStageBytes);
                     uint4 wv[4], xv[ROWS / 64];
 #pragma unroll
@@ -525,13 +529,6 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
 #pragma unroll
                     for (int j = 0; j < ROWS / 64; ++j)
                         if (32 * j + 8 * w < rows) xv[j] = read_shared(base + kWBytes + (xrow + 32 * j) * 128 + xfrom);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->empty[at]);
-                    if (uses > 0 && !wait_here(bars, &bars->used[group], (uses - 1) & 1, a)) {
-                        ok = false;
-                        break;
-                    }
-                    ++uses;
                     uint32_t h[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) halves16(wv[c], h + 8 * c);
@@ -546,8 +543,12 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
                         write_shared(dst + xto, x[0], x[1], x[2], x[3]);
                         write_shared(dst + (xto ^ 16), x[4], x[5], x[6], x[7]);
                     }
-                    // Seen by the tensor cores once the arrival is: every lane's f16 rows and tensor memory.
+                    // Every lane's codes have been used and its f16 rows written, by the generic proxy: before the loader
+                    // (the async proxy) writes the stage again, and before the tensor cores read the rows. A stage that
+                    // went back once its codes were read, without the fence, was refilled under reads still in flight.
                     fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->empty[at]);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
