@@ -58,10 +58,14 @@ constexpr int kMostStages = 10;
 constexpr int kGroups = 4;     // of four converting warps: two by turns at a stage, one at each half of its K
 constexpr int kACol = 512 - 32 * kGroups;  // the f16 weights: a place of 32 columns for each group
 
-// Up to ROWS rows to a tile: fewer of them in shared memory make room for more stages.
+// Up to ROWS rows to a tile: fewer of them in shared memory make room for more stages. Their number is even: groups take
+// stages by turns, so each place of the ring is always the same two groups', which see every use of it. (Of seven, a
+// group saw every second use, of the same parity, and one that skips the short end of K, waiting for no product, could
+// take the use in between for its own.)
 template <int ROWS>
 struct Cut {
-    static constexpr int kStages = ROWS <= 64 ? 10 : ROWS <= 128 ? 7 : 4;
+    static constexpr int kStages = ROWS <= 64 ? 10 : ROWS <= 128 ? 6 : 4;
+    static_assert(kStages % 2 == 0, "a place of the ring is the same groups' at every use");
     static constexpr int kEpiWarps = ROWS <= 128 ? 4 : 8;            // that take sums out: one or two for each quarter of the lanes
     static constexpr int kThreads = 128 + 32 * kEpiWarps + 128 * kGroups;
     static constexpr uint32_t kStageBytes = kWBytes + ROWS / 64 * kXBox;

@@ -100,3 +100,10 @@ def _counts(E, least, most, seed):
 ])
 def test_the_whole_result(E, N, K, least, most, gated, slots, repeats):
     _check_all(E, N, K, _counts(E, least, most, E + N), gated, slots, repeats, seed=K)
+
+
+@pytest.mark.parametrize("K", [16, 64, 160, 192, 416, 448])
+@pytest.mark.parametrize("gated", [0, 1])
+def test_short_ends_of_k_in_tiles_of_128_rows(K, gated):
+    """K of one, two and four stages whose last has one half: a converting group waits for no product there."""
+    _check_all(256, 1024, K, _counts(256, 25, 110, K), gated, bool(gated), 30, seed=K)
