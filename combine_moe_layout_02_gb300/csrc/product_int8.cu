@@ -22,13 +22,12 @@
 // 8.0-8.4 ms, 1.84-1.92 PFLOP/s; bursts of 8192 rows 2.0; back to back for seconds 9.6).
 // Weights through tensor memory save shared memory's rate: 64 of K are 16 KB of codes in,
 // 16 out, 16 of f16 rows in and 16 out, 64 KB in the 512 cycles of their products, at 128
-// bytes a cycle. Few rows: the weights' bytes (2 rows to each of 256 experts: 1.07 ms,
-// 7.0 TB/s). What it took there: four converting groups (two: 1.65 ms); one place to a
+// bytes a cycle. Few rows: the weights' bytes (2 rows to each of 256 experts: 1.13 ms,
+// 6.6 TB/s). What it took there: four converting groups (two: 1.65 ms); one place to a
 // group (two, which let groups run ahead of the products: 1.18); four warps for the sums
-// (eight: 1.18); stages given back as soon as their codes are in registers (after the wait
-// for the group's place: 1.11); and arrivals and waits at the CTA's scope (at the cluster's
-// 3.6, and many rows 14.4): what an arrival hands over is tensor memory, ordered by the tcgen05 fences,
-// and f16 rows, for which every writer has fenced the async proxy.
+// (eight: 1.18); and arrivals and waits at the CTA's scope (all at the cluster's 3.6, and many
+// rows 14.4; those of `ready` alone 2.0, and 10.7 against 8.1): why that holds for operands of the
+// other CTA is said at mbar_arrive_cluster.
 //
 // Tensor memory: sums in two places, columns 0 and 128 on, which share 128 columns in
 // tiles of more than 128 rows (read first and given back early), and the f16 weights,

@@ -15,10 +15,15 @@ namespace moe {
 
 constexpr long long kWaitCycles = 1ll << 32;  // bound of a wait, about two seconds
 
-// Arrival on a barrier of the leading CTA. What it hands over is tensor memory that
-// has been read (ordered by the tcgen05 fences), not data, so it releases at the
-// CTA's scope: at the cluster's it waited for the thread's global stores, about
-// a microsecond per tile (128 tokens, 1024 -> 14336: 456 us against 299).
+// Arrival on a barrier of the leading CTA, released at the CTA's scope (at the cluster's it
+// waits for all that the thread has stored: about a microsecond per tile where a thread stores
+// results, 128 tokens, 1024 -> 14336: 456 us against 299). It hands over
+// - tensor memory that has been read: ordered by the tcgen05 fences, no data;
+// - in product_int8.cu also operands of the arriving CTA, f16 rows in its shared memory and weights in its
+//   tensor memory, for an instruction that the leading CTA issues. The scope alone does not promise those to
+//   another CTA. No thread of the other CTA reads them, though: each SM's tensor core reads its own SM's
+//   memories, of which there is no second copy, and before the arrival every writer has completed the proxy fence (rows) and
+//   tcgen05.wait::st (weights), so nothing is on its way when the arrival leaves.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
