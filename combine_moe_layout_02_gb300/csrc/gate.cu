@@ -10,6 +10,7 @@
 //   c[e]   = dl * balance * E * f[e] / n              (counts are constants)
 //   dz[e]  = p[e] * (c[e] + sum over k with i_k = e of a_k - T),
 //   T      = sum over e of p[e] c[e] + sum over k of p[i_k] a_k
+// (0 in the second sum where weights are normalized; p a_k is formed as scale (p[i_k] / D) (..), which is bounded).
 //
 // A token is a warp's, V of its logits a lane's, in registers; the next token's are
 // loaded meanwhile. The logits are read once and the sums of p stay in registers over
@@ -632,28 +633,43 @@ __global__ void __launch_bounds__(1024) gate_join_kernel(const GateArgs a, int p
     cluster_sync_all();
 }
 
-// The slots' part of the gradient, in lanes below K (K <= 16): expert (or -1), p, and a_k summed
+// The sum of the chosen exponentials below which they are formed again, from the largest chosen logit (a program has dropped
+// the slots above it): from it down they lose bits, and 1 / sum leaves binary32.
+constexpr float kFarSum = 0x1p-60f;
+
+// The slots' part of the gradient, in lanes below K (K <= 16): expert (or -1), p, and p_k a_k summed
 // over slots of the same expert in ascending order (in all of them); in all lanes t, the sum
 // over k of p[i_k] a_k: scale / D times sum_k dw_k p_k - sum_j dw_j p_j = 0 of normalized
-// weights, scale sum_k dw_k p_k of others. `e`: the slots' exponentials, 0 where there is none;
+// weights, scale sum_k dw_k p_k of others. p_k a_k is scale (p_k / D) (dw_k - mean), whose factors are
+// numbers however far the slots are below the row's largest logit. `chosen`: the slots' logits, `top` the row's largest;
 // whose [E]: the warp's, in shared memory, or none (then the slots are compared).
 struct Slots {
     int32_t i;
-    float p, a, t;
+    float p, pa, t;
 };
 static_assert(MOE_MAX_TOPK <= 16, "slots in half a warp");
-__device__ __forceinline__ Slots slots_of(const GateArgs& a, int lane, int32_t i, float dw, float e, float inv, volatile uint8_t* whose) {
+__device__ __forceinline__ Slots slots_of(const GateArgs& a, int lane, int32_t i, float dw, float chosen, float top, float inv,
+                                          volatile uint8_t* whose) {
+    float e = i >= 0 ? exp_of(chosen - top) : 0.f;
     Slots s{i, e * inv, 0.f, 0.f};
     if (a.dweights == nullptr) return s;
-    const float back = half_sum(dw * e);
-    float own = a.scale * dw;
+    float back = half_sum(dw * e);
+    float own;
     if (a.normalize) {
-        const float d = half_sum(e);
-        own = d > 0.f || d != d ? a.scale * (dw - back / d) / (d * inv) : 0.f;  // (0: no slot, or none that counts)
+        float d = half_sum(e);
+        if (__any_sync(kAll, i >= 0 && !(d >= kFarSum))) {
+            const uint32_t most = __reduce_max_sync(kAll, i >= 0 ? order_of(chosen) : 0u);
+            e = i >= 0 && most > kNoLogit ? exp_of(chosen - logit_of(most)) : 0.f;
+            back = half_sum(dw * e);
+            d = half_sum(e);
+        }
+        const float each = __frcp_rn(d);  // (two divisions instead: 262144 x 256 115 us against 101)
+        own = d > 0.f || d != d ? a.scale * (e * each * (dw - back * each)) : 0.f;  // (0: no slot, or none that counts)
     } else {
+        own = a.scale * dw * s.p;
         s.t = __shfl_sync(kAll, a.scale * back * inv, 0);
     }
-    s.a = own;
+    s.pa = own;
     bool twice;
     if (whose != nullptr) {  // two slots of one expert read back one's lane
         if (i >= 0) whose[i] = static_cast<uint8_t>(lane);
@@ -663,10 +679,10 @@ __device__ __forceinline__ Slots slots_of(const GateArgs& a, int lane, int32_t i
         twice = __popc(__match_any_sync(kAll, i)) > 1 && i >= 0;
     }
     if (__any_sync(kAll, twice)) {
-        s.a = 0.f;
+        s.pa = 0.f;
         for (int k = 0; k < a.K; ++k) {
             const float o = __shfl_sync(kAll, own, k);
-            if (__shfl_sync(kAll, i, k) == i) s.a += o;
+            if (__shfl_sync(kAll, i, k) == i) s.pa += o;
         }
     }
     __syncwarp();
@@ -764,20 +780,20 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateAr
             }
             inv = inverse_of(warp_sum(sum));
             t = warp_sum(t) * inv;
-            s = slots_of(a, lane, i_now, dw_now, i_now >= 0 ? exp_of(chosen_now - top) : 0.f, inv, whose[warp]);
+            s = slots_of(a, lane, i_now, dw_now, chosen_now, top, inv, whose[warp]);
             t += s.t;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = routed ? z[i] * inv * (c[i] - t) : 0.f;
         put_row<V, VEC>(to, a.E, lane, z);
         __syncwarp();  // the chosen experts' over what was stored for them
-        if (s.i >= 0) put(to + s.i, s.p * (table[s.i] + s.a - t));
+        if (s.i >= 0) put(to + s.i, fmaf(s.p, table[s.i] - t, s.pa));
         __syncwarp();
     }
 }
 
 // As gate_team_kernel. A token's slots are the team's, in turn; the lane that has a slot's expert
-// adds a_k to its column, in ascending order of k.
+// adds p_k a_k to its column, in ascending order of k.
 __device__ __forceinline__ void fetch_word(void* to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from)
                  : "memory");
@@ -792,7 +808,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_team_grad_kernel(const G
     __shared__ float table[V * L];  // c of each expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, team = lane / L;
     float* column = smem + warp * (64 * V + 4 * slots);  // the exponentials
-    float* add = column + 32 * V;                         // sum over k with i_k = e of a_k
+    float* add = column + 32 * V;                         // sum over k with i_k = e of p_k a_k
     int32_t* ids = reinterpret_cast<int32_t*>(add + 32 * V);
     float* dws = reinterpret_cast<float*>(ids + 2 * slots);
     const float unit = loss_unit(a);
@@ -848,34 +864,49 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_team_grad_kernel(const G
         if (a.dweights != nullptr) {
             const int32_t* i_k = ids + place * slots + team * a.K;
             const float* dw_k = dws + place * slots + team * a.K;
-            float back = 0.f, d = 0.f;
-            if (live)
-                for (int s = l; s < a.K; s += L) {
-                    const int32_t i = i_k[s];
-                    if (i < 0 || i >= a.E) continue;
-                    const float e = column[team * L + column_of<VEC, L>(i)];
-                    back = fmaf(dw_k[s], e, back);
-                    d += e;
-                }
-            back = team_sum<L>(back);
-            d = team_sum<L>(d);
-            float unit_a = a.scale, mean = 0.f;
-            if (a.normalize) {
-                mean = back / d;
-                unit_a = a.scale / (d * inv);
-            } else {
-                t += a.scale * back * inv;
+            float back, d;
+            const auto add_up = [&] {
+                back = d = 0.f;
+                if (live)
+                    for (int s = l; s < a.K; s += L) {
+                        const int32_t i = i_k[s];
+                        if (i < 0 || i >= a.E) continue;
+                        const float e = column[team * L + column_of<VEC, L>(i)];
+                        back = fmaf(dw_k[s], e, back);
+                        d += e;
+                    }
+                back = team_sum<L>(back);
+                d = team_sum<L>(d);
+            };
+            add_up();
+            const bool far = live && a.normalize && !(d >= kFarSum);
+            if (__any_sync(kAll, far)) {  // the slots' columns from their largest logit
+                const T* from = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.logits) + g * a.row_stride);
+                uint32_t most = 0;
+                if (far)
+                    for (int s = l; s < a.K; s += L)
+                        if (i_k[s] >= 0 && i_k[s] < a.E) most = max(most, order_of(logit(from, i_k[s])));
+                most = team_max<L>(most);
+                if (far && most > kNoLogit)
+                    for (int s = l; s < a.K; s += L)
+                        if (i_k[s] >= 0 && i_k[s] < a.E)
+                            column[team * L + column_of<VEC, L>(i_k[s])] = exp_of(logit(from, i_k[s]) - logit_of(most));
+                __syncwarp();
+                add_up();
             }
+            const float mean = a.normalize ? back / d : 0.f, each = a.normalize ? 1.f / d : inv;
+            if (!a.normalize) t += a.scale * back * inv;
             if (live && (!a.normalize || d > 0.f || d != d))  // (0: no slot, or none that counts)
                 for (int s = 0; s < a.K; ++s) {
                     const int32_t i = i_k[s];
                     if (i < 0 || i >= a.E || (i / VEC) % L != l) continue;
-                    add[column_of<VEC, L>(i) - l + lane] += unit_a * (dw_k[s] - mean);
+                    const int at = column_of<VEC, L>(i) - l + lane;
+                    add[at] += a.scale * (column[at] * each * (dw_k[s] - mean));
                 }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            z[i] = live ? z[i] * inv * (c[i] + add[32 * i + lane] - t) : 0.f;
+            z[i] = live ? fmaf(z[i] * inv, c[i] - t, add[32 * i + lane]) : 0.f;
             add[32 * i + lane] = 0.f;  // a lane's own
         }
         if (g < a.S) put_row<V, VEC, L>(reinterpret_cast<T*>(static_cast<uint8_t*>(a.dlogits) + g * a.dlogits_stride), a.E, l, z);
@@ -1081,7 +1112,7 @@ __global__ void __launch_bounds__(32 * kWideWarps) gate_wide_grad_kernel(const G
             __syncthreads();
             inv = inverse_of(warp_sum(lane < warps ? sums[turn][0][lane] : 0.f));
             t = warp_sum(lane < warps ? sums[turn][1][lane] : 0.f) * inv;
-            s = slots_of(a, lane, i_now, dw_now, i_now >= 0 ? exp_of(chosen_now - top) : 0.f, inv, nullptr);
+            s = slots_of(a, lane, i_now, dw_now, chosen_now, top, inv, nullptr);
             t += s.t;
         }
 #pragma unroll
@@ -1089,7 +1120,7 @@ __global__ void __launch_bounds__(32 * kWideWarps) gate_wide_grad_kernel(const G
         put_row<V, VEC>(to, mine.E, lane, z);
         __syncwarp();  // the warp's chosen experts' over what was stored for them
         const int at = s.i - warp * kWide;
-        if (s.i >= 0 && at >= 0 && at < kWide) put(to + at, s.p * (unit * static_cast<float>(__ldg(a.expert_count + s.i)) + s.a - t));
+        if (s.i >= 0 && at >= 0 && at < kWide) put(to + at, fmaf(s.p, unit * static_cast<float>(__ldg(a.expert_count + s.i)) - t, s.pa));
         __syncwarp();
     }
 }
