@@ -1094,7 +1094,7 @@ class Buffers:
 
     # ---- MXFP4 experts (after layout, notify and notify_expert; expert_alignment a
     # multiple of MOE_FP4_ROW_TILE) ------------------------------------------------
-    _fp4 = None
+    _fp4 = _fp4_rows = None
 
     def _plan_buffer(self, stream=None):
         if getattr(self, "plan", None) is None:
@@ -1104,19 +1104,34 @@ class Buffers:
     def _fp4_buffers(self, stream=None):
         if getattr(self, "plan", None) is not None and self._fp4 is not None:
             return
-        s, dev = self.shape, self.device
         self._slot_tables(stream)
         self._plan_buffer(stream)
-        t = MOE_FP4_ROW_TILE
-        self.fp4_rows = (moe_max_expert_rows(s) + t - 1) // t * t
         if self._fp4 is None:
-            with _made_on(stream, dev):
-                self._fp4 = Fp4Rows(self.fp4_rows, s.H, dev)
+            with _made_on(stream, self.device):
+                self._fp4 = Fp4Rows(self.fp4_rows, self.shape.H, self.device)
+
+    @property
+    def fp4_rows(self):
+        """Rows of ``fp4``: enough for every routing, whole tiles."""
+        if self._fp4_rows is None:
+            t = MOE_FP4_ROW_TILE
+            self._fp4_rows = (moe_max_expert_rows(self.shape) + t - 1) // t * t
+        return self._fp4_rows
+
+    @fp4_rows.setter
+    def fp4_rows(self, rows):
+        self._fp4_rows = rows
 
     @property
     def fp4(self):
-        """The arena's rows as MXFP4. With the int8 payload they are made when something first uses them."""
-        self._fp4_buffers()
+        """The arena's rows as MXFP4. With the int8 payload they are made by dispatch_expert_fp4 on its stream, or here. What
+        is made here comes from the current stream's memory, whose queued work is waited for once: any stream may use it."""
+        if self._fp4 is None:
+            self._fp4_buffers()
+            import torch
+
+            if torch.device(self.device).type == "cuda" and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.device).synchronize()
         return self._fp4
 
     @fp4.setter
