@@ -66,10 +66,11 @@ __device__ __forceinline__ void block_join(float (&v)[SUMS + MOST], float (*plac
     }
 }
 
-// rstd of a row whose squares add up past binary32: the sum is taken of h 2^-90. (An
-// infinity or a NaN in the row gives 0 or NaN, as it does without this.) Whole blocks call it.
+// rstd of a row whose mean square and eps add up past binary32: the sum is taken of h 2^-90, and eps joins it by
+// 2^-180, which no eps that counts leaves binary32 by. (An infinity or a NaN in the row gives 0 or NaN, as it does
+// without this.) Whole blocks call it.
 template <int C>
-__device__ __forceinline__ float far_rstd(const float (&h)[C][8], int32_t H, float (*place)[32]) {
+__device__ __forceinline__ float far_rstd(const float (&h)[C][8], int32_t H, float eps, float (*place)[32]) {
     float sum[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < C; ++j)
@@ -79,7 +80,7 @@ __device__ __forceinline__ float far_rstd(const float (&h)[C][8], int32_t H, flo
             sum[0] = fmaf(v, v, sum[0]);
         }
     block_join<1, false>(sum, place);
-    return __frsqrt_rn(__fdiv_rn(sum[0], static_cast<float>(H))) * kFarUnit;
+    return __frsqrt_rn(__fdiv_rn(sum[0], static_cast<float>(H)) + eps * kFarUnit * kFarUnit) * kFarUnit;
 }
 
 // The tile of rows that a block of a plan's call shares with others: [row, end) by kPlanParts.
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(512, QUANT ? 1 : 2) norm_kernel(const NormArgs
             }
         }
         block_join<1, QUANT>(joined, place);
-        float rstd = __frsqrt_rn(__fdiv_rn(joined[0], static_cast<float>(a.H)) + a.eps);
-        if (!(joined[0] <= kFloatMax)) rstd = far_rstd<C>(h, a.H, place + 2);
+        const float mean = __fdiv_rn(joined[0], static_cast<float>(a.H)) + a.eps;
+        float rstd = __frsqrt_rn(mean);
+        if (!(mean <= kFloatMax)) rstd = far_rstd<C>(h, a.H, a.eps, place + 2);
         if (a.y) {
 #pragma unroll
             for (int j = 0; j < C; ++j) {
@@ -329,12 +331,13 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradArgs a) {
         float sums[2];
         add_up(1.f, sums);
         block_join<2, false, (TEAMS > 1)>(sums, place);
-        float rstd = __frsqrt_rn(__fdiv_rn(sums[0], static_cast<float>(a.H)) + a.eps);
+        const float mean = __fdiv_rn(sums[0], static_cast<float>(a.H)) + a.eps;
+        float rstd = __frsqrt_rn(mean);
         float back = sums[1] / static_cast<float>(a.H) * rstd * rstd;
-        if (!(sums[0] <= kFloatMax)) {  // squares past binary32: all in h 2^-90, where eps is nothing
+        if (!(mean <= kFloatMax)) {  // past binary32: all in h 2^-90, as in far_rstd()
             add_up(kFarUnit, sums);
             block_join<2, false, (TEAMS > 1)>(sums, place + 2);
-            rstd = __frsqrt_rn(__fdiv_rn(sums[0], static_cast<float>(a.H)));
+            rstd = __frsqrt_rn(__fdiv_rn(sums[0], static_cast<float>(a.H)) + a.eps * kFarUnit * kFarUnit);
             back = sums[1] / static_cast<float>(a.H) * rstd * rstd * kFarUnit;
             rstd *= kFarUnit;
         }

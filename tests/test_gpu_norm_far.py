@@ -1,0 +1,34 @@
+"""The norm and its gradient where the mean square and eps are near the end of binary32."""
+
+import numpy as np
+import pytest
+
+from combine_moe_layout_02_gb300 import moe
+from tests import router_ref as ref
+from tests.test_gpu_norm import BF, U, _bf16, _np, _rel
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H", [16, 64, 1040, 7168])
+@pytest.mark.parametrize("eps", [3.4e38, 1e38, 1e36, 1e-6])
+def test_large_eps(H, eps):
+    """eps counts next to squares whose sum leaves binary32, and where only the two together do."""
+    import torch
+
+    powers = [40, 58, 60, 61, 62, 63, 64, 66, 70, 100]
+    x = _bf16((len(powers), H), 1) * torch.tensor([2.0 ** p for p in powers])[:, None].to(torch.bfloat16)
+    w, dy = _bf16((H,), 2), _bf16((len(powers), H), 3)
+    e32 = float(np.float32(eps))
+    y, q, qs = torch.empty_like(x).cuda(), torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(len(x), device="cuda")
+    moe.moe_rms_norm(x.cuda(), w.cuda(), eps, y=y, q=q, q_scale=qs)
+    v, _ = ref.rms(_np(x), _np(w), e32)
+    assert (np.abs(_np(y) - v) <= np.abs(v) * (BF + _rel(H) * (1 + BF)) + 1e-40).all()
+    scale = np.abs(v).max(1) / 127
+    assert (np.abs(_np(qs) - scale) <= scale * (_rel(H) + 2 * U)).all()
+    assert (np.abs(_np(q) - v / scale[:, None]) <= 0.5 + 127 * (2 * _rel(H) + 4 * U)).all()
+    dh = torch.empty_like(y)
+    moe.moe_rms_norm_grad(dy.cuda(), x.cuda(), w.cuda(), eps, dh)
+    want, _, mag, _ = ref.rms_grad(_np(dy), _np(x), _np(w), e32)
+    # products of numbers of fewer bits near the end of binary32: as test_gpu_norm's rows of far values
+    assert (np.abs(_np(dh) - want) <= np.abs(want) * BF + mag * (2 * _rel(H) + 80 * U) + 1e-37).all()
