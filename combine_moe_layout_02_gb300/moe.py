@@ -454,6 +454,7 @@ class _Types:
         import torch
 
         self.bf16, self.f32, self.i8, self.u8, self.flag = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.bool
+        self.i32 = torch.int32
         self.empty_like = torch.empty_like  # 1.3 us of host time, new_empty 3
         # int8 codes (dispatch's slots are bytes); scales; bf16 rows or their bit patterns
         self.codes, self.scales, self.rows = (torch.int8, torch.uint8), (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
@@ -666,7 +667,7 @@ class Int8Rows:
         dev = T.device()
         b = _rows_of(x, shape, T.bf16, 2, "x" if pack else "out", dev)
         q, s = _rows_of(self.q, shape, T.i8, 1, "q", dev), _scales_of(self.scale, shape[0], "scale")
-        plan = _NO_PLAN if plan is None else _plan_args(E, plan)
+        plan = _NO_PLAN if plan is None else _plan_on(E, plan, dev)
         if pack:
             st = lib().moe_int8_pack(*self._sizes, *b, *q, *s, *plan, _stream(stream))
         else:
@@ -685,31 +686,54 @@ class Int8Rows:
         return out
 
 
-def _held(t, rows, stride, row_bytes, dtypes, name, device):
-    """Address of a tensor that holds `rows` rows of row_bytes, `stride` bytes apart; an address is taken as it is."""
+def _held(t, rows, stride, row_bytes, dtypes, name, device, packed=False):
+    """Address of a tensor that holds `rows` rows of row_bytes, `stride` bytes apart; an address is taken as it is. packed:
+    the stride is not the caller's, so a tensor of several dimensions has rows of that width."""
     if t is None or isinstance(t, int):
         return t
+    if packed and t.dim() > 1 and t.size(-1) * t.element_size() != row_bytes:
+        raise ValueError("expected %s with rows of %d bytes, got %s in %s (or its row stride)" % (name, row_bytes, tuple(t.shape), t.dtype))
     if t.dtype not in dtypes or not t.is_contiguous() or (t.nbytes < (rows - 1) * stride + row_bytes and rows > 0):
         raise ValueError("expected %s contiguous in %s with %d rows of %d bytes, %d apart, got %s in %s" % (
             name, " or ".join(str(d) for d in dtypes), rows, row_bytes, stride, tuple(t.shape), t.dtype))
     return t.data_ptr() if t.get_device() == device else _placed(t, name)
 
 
+def _plan_on(E, plan, device):
+    """A plan's arguments, held to its type and place."""
+    if plan.dtype is not _t().i32 or plan.get_device() != device or not plan.is_contiguous():
+        return E, _flat(plan, plan.numel(), _t().i32, "plan"), plan.numel()
+    return E, plan.data_ptr(), plan.numel()
+
+
+def _word(err, device):
+    """Address of an error word (int32, one or more)."""
+    if err is None or isinstance(err, int):
+        return err
+    if err.dtype is not _t().i32 or err.get_device() != device or err.numel() < 1:
+        _typed(err, _t().i32, "err")
+        if err.numel() < 1:
+            raise ValueError("expected err of one word or more")
+        return _placed(err, "err")
+    return err.data_ptr()
+
+
 def moe_expert_product_int8(E, N, K, gated, wq, ws, xq, xs, rows, plan, y, err, x_row_stride=None, xs_stride=4,
                             y_row_stride=None, stream=None):
     """y's rows of every expert (plan None, E 1: of all rows) from int8 weights and rows (include/moe.h). Rows of xq are
     packed, scales of xs one after another and y rows packed unless the strides (bytes) say otherwise. Tensors are held to
-    their sizes and types; addresses (of the scales in dispatch's slots, say) are taken as they are."""
+    their sizes, types and device, packed rows to their width; addresses (of the scales in dispatch's slots, say) are taken as they are."""
     T, width = _t(), (N // 2 if gated else N) * 2
     dev = T.device()
-    x_row_stride = K if x_row_stride is None else x_row_stride
-    y_row_stride = width if y_row_stride is None else y_row_stride
+    x_packed, y_packed = x_row_stride is None, y_row_stride is None
+    x_row_stride = K if x_packed else x_row_stride
+    y_row_stride = width if y_packed else y_row_stride
     st = lib().moe_expert_product_int8(
-        E, N, K, gated, _held(wq, E * N, K, K, T.codes, "wq", dev), _held(ws, E * N, 4, 4, T.scales, "ws", dev),
-        _held(xq, rows, x_row_stride, K, T.codes, "xq", dev), x_row_stride,
+        E, N, K, gated, _held(wq, E * N, K, K, T.codes, "wq", dev, True), _held(ws, E * N, 4, 4, T.scales, "ws", dev),
+        _held(xq, rows, x_row_stride, K, T.codes, "xq", dev, x_packed), x_row_stride,
         _held(xs, rows, xs_stride, 4, T.scales, "xs", dev), xs_stride, rows,
-        *(_NO_PLAN if plan is None else _plan_args(E, plan))[1:], _held(y, rows, y_row_stride, width, T.rows, "y", dev),
-        y_row_stride, _ptr(err), _stream(stream))
+        *(_NO_PLAN if plan is None else _plan_on(E, plan, dev))[1:],
+        _held(y, rows, y_row_stride, width, T.rows, "y", dev, y_packed), y_row_stride, _word(err, dev), _stream(stream))
     if st:
         raise MoeError(st, "moe_expert_product_int8")
 
