@@ -800,9 +800,9 @@ moe_status moe_test_fused_barrier(uint32_t spin_limit, int32_t skip_cta);
  * moe_expert_product_int8 but for dense calls of few rows, which wait on nothing, or
  * the first product of moe_expert_ffn_fp4; that one only): its waits give up
  * after `wait_cycles` clock cycles (instead of 2^32), and if quit_warp >= 0 that
- * warp of each CTA (0 loads, 1 issues, 4..11 take the sums out or, of int8 codes
- * in small tiles, 8..11 convert them) acts as if its
- * first wait had run out. The call records MOE_ERR_DEVICE_TIMEOUT in err, every
+ * warp of each CTA (0 loads, 1 issues, 4..11 take the sums out; of int8 codes
+ * 4..7 and 3, the last of its kind, take the sums out and 8..11 are one of each
+ * group that converts) acts as if its first wait had run out. The call records MOE_ERR_DEVICE_TIMEOUT in err, every
  * role ends, what is in flight lands (bounded), and the context stays usable;
  * results are undefined. Returns MOE_ERR_INVALID_ARG for wait_cycles = 0 or a
  * quit_warp outside -1..11.
