@@ -58,7 +58,10 @@ __device__ __forceinline__ float logit_of(uint32_t order) {
 }
 constexpr uint32_t kNoLogit = 0x007fffffu;  // order_of(-infinity): an expert that may not be chosen; numbers are above
 
-// e^x for x <= 0 by the hardware's 2^x (to 2^-22; below 2^-126: 0); x log2 e is rounded once.
+// e^x for x <= 0 by the hardware's 2^x (to 2^-22; below 2^-126: 0); x log2 e is rounded once, which adds |x| 2^-24 at most,
+// as much as the rounding of x = z - max does. With this and the reciprocal and quotient below, 262144 tokens of 256 experts have weights
+// off by 6.0e-8 in the root mean square (binary32 torch: 5.7e-8); rounded reciprocals and quotients make it 5.8e-8 and the forward pass
+// 128 -> 146 us, the product's lost bits added back 5.7e-8 and 153 us.
 __device__ __forceinline__ float exp_of(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));

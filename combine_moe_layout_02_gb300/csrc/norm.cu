@@ -136,7 +136,8 @@ constexpr int kDepth = 2, kPlainDepth = 3;
 
 // QUANT: int8 rows are wanted. Their scale is rstd max |h weight| / 127 and the codes are
 // h weight 127 / max |h weight|, so that the row's sum and its maximum are joined at
-// once. Where h weight leaves binary32's range on the way (and in rows of zeros) the
+// once. A code's quotient has two roundings (h weight, 127 / max) and is off by 127 * 2^-23 at most, so codes beside a tie
+// may differ from those of rows that are normed first and divided by their scale. Where h weight leaves binary32's range on the way (and in rows of zeros) the
 // values are formed first and their maximum joined by itself.
 template <int C, bool QUANT>
 __global__ void __launch_bounds__(512, QUANT ? 1 : 2) norm_kernel(const NormArgs a) {

@@ -153,6 +153,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 }
 
 // silu(g) * u. e^-|g| <= 1, so nothing overflows and the denominator is in [1, 2].
+// The hardware's exponential and quotient are off by 2 + 1.173 |g| and 2 units, far below the result's rounding to bf16; expf and a
+// rounded division change no digit of the int8 chain's error (500 rows 7168 -> 2048 -> 7168: 0.0018 against 64 bits, as binary32 torch) and cost
+// 262144 rows 7168 -> 4096 9.2 ms against 8.2.
 __device__ __forceinline__ float gate_times_up(float g, float u) {
     const float e = __expf(-fabsf(g));
     return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;

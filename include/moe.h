@@ -506,7 +506,8 @@ moe_status moe_expert_ffn_fp4(const moe_shape* shape, int32_t inner, const uint1
  * ids are -1, its weights 0 and it is in no sum. An expert whose logit is
  * -infinity is not chosen: slots that find no expert hold -1 and 0. NaN counts as
  * the largest logit; a row with a NaN or +infinity has valid ids and weights NaN
- * (and makes expert_prob and the loss NaN).
+ * (and makes expert_prob and the loss NaN). Ids and counts are exact; the exponentials
+ * are the hardware's (binary32, off by up to 2^-21 + |z - max| 2^-23, relative).
  *
  *   shape        E, S and K are used; the rest is only checked
  *   type         of the logits (and of their gradient): MOE_F32 or MOE_BF16
@@ -553,9 +554,10 @@ moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logit
  *
  *   h = x + residual (binary32),  rstd = 1 / sqrt(mean h^2 + eps)
  *   sum = bf16_rne(h),  y = bf16_rne(v),  v = h * rstd * weight
- *   q_scale = max|v| / 127,  q = rint(v / q_scale) as dispatch's int8 payload has it
- *             (a row of zeros: 0; a row whose v holds an infinity or a NaN: q_scale
- *             NaN, codes 0)
+ *   q_scale = max|v| / 127,  q = v / q_scale to the nearest whole number; a quotient
+ *             within 2^-15 of a tie may go either way (v is not rounded on the way, so these
+ *             are not moe_int8_pack's codes of y, which alone are dispatch's bit for bit).
+ *             A row of zeros: 0; a row whose v holds an infinity or a NaN: q_scale NaN, codes 0
  *
  * Every result may be NULL, but not all of them.
  *

@@ -32,3 +32,21 @@ def test_large_eps(H, eps):
     want, _, mag, _ = ref.rms_grad(_np(dy), _np(x), _np(w), e32)
     # products of numbers of fewer bits near the end of binary32: as test_gpu_norm's rows of far values
     assert (np.abs(_np(dh) - want) <= np.abs(want) * BF + mag * (2 * _rel(H) + 80 * U) + 1e-37).all()
+
+
+@pytest.mark.parametrize("H,rows", [(16, 4000), (128, 4000), (1040, 1000), (7168, 300)])
+def test_codes_are_the_nearest(H, rows):
+    """Of v's quotients themselves: the row's factor cancels, so a code is off by half and the two roundings of its quotient
+    (three, and the scale's, where rows are normed first): 127 * 2^-22."""
+    import torch
+
+    x, r, w = _bf16((rows, H), 5), _bf16((rows, H), 6, 3.0), _bf16((H,), 7)
+    x[-rows // 8:] *= 2.0 ** -80  # normed first
+    r[-rows // 8:] *= 2.0 ** -80
+    h = (x.float() + r.float()).double().numpy()  # binary32, as the sum is
+    q, qs = torch.empty((rows, H), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    moe.moe_rms_norm(x.cuda(), w.cuda(), 1e-30, residual=r.cuda(), q=q, q_scale=qs)
+    v = h * _np(w)
+    quotient = v / (np.abs(v).max(1, keepdims=True) / 127)
+    off = np.abs(_np(q) - quotient)
+    assert off.max() <= 0.5 + 127 * 2.0 ** -22 <= 0.5 + 2.0 ** -15
