@@ -385,7 +385,12 @@ product_int8_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, cons
 
     using List = typename ListOf<ROWS>::Type;
     uint32_t tiles = a.p.tile_cap;
-    if (a.p.plan) tiles = max(0, min(uniform(__ldg(a.p.plan)), a.p.tile_cap));
+    if (a.p.plan) {
+        const int32_t planned = uniform(__ldg(a.p.plan));
+        // More tiles than the rows have room for (tile_cap): the last ones lie outside and are not looked up.
+        if (planned > a.p.tile_cap && blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, MOE_ERR_CAPACITY);
+        tiles = max(0, min(planned, a.p.tile_cap));
+    }
     const uint32_t mtiles = (a.p.N + kMTile - 1) / kMTile;
     const uint32_t step = gridDim.x / (2 * a.split), first = blockIdx.x / (2 * a.split);
     const int nstages = static_cast<int>(ceil_div(a.p.K, kStageK));

@@ -46,3 +46,24 @@ def test_a_warp_of_every_kind_gives_up(form, quit_warp):
     call(y[2])  # the hook armed one call only
     torch.cuda.synchronize()
     assert int(err[0]) == 0 and torch.equal(y[0], y[2])
+
+
+@pytest.mark.parametrize("rows,fit", [(100, 1), (129, 2), (200, 2), (257, 3), (300, 3)])
+def test_a_plan_of_more_rows_than_there_are_is_reported(rows, fit):
+    """Tiles behind the rows are skipped and reported, however many there are; the others are computed."""
+    import torch
+
+    E, N, K = 5, 64, 64
+    plan, first = _plan(E, np.full(E, 1))
+    a, b, c, d = _up(*_operands(E, N, K, rows, 2))
+    got = []
+    for n in (rows, int(first[-1])):
+        x, s = torch.zeros((n, K), dtype=torch.int8, device="cuda"), torch.zeros((n,), device="cuda")
+        x[:rows], s[:rows] = c, d
+        y, err = torch.full((n, N), 7.0, dtype=torch.bfloat16, device="cuda"), _err()
+        moe.moe_expert_product_int8(E, N, K, 0, a, b, x, s, n, plan, y, err)
+        got.append((y, int(err[0])))
+    assert got[0][1] == moe.MOE_ERR_CAPACITY and got[1][1] == 0
+    live = torch.arange(rows, device="cuda") % 128 == 0
+    assert int(live.sum()) == fit and (got[0][0][live] != 7).any(1).all()
+    assert torch.equal(got[0][0], got[1][0][:rows])
