@@ -780,6 +780,13 @@ moe_status moe_rms_norm(int64_t rows, int32_t H, float eps, const uint16_t* x, i
         !ok_rows(sum, sum_stride, bytes) || !ok_rows(y, y_stride, bytes) || !ok_rows(q, q_stride, H))
         return MOE_ERR_INVALID_ARG;
     if ((!sum && !y && !q) || !q != !q_scale || (y && y == sum)) return MOE_ERR_INVALID_ARG;
+    // In place: the same rows, and none of another width.
+    const auto apart = [](const void* p, int64_t p_stride, const void* r, int64_t r_stride) { return p != r || p_stride == r_stride; };
+    if ((sum && !(apart(sum, sum_stride, x, x_stride) && apart(sum, sum_stride, residual, residual_stride))) ||
+        (y && !(apart(y, y_stride, x, x_stride) && apart(y, y_stride, residual, residual_stride))))
+        return MOE_ERR_INVALID_ARG;
+    for (const void* p : {x, residual, static_cast<const uint16_t*>(sum), static_cast<const uint16_t*>(y)})
+        if (q && static_cast<const void*>(q) == p) return MOE_ERR_INVALID_ARG;
     if (q && (H % 16 != 0 || !aligned(q_scale, 4) || !ok_stride(q_scale_stride, 4, 4))) return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.rows = rows;
@@ -817,6 +824,7 @@ moe_status moe_rms_norm_grad(int64_t rows, int32_t H, float eps, const uint16_t*
     if (rows > 0 && (dy == nullptr || h == nullptr || dh == nullptr || !ok_rows(dy, dy_stride, bytes) ||
                      !ok_rows(h, h_stride, bytes) || !ok_rows(dh, dh_stride, bytes) || !ok_rows(dsum, dsum_stride, bytes)))
         return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (dh == h || (dh == dy && dh_stride != dy_stride) || (dh == dsum && dh_stride != dsum_stride))) return MOE_ERR_INVALID_ARG;
     if (!ok_ptr(weight, 1, 16) || !ok_opt(dweight, 16)) return MOE_ERR_INVALID_ARG;
     if (dweight && (!ok_ptr(scratch, 1, 256) || scratch_bytes < moe_rms_norm_grad_scratch_bytes(rows, H))) return MOE_ERR_INVALID_ARG;
     NormGradArgs a{};
@@ -849,7 +857,7 @@ moe_status int8_rows_args(int32_t groups, int64_t rows, int32_t width, int32_t g
     if (!ok_stride(x_stride, 2 * static_cast<int64_t>(width), 16) || !ok_stride(q_stride, width, 16) || !ok_stride(scale_stride, 4, 4))
         return MOE_ERR_INVALID_ARG;
     const int64_t n = groups * rows;
-    if (!ok_ptr(x, n, 16) || !ok_ptr(q, n, 16) || !ok_ptr(scale, n, 4)) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(x, n, 16) || !ok_ptr(q, n, 16) || !ok_ptr(scale, n, 4) || (n > 0 && x == q)) return MOE_ERR_INVALID_ARG;
     if (plan) {
         if (groups != 1 || gated || E < 1 || E > MOE_MAX_EXPERTS || rows > INT32_MAX) return MOE_ERR_INVALID_ARG;
         if (!aligned(plan, 16) || plan_ints < plan_tiles_at(E)) return MOE_ERR_INVALID_ARG;

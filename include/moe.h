@@ -569,8 +569,8 @@ moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logit
  *   strides      bytes from row to row: multiples of 16, at least a row's bytes;
  *                q_scale_stride a multiple of 4 >= 4 (int8 slots of dispatch hold the
  *                scale behind the row: any pair of strides will do)
- * sum may be x or residual itself, y may be x, residual or neither (not also sum);
- * no other overlap.
+ * sum may be x or residual itself, y may be x, residual or neither (not also sum), with
+ * the same stride; no other overlap.
  *
  * moe_rms_norm_grad -- its gradient at h (the sum as it was kept), without int8:
  *
@@ -580,7 +580,7 @@ moe_status moe_gate_grad(const moe_shape* shape, int32_t type, const void* logit
  * dh is the gradient of x and of the residual alike. dsum: the gradient of the
  * sum that was passed on, or NULL. dweight: float [H] or NULL; with it scratch
  * holds moe_rms_norm_grad_scratch_bytes(rows, H) bytes (256-byte aligned). dh may be
- * dy or dsum itself; no other overlap.
+ * dy or dsum itself, with the same stride; no other overlap.
  */
 moe_status moe_rms_norm(int64_t rows, int32_t H, float eps, const uint16_t* x, int64_t x_stride,
                         const uint16_t* residual, int64_t residual_stride, const uint16_t* weight, uint16_t* sum,
@@ -602,7 +602,8 @@ moe_status moe_rms_norm_grad(int64_t rows, int32_t H, float eps, const uint16_t*
  *   width          a multiple of 16, at most MOE_INT8_MAX_WIDTH
  *   gated          0, or 1: x holds all gate rows, then all up rows of an operand
  *                  (rows % 32 == 0), the operand 16 gate rows and their 16 up rows by turns
- *   x              bf16 bits, rows x_row_stride bytes apart (a multiple of 16, >= 2 * width)
+ *   x              bf16 bits, rows x_row_stride bytes apart (a multiple of 16, >= 2 * width);
+ *                  it and q may not overlap
  *   q              int8, rows q_row_stride bytes apart (a multiple of 16, >= width)
  *   scale          float, scale_stride bytes apart (a multiple of 4, >= 4)
  *   plan           NULL, or a plan of moe_expert_plan for E experts (plan_ints words):
