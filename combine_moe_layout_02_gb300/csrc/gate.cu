@@ -15,8 +15,8 @@
 // A token is a warp's, V of its logits a lane's, in registers; the next token's are
 // loaded meanwhile. The logits are read once and the sums of p stay in registers over
 // a warp's tokens. Bound by the selection's instructions (forward: 262144 tokens, 256
-// experts, 8 picks 130 us, 2.2 TB/s, 0.73 instructions a cycle) and by memory (backward:
-// 102 us, 5.4 TB/s). Up to 64 experts several tokens share a warp.
+// experts, 8 picks 119-128 us, 2.2 TB/s, 0.74 instructions a cycle) and by memory (backward:
+// 99-101 us, 5.5 TB/s). Up to 64 experts several tokens share a warp.
 //
 // Selection: whole numbers in the order of the logits, the low bits replaced by the
 // expert's number counted down: one maximum over the warp then gives the next expert,
@@ -1175,6 +1175,7 @@ Kernel kernel_for(int E, bool by) {
         case 8: return team_at<GRAD, T, 8>(by);
         default: break;
     }
+    // Of four logits to a lane 16-bit ones are no 16 bytes: they go one by one (262144 x 128, 8 picks: 99 us each way; 32-bit ones 98 and 87).
     constexpr int kVec = 16 / sizeof(T), kVec4 = kVec <= 4 ? kVec : 1;
     switch (logits_of_a_lane(E)) {
         case 4: return by ? kernel_at<GRAD, T, 4, kVec4>() : kernel_at<GRAD, T, 4, 1>();

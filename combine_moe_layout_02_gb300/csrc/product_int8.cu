@@ -19,11 +19,11 @@
 // of its own for what it makes, so they work while others' places are multiplied.
 //
 // What bounds it. Many rows: the tensor pipe and power (262144 rows 7168 -> 4096 gated:
-// 8.0-8.4 ms, 1.84-1.92 PFLOP/s; bursts of 8192 rows 2.0; back to back for seconds 9.6).
+// 8.0-8.5 ms, 1.81-1.92 PFLOP/s; back to back for seconds 9.5-9.8).
 // Weights through tensor memory save shared memory's rate: 64 of K are 16 KB of codes in,
 // 16 out, 16 of f16 rows in and 16 out, 64 KB in the 512 cycles of their products, at 128
-// bytes a cycle. Few rows: the weights' bytes (2 rows to each of 256 experts: 1.13 ms,
-// 6.6 TB/s). What it took there: four converting groups (two: 1.65 ms); one place to a
+// bytes a cycle. Few rows: the weights' bytes (2 rows to each of 256 experts: 1.09 ms,
+// 6.9 TB/s; 1.13 out of a cold L2). What it took there: four converting groups (two: 1.65 ms); one place to a
 // group (two, which let groups run ahead of the products: 1.18); four warps for the sums
 // (eight: 1.18); and arrivals and waits at the CTA's scope (all at the cluster's 3.6, and many
 // rows 14.4; those of `ready` alone 2.0, and 10.7 against 8.1): why that holds for operands of the
@@ -251,8 +251,8 @@ struct Units {
 
 // The same of tiles of up to 128 rows, which a plan's average asks for where some experts may have far more: both halves of a
 // plan's tile are units, neighbours in the order, so that the pairs, which get units by turns, get as much to do. A warp holds
-// 32 of the plan's tiles, a lane each. 8008 rows over 249 experts, one with 1001, 2048 -> 7168 701 -> 670 us, 31 rows
-// each 643 -> 621. (Looking units up costs more than it gives where rows are few, 2 rows each 7168 -> 4096 in tiles of
+// 32 of the plan's tiles, a lane each. 8008 rows over 255 experts, one with 933, 2048 -> 7168 721 -> 705 us, 7168 -> 4096
+// 1435 -> 1324, 31 rows each 636 -> 629. (Looking units up costs more than it gives where rows are few, 2 rows each 7168 -> 4096 in tiles of
 // 64 1098 -> 1135, and where a tile is a unit anyway, 1024 rows each 8.28 -> 8.38 ms.)
 struct HalfUnits {
     static constexpr int kSize = kPlanTileRows / 2;
@@ -845,9 +845,9 @@ cudaError_t launch_cut(Args a, cudaStream_t stream) {
     if (a.p.plan) {
         // By the rows that the routing gives an expert on average: more stages where they are few, against experts of more
         // rows than the kernel takes at a time, whose weights are read again. 256 experts 7168 -> 4096 with 2 / 31 / 64 / 96 /
-        // 140 rows each: 1098 / 1115 / 1133 / 2230 / - us with 64 at a time, 1151 / 1174 / 1215 / 1295 / 2463 with 128,
-        // 1253 / - / 1323 / 1384 / 1575 with 256; 8008 rows, one expert with 1001: 1395 with 64, 1265 with 128; 24576
-        // rows, one with 1209: 1568 with 128, 1534 with 256.
+        // 140 rows each: 1091 / 1109 / 1134 / 2218 / 3326 us with 64 at a time, 1176 / 1192 / 1219 / 1281 / 2411 with 128,
+        // 1259 / 1302 / 1339 / 1388 / 1550 with 256; 8008 rows, one expert with 933: 1607 with 64, 1326 with 128; 24576
+        // rows, one with 2872: 1791 with 128, 1716 with 256.
         const int64_t each = a.p.plan_rows / a.p.E;
         if (plan.split == 1 && plan.shift == 0) plan.rows = each <= 24 ? 64 : each <= 96 ? 128 : 256;
     } else {
