@@ -702,8 +702,8 @@ def _held(t, rows, stride, row_bytes, dtypes, name, device, packed=False):
 def _plan_on(E, plan, device):
     """A plan's arguments, held to its type and place."""
     if plan.dtype is not _t().i32 or plan.get_device() != device or not plan.is_contiguous():
-        return E, _flat(plan, plan.numel(), _t().i32, "plan"), plan.numel()
-    return E, plan.data_ptr(), plan.numel()
+        return int(E), _flat(plan, plan.numel(), _t().i32, "plan"), plan.numel()
+    return int(E), plan.data_ptr(), plan.numel()
 
 
 def _word(err, device):

@@ -73,3 +73,13 @@ def test_packing_holds_its_plan():
     op = moe.Int8Rows(4, 64, "cpu")
     with pytest.raises(ValueError):
         op.pack(torch.zeros((4, 64), dtype=torch.bfloat16), E=2, plan=torch.zeros(64, dtype=torch.int64))
+
+
+def test_a_plan_s_experts_may_be_any_whole_number(monkeypatch):
+    """As the other calls that take a plan: a count out of numpy will do."""
+    import numpy as np
+
+    plan = torch.zeros(64, dtype=torch.int32)
+    monkeypatch.setattr(moe, "_flat", lambda t, n, dtype, name: t.data_ptr())
+    for e, _, ints in (moe._plan_on(np.int64(2), plan, 0), moe._plan_on(np.int64(2), plan, plan.get_device())):
+        assert type(e) is int and e == 2 and ints == 64
