@@ -781,7 +781,7 @@ moe_status moe_rms_norm(int64_t rows, int32_t H, float eps, const uint16_t* x, i
         return MOE_ERR_INVALID_ARG;
     if ((!sum && !y && !q) || !q != !q_scale || (y && y == sum)) return MOE_ERR_INVALID_ARG;
     // In place: the same rows, and none of another width.
-    const auto apart = [](const void* p, int64_t p_stride, const void* r, int64_t r_stride) { return p != r || p_stride == r_stride; };
+    const auto apart = [rows](const void* p, int64_t p_stride, const void* r, int64_t r_stride) { return p != r || rows == 1 || p_stride == r_stride; };
     if ((sum && !(apart(sum, sum_stride, x, x_stride) && apart(sum, sum_stride, residual, residual_stride))) ||
         (y && !(apart(y, y_stride, x, x_stride) && apart(y, y_stride, residual, residual_stride))))
         return MOE_ERR_INVALID_ARG;
@@ -824,7 +824,7 @@ moe_status moe_rms_norm_grad(int64_t rows, int32_t H, float eps, const uint16_t*
     if (rows > 0 && (dy == nullptr || h == nullptr || dh == nullptr || !ok_rows(dy, dy_stride, bytes) ||
                      !ok_rows(h, h_stride, bytes) || !ok_rows(dh, dh_stride, bytes) || !ok_rows(dsum, dsum_stride, bytes)))
         return MOE_ERR_INVALID_ARG;
-    if (rows > 0 && (dh == h || (dh == dy && dh_stride != dy_stride) || (dh == dsum && dh_stride != dsum_stride))) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (dh == h || (rows > 1 && ((dh == dy && dh_stride != dy_stride) || (dh == dsum && dh_stride != dsum_stride))))) return MOE_ERR_INVALID_ARG;
     if (!ok_ptr(weight, 1, 16) || !ok_opt(dweight, 16)) return MOE_ERR_INVALID_ARG;
     if (dweight && (!ok_ptr(scratch, 1, 256) || scratch_bytes < moe_rms_norm_grad_scratch_bytes(rows, H))) return MOE_ERR_INVALID_ARG;
     NormGradArgs a{};

@@ -50,3 +50,22 @@ def test_codes_are_the_nearest(H, rows):
     quotient = v / (np.abs(v).max(1, keepdims=True) / 127)
     off = np.abs(_np(q) - quotient)
     assert off.max() <= 0.5 + 127 * 2.0 ** -22 <= 0.5 + 2.0 ** -15
+
+
+def test_one_row_in_place_at_any_stride():
+    """A single row has no next one: its strides mean nothing, in place either."""
+    import torch
+
+    x, w = _bf16((1, 64), 1).cuda(), _bf16((64,), 2).cuda()
+    want, got = torch.empty_like(x), x.clone()
+    moe.moe_rms_norm(x, w, 1e-6, y=want)
+    p = got.data_ptr()
+    assert moe.lib().moe_rms_norm(1, 64, 1e-6, p, 128, None, 0, w.data_ptr(), None, 0, p, 256, None, 0, None, 0, None) == moe.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    grads = [torch.empty_like(x), _bf16((1, 64), 3).cuda()]
+    moe.moe_rms_norm_grad(grads[1], x, w, 1e-6, grads[0])
+    p = grads[1].data_ptr()
+    assert moe.lib().moe_rms_norm_grad(1, 64, 1e-6, p, 128, x.data_ptr(), 128, w.data_ptr(), None, 0, p, 256, None, None, 0, None) == moe.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(grads[1], grads[0])
